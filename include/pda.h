@@ -367,6 +367,215 @@ pda_status pda_decode_host(void* out, const void* q, const void* k_cache, const 
                            int num_kv_heads, int head_size, int block_size, int max_num_blocks_per_seq,
                            long long num_blocks, float scale, float k_scale, float v_scale, cudaStream_t stream);
 
+/*
+ * pda_rope -- rotary positions of query and key heads.
+ *
+ * For pair i < rot_dim/2 of every head of token t, with the angle
+ * positions[t] * inv_freq[i] (radians):
+ *
+ *   (a, b) -> magnitude * (a cos - b sin, a sin + b cos)
+ *
+ * where (a, b) is (x[i], x[i + rot_dim/2]) (interleaved == 0, the "half"
+ * layout) or (x[2i], x[2i+1]) (interleaved != 0). Dims from rot_dim on are
+ * copied unchanged (not scaled by magnitude).
+ *
+ *   q, k         head arrays (see pda_rope_heads); k may be NULL (or have 0
+ *                heads): queries only
+ *   positions    int64 [num_tokens] on the device; any value, negative ones
+ *                turn backwards (so -p undoes p, up to magnitude)
+ *   inv_freq     double [rot_dim/2] in HOST memory, read before the call
+ *                returns: radians per position, each in [-pi, pi). Long
+ *                contexts are reached by scaling these
+ *                (pda_rope_frequencies)
+ *   magnitude    finite factor of the rotated dims
+ *
+ * The angle is reduced modulo a turn in 64-bit integers, so it is as
+ * accurate at position 10^6 as at 1 (about 1e-7 rad); the rotation is fp32
+ * and rounds once, to bf16. out may be in (in place) when the strides agree;
+ * otherwise the two must not overlap. Supported: head_size 128, rot_dim
+ * even, 0..128. Heads on the 16-byte grid (base, strides) with rot_dim a
+ * multiple of 16 run the wide-access kernel; anything else runs a slower one
+ * of 2-byte accesses. Stream-ordered, no workspace, capturable.
+ */
+typedef struct pda_rope_heads {
+  const void* in;               /* bf16: head h of token t at in + t*in_token_stride + h*in_head_stride */
+  void* out;                    /* bf16, likewise with the out strides (ignored where nothing is written) */
+  long long in_token_stride;    /* strides in elements; the head's 128 dims are contiguous */
+  long long in_head_stride;
+  long long out_token_stride;
+  long long out_head_stride;
+  int num_heads;
+} pda_rope_heads;
+
+pda_status pda_rope(const pda_rope_heads* q, const pda_rope_heads* k, const int64_t* positions, int num_tokens,
+                    int head_size, const double* inv_freq, int rot_dim, int interleaved, float magnitude,
+                    cudaStream_t stream);
+
+/*
+ * pda_rope_and_cache -- pda_rope and pda_reshape_and_cache in one pass:
+ * rotates q into q->out, and writes the rotated keys and the values into the
+ * paged cache as e4m3.
+ *
+ * A key is rotated in fp32 and quantised from there, so it rounds once (the
+ * two calls in a row round twice, by way of bf16, and can differ from this
+ * one by an e4m3 step). v->in is not rotated; k->out and v->out are ignored.
+ * slot_mapping, the caches, scales, kv_layout, padding (negative slots write
+ * nothing to the cache; their q is rotated all the same) and slots past the
+ * pool are as for pda_reshape_and_cache, rotary arguments as for pda_rope.
+ * q->out must not overlap k->in or v->in.
+ */
+pda_status pda_rope_and_cache(const pda_rope_heads* q, const pda_rope_heads* k, const pda_rope_heads* v,
+                              const int64_t* positions, const int64_t* slot_mapping, int num_tokens, int head_size,
+                              const double* inv_freq, int rot_dim, int interleaved, float magnitude, void* k_cache,
+                              void* v_cache, int block_size, long long num_blocks, float k_scale, float v_scale,
+                              int kv_layout, cudaStream_t stream);
+
+/*
+ * pda_rope_frequencies -- inv_freq and magnitude for pda_rope (host only,
+ * pure). Plain: inv_freq[i] = base^(-2i/rot_dim), magnitude 1. The scalings
+ * stretch a context by `factor` >= 1:
+ *   PDA_ROPE_LINEAR  every frequency divided by factor
+ *   PDA_ROPE_BASE    base raised to base * factor^(rot_dim/(rot_dim-2)): the
+ *                    fastest pair kept, the slowest divided by factor
+ *   PDA_ROPE_RAMP    pairs that make more than `high` turns over
+ *                    original_length kept, those below `low` divided by
+ *                    factor, a linear ramp over the pair index between (its
+ *                    ends rounded outwards to whole indices); magnitude
+ *                    0.1 ln(factor) + 1 (the YaRN paper, arXiv 2309.00071;
+ *                    it uses low 1, high 32)
+ *   PDA_ROPE_BANDS   the same two bands by turns over original_length, with
+ *                    a blend linear in the turns between (usual: low 1,
+ *                    high 4); magnitude 1
+ * original_length, low and high are read by RAMP and BANDS only (all > 0,
+ * high > low). magnitude may be NULL.
+ */
+typedef enum pda_rope_scaling {
+  PDA_ROPE_PLAIN = 0,
+  PDA_ROPE_LINEAR = 1,
+  PDA_ROPE_BASE = 2,
+  PDA_ROPE_RAMP = 3,
+  PDA_ROPE_BANDS = 4
+} pda_rope_scaling;
+
+pda_status pda_rope_frequencies(double* inv_freq, double* magnitude, int rot_dim, double base, int scaling,
+                                double factor, double original_length, double low, double high);
+
+/*
+ * pda_extend -- causal attention of new tokens over the paged cache: a chunk
+ * of a prompt, drafted tokens to check, or a batch that mixes chunks with
+ * single tokens.
+ *
+ *   out, q        [num_tokens][num_heads][head_size], the new tokens of all
+ *                 sequences packed one after the other
+ *   query_starts  int32 [num_seqs + 1]: sequence s owns rows
+ *                 [query_starts[s], query_starts[s+1]) (nondecreasing, within
+ *                 [0, num_tokens]; a sequence may own none). Rows that
+ *                 belong to no sequence (in front of the first, behind the
+ *                 last) are left as they were
+ *   seq_lens      int32 [num_seqs]: tokens in the cache, the new ones (whose
+ *                 K and V must already be written) included
+ *
+ * With n the rows of sequence s, its row i stands at position
+ * p = seq_lens[s] - n + i and attends to tokens max(0, p - window + 1) .. p
+ * (window > 0) or 0 .. p (window == 0: no limit); a row with p < 0 (fewer
+ * tokens in the cache than rows) gets zeros. Everything else (cache, table,
+ * scales, sinks, out_dtype, output_scale, kv_layout, supported set, value
+ * range, pda_set_block_check) is as for pda_decode / pda_decode_ex; the
+ * first row's position and the window also bound which table entries are
+ * read: those of pages that hold a token some row attends to. A NaN among the
+ * tokens below seq_lens[s] gives undefined output in the sequence's rows.
+ *
+ * Limits: as pda_decode, and num_tokens * num_heads < 2^31.
+ */
+pda_status pda_extend(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                      const int32_t* seq_lens, const int32_t* query_starts, int num_tokens, int num_seqs,
+                      int num_heads, int num_kv_heads, int head_size, int block_size, int max_num_blocks_per_seq,
+                      float scale, float k_scale, float v_scale, int window, int kv_layout, const float* sinks,
+                      int out_dtype, float output_scale, cudaStream_t stream);
+
+/*
+ * Pages. The calls below keep a block table, its lengths and a reference
+ * count per page on the device, so that a captured step can grow, fork and
+ * free sequences without the host.
+ *
+ *   ref_counts    int32 [num_blocks]: table entries that hold the page; a
+ *                 page with count 0 is free. (A caller that pins a page
+ *                 adds 1.)
+ *   block_tables  int32 [num_rows][max_num_blocks_per_seq]
+ *   seq_lens      int32 [num_rows]: row r holds its first
+ *                 ceil(seq_lens[r] / block_size) entries; others are unused
+ *                 and left as they are
+ *
+ * All on the current device, updated in place in stream order. New pages are
+ * the lowest free ids in the order of the requests: the outcome is a function
+ * of the state alone. Requests are lists of row numbers on the device;
+ * negative rows are padding. A request that cannot be served (a row out of
+ * range, a row that an earlier request of the call already named, a length
+ * past the table row, too few free pages: request i is short when requests
+ * 0..i together need more pages than are free) changes nothing and sets bit 128 of the
+ * device status word (pda_query_device_status); table entries outside
+ * [0, num_blocks) are skipped and set bit 64.
+ *
+ * The calls share one workspace per (device, stream), grown like
+ * pda_decode's (PDA_ERR_WORKSPACE when it must grow during capture: size it
+ * with pda_reserve_pages) and freed by pda_release; calls on one stream run
+ * in its order. block_size a multiple of 16 up to 128.
+ */
+typedef struct pda_page_table {
+  int32_t* ref_counts;
+  int32_t* block_tables;
+  int32_t* seq_lens;
+  long long num_blocks;
+  int num_rows;
+  int max_num_blocks_per_seq;
+  int block_size;
+} pda_page_table;
+
+/* One array of pages: a layer's K cache, V cache or scale table. The page of
+ * block b is the bytes_per_block bytes at base + b * bytes_per_block; base
+ * 16-byte aligned, bytes_per_block a multiple of 16. Arrays of one call must
+ * not overlap. */
+typedef struct pda_page_array {
+  void* base;
+  long long bytes_per_block;
+} pda_page_array;
+
+/* pda_copy_pages -- pages src[i] -> dst[i] in every array. src, dst int32
+ * [num_pairs] on the device; pairs with a negative entry, or src == dst, are
+ * skipped, ids past num_blocks are skipped and set bit 64. Targets must be
+ * distinct and no source of the call. arrays is host memory. */
+pda_status pda_copy_pages(const pda_page_array* arrays, int num_arrays, const int32_t* src, const int32_t* dst,
+                          int num_pairs, long long num_blocks, cudaStream_t stream);
+
+/* pda_grow_pages -- row rows[i] takes add[i] >= 0 more tokens: its length
+ * grows, and it gets fresh pages where its last page does not hold them. */
+pda_status pda_grow_pages(const pda_page_table* table, const int32_t* rows, const int32_t* add, int n,
+                          cudaStream_t stream);
+
+/* pda_fork_pages -- row children[i], which must be empty, becomes a copy of
+ * row parents[i]: the parent's full pages are shared (their counts grow),
+ * a last page that is partly filled is copied, in every array, to a fresh
+ * page of the child's own, so that both rows can grow. A row that is a child
+ * of the call cannot be a parent in it. arrays (host memory) may be empty: the
+ * bookkeeping alone. */
+pda_status pda_fork_pages(const pda_page_table* table, const int32_t* parents, const int32_t* children, int n,
+                          const pda_page_array* arrays, int num_arrays, cudaStream_t stream);
+
+/* pda_free_pages -- rows rows[i] become empty and give their pages up (a row
+ * named twice is freed once). */
+pda_status pda_free_pages(const pda_page_table* table, const int32_t* rows, int n, cudaStream_t stream);
+
+/* pda_compact_pages -- moves pages so that the L held pages are ids 0..L-1:
+ * the k-th free id below L takes the k-th held page at or above L, in every
+ * array; counts move along, and every table entry in use follows. */
+pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* arrays, int num_arrays,
+                             cudaStream_t stream);
+
+/* pda_reserve_pages -- size the page calls' workspace of (current device,
+ * stream) for pools and tables up to these sizes and calls of up to
+ * max_requests requests. */
+pda_status pda_reserve_pages(long long num_blocks, int num_rows, int max_requests, cudaStream_t stream);
+
 /* Static text for a status code; never NULL. */
 const char* pda_status_string(int status);
 
@@ -561,8 +770,9 @@ pda_status pda_workspace_info(cudaStream_t stream, long long* bytes, int* retire
  * kernel since the last query finished normally, or a nonzero code when a
  * kernel gave up on a bounded wait, or skipped or redirected an access
  * outside the pool (a cache-write slot past the pool: bit 16; with
- * pda_set_block_check, a block id outside the pool: bit 64); the output of
- * that call is then undefined. Returns PDA_ERR_DEVICE_TIMEOUT when
+ * pda_set_block_check, or in the page calls, a block id outside the pool: bit
+ * 64), or refused a page request (bit 128, which changes nothing); the output
+ * of that call is then undefined but for what the call says of it. Returns PDA_ERR_DEVICE_TIMEOUT when
  * *code != 0. Test / debug call: it blocks.
  */
 pda_status pda_query_device_status(cudaStream_t stream, int* code);

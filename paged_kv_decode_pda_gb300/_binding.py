@@ -25,8 +25,27 @@ PDA_ERR_CUDA = 4
 PDA_ERR_DEVICE_TIMEOUT = 5
 PDA_ERR_NOALLOC_CAPACITY = 6
 
+PDA_ROPE_PLAIN, PDA_ROPE_LINEAR, PDA_ROPE_BASE, PDA_ROPE_RAMP, PDA_ROPE_BANDS = range(5)
+
+
+class _RopeHeads(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("src_token", ctypes.c_longlong),
+                ("src_head", ctypes.c_longlong), ("dst_token", ctypes.c_longlong), ("dst_head", ctypes.c_longlong),
+                ("num_heads", ctypes.c_int)]
+
+
+class _PageTable(ctypes.Structure):
+    _fields_ = [("ref_counts", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("num_blocks", ctypes.c_longlong), ("num_rows", ctypes.c_int), ("max_blocks", ctypes.c_int),
+                ("block_size", ctypes.c_int)]
+
+
+class _PageArray(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("bytes_per_block", ctypes.c_longlong)]
+
+
 # Functions (name -> (restype, argtypes)) the header declares.
-_P, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+_P, _I, _F, _D = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_double
 SIGNATURES = {
     "pda_decode": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _F, _F, _P]),
     "pda_status_string": (ctypes.c_char_p, [_I]),
@@ -54,6 +73,17 @@ SIGNATURES = {
     "pda_decode_ex": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _F, _F, _I, _P, _I, _F, _P]),
     "pda_decode_strided": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I] + [ctypes.c_longlong] * 7
                            + [_F, _F, _F, _P]),
+    "pda_rope": (_I, [_P, _P, _P, _I, _I, _P, _I, _I, _F, _P]),
+    "pda_rope_and_cache": (_I, [_P, _P, _P, _P, _P, _I, _I, _P, _I, _I, _F, _P, _P, _I, ctypes.c_longlong, _F, _F, _I,
+                                _P]),
+    "pda_rope_frequencies": (_I, [_P, _P, _I, _D, _I, _D, _D, _D, _D]),
+    "pda_extend": (_I, [_P] * 7 + [_I] * 7 + [_F, _F, _F, _I, _I, _P, _I, _F, _P]),
+    "pda_copy_pages": (_I, [_P, _I, _P, _P, _I, ctypes.c_longlong, _P]),
+    "pda_grow_pages": (_I, [_P, _P, _P, _I, _P]),
+    "pda_fork_pages": (_I, [_P, _P, _P, _I, _P, _I, _P]),
+    "pda_free_pages": (_I, [_P, _P, _I, _P]),
+    "pda_compact_pages": (_I, [_P, _P, _I, _P]),
+    "pda_reserve_pages": (_I, [ctypes.c_longlong, _I, _I, _P]),
 }
 
 PDA_OUT_BF16 = 0
@@ -462,3 +492,270 @@ def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Ten
                                      slot_mapping.data_ptr(), T, Hk, D, bs, NB, float(k_scale), float(v_scale),
                                      PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE, _stream_ptr(stream)),
            "pda_reshape_and_cache")
+
+
+def _on_device(what: str, tensors) -> None:
+    """Every tensor must lie on the current CUDA device, whose streams the calls use."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t.get_device() != dev:
+            raise PdaError(PDA_ERR_INVALID_ARG, "%s: tensors must be on the current CUDA device" % what)
+
+
+# ---------------------------------------------------------------- rotary
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: int = PDA_ROPE_PLAIN, factor: float = 1.0,
+                     original_length: float = 0.0, low: float | None = None,
+                     high: float | None = None) -> tuple[torch.Tensor, float]:
+    """``pda_rope_frequencies``: (inv_freq float64 ``[rot_dim/2]`` on the CPU, magnitude).
+
+    ``scaling`` is one of ``PDA_ROPE_*``; ``low`` / ``high`` default to 1 and
+    32 (RAMP) or 1 and 4 (BANDS).
+    """
+    if int(rot_dim) <= 0:
+        raise PdaError(PDA_ERR_INVALID_ARG, "rope_frequencies: rot_dim")
+    f = torch.empty(int(rot_dim) // 2, dtype=torch.float64)
+    mag = _D(1.0)
+    lo = 1.0 if low is None else float(low)
+    hi = (4.0 if scaling == PDA_ROPE_BANDS else 32.0) if high is None else float(high)
+    _check(load().pda_rope_frequencies(f.data_ptr(), ctypes.addressof(mag), int(rot_dim), float(base), int(scaling),
+                                       float(factor), float(original_length), lo, hi), "pda_rope_frequencies")
+    return f, mag.value
+
+
+def _rope_inputs(what, q, k, positions, inv_freq):
+    if q.dim() != 3 or q.dtype != torch.bfloat16 or (k is not None and (k.dim() != 3 or k.dtype != torch.bfloat16)):
+        raise PdaError(PDA_ERR_INVALID_ARG, "%s: q and k must be bf16 [T, heads, 128]" % what)
+    T, _, D = q.shape
+    if (k is not None and (k.shape[0] != T or k.shape[2] != D)) or positions.dtype != torch.int64 \
+            or positions.shape != (T,) or not positions.is_contiguous():
+        raise PdaError(PDA_ERR_INVALID_ARG, "%s: shapes (positions: contiguous int64 [T])" % what)
+    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.is_cuda or not inv_freq.is_contiguous()):
+        raise PdaError(PDA_ERR_INVALID_ARG, "%s: inv_freq must be a contiguous CPU float64 [rot_dim/2]" % what)
+    for t in (q, k):
+        if t is not None and t.stride(2) != 1 and t.numel():
+            raise PdaError(PDA_ERR_INVALID_ARG, "%s: the 128 dims of a head must be contiguous" % what)
+
+
+def _rope_heads(src, dst):
+    s0, s1, _ = src.stride()
+    if dst is None:
+        return _RopeHeads(src.data_ptr(), None, s0, s1, 0, 0, src.shape[1])
+    d0, d1, _ = dst.stride()
+    return _RopeHeads(src.data_ptr(), dst.data_ptr(), s0, s1, d0, d1, src.shape[1])
+
+
+def _rope_out(what, x, out):
+    if out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype or (out.stride(2) != 1 and out.numel()):
+        raise PdaError(PDA_ERR_INVALID_ARG, "%s: out must be bf16, shaped like its input, heads contiguous" % what)
+    return out
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor, *,
+         magnitude: float = 1.0, interleaved: bool = False, q_out: torch.Tensor | None = None,
+         k_out: torch.Tensor | None = None, stream=None):
+    """``pda_rope``: rotary positions of q ``[T, H, 128]`` and k ``[T, Hk, 128]`` (bf16; any token and head strides).
+
+    positions ``[T]`` int64; inv_freq float64 ``[rot_dim/2]`` on the CPU
+    (``rope_frequencies``). k may be None. Returns (q_out, k_out), allocated
+    contiguous when not given; ``q_out=q`` rotates in place.
+    """
+    lib = load()
+    _rope_inputs("rope", q, k, positions, inv_freq)
+    qo = _rope_out("rope", q, q_out)
+    ko = _rope_out("rope", k, k_out) if k is not None else None
+    _on_device("rope", (q, positions, qo) if k is None else (q, positions, qo, k, ko))
+    hq = _rope_heads(q, qo)
+    hk = _rope_heads(k, ko) if k is not None else None
+    _check(lib.pda_rope(ctypes.addressof(hq), ctypes.addressof(hk) if hk is not None else None, positions.data_ptr(),
+                        q.shape[0], q.shape[2], inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+                        magnitude, _stream_ptr(stream)), "pda_rope")
+    return qo, ko
+
+
+def rope_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                   slot_mapping: torch.Tensor, inv_freq: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   k_scale: float, v_scale: float, *, magnitude: float = 1.0, interleaved: bool = False,
+                   v_shuffled: bool = False, q_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``pda_rope_and_cache``: rotate q and k, and write the rotated k and v into the paged fp8 cache.
+
+    q ``[T, H, 128]``, k and v ``[T, Hk, 128]`` bf16 with any token and head
+    strides; slot_mapping and the caches as for ``reshape_and_cache``. Returns
+    the rotated queries (``q_out``, allocated contiguous when not given).
+    """
+    lib = load()
+    _rope_inputs("rope_and_cache", q, k, positions, inv_freq)
+    if v.shape != k.shape or v.dtype != torch.bfloat16 or (v.stride(2) != 1 and v.numel()):
+        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: v must be shaped and typed like k")
+    T, Hk, D = k.shape
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
+        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: slot_mapping must be contiguous int64 [T]")
+    for t in (k_cache, v_cache):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_contiguous():
+            raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: caches must be contiguous float8_e4m3fn")
+    if k_cache.dim() != 5:
+        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: shapes")
+    NB, Hk2, D16, bs, sixteen = k_cache.shape
+    v_want = (NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs)
+    if Hk2 != Hk or D16 * 16 != D or sixteen != 16 or tuple(v_cache.shape) != v_want:
+        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: shapes")
+    qo = _rope_out("rope_and_cache", q, q_out)
+    _on_device("rope_and_cache", (q, k, v, positions, slot_mapping, k_cache, v_cache, qo))
+    hq, hk, hv = _rope_heads(q, qo), _rope_heads(k, None), _rope_heads(v, None)
+    _check(lib.pda_rope_and_cache(ctypes.addressof(hq), ctypes.addressof(hk), ctypes.addressof(hv),
+                                  positions.data_ptr(), slot_mapping.data_ptr(), T, D, inv_freq.data_ptr(),
+                                  2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude, k_cache.data_ptr(),
+                                  v_cache.data_ptr(), bs, NB, k_scale, v_scale,
+                                  PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE, _stream_ptr(stream)),
+           "pda_rope_and_cache")
+    return qo
+
+
+# ------------------------------------------------- attention of new tokens
+
+def extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+           seq_lens: torch.Tensor, query_starts: torch.Tensor, scale: float, k_scale: float, v_scale: float, *,
+           window: int = 0, sinks: torch.Tensor | None = None, output_scale: float | None = None,
+           v_shuffled: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``pda_extend``: causal attention of each sequence's new tokens over its pages.
+
+    q ``[T, H, 128]`` bf16, the new tokens packed; query_starts ``[S + 1]``
+    int32; seq_lens ``[S]`` int32 counts the new tokens too. ``window`` > 0
+    limits a token to the last ``window`` tokens. sinks, output_scale and
+    v_shuffled as for ``decode_ex``. Rows of no sequence are left as they are
+    in ``out`` (uninitialised when ``out`` is not given).
+    """
+    lib = load()
+    if q.dim() != 3 or k_cache.dim() != 5 or block_tables.dim() != 2:
+        raise PdaError(PDA_ERR_INVALID_ARG, "extend: tensor ranks")
+    T, H, D = q.shape
+    NB, Hk, D16, bs, sixteen = k_cache.shape
+    S, MB = block_tables.shape
+    i32 = torch.int32
+    if (q.dtype != torch.bfloat16 or block_tables.dtype != i32 or seq_lens.dtype != i32 or query_starts.dtype != i32):
+        raise PdaError(PDA_ERR_INVALID_ARG, "extend: dtypes (q bf16, tables / seq_lens / query_starts int32)")
+    f8 = (torch.float8_e4m3fn, torch.uint8)
+    if k_cache.dtype not in f8 or v_cache.dtype not in f8:
+        raise PdaError(PDA_ERR_INVALID_ARG, "extend: cache dtype must be float8_e4m3fn")
+    v_want = (NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs)
+    if (sixteen != 16 or D16 * 16 != D or tuple(v_cache.shape) != v_want or seq_lens.shape != (S,)
+            or query_starts.shape != (S + 1,)):
+        raise PdaError(PDA_ERR_INVALID_ARG, "extend: shapes")
+    fp8 = output_scale is not None
+    want = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    if out is None:
+        out = torch.empty(q.shape, dtype=want, device=q.device)
+    elif out.shape != q.shape or out.dtype not in ((want, torch.uint8) if fp8 else (want,)):
+        raise PdaError(PDA_ERR_INVALID_ARG, "extend: out")
+    ts = [q, k_cache, v_cache, block_tables, seq_lens, query_starts, out]
+    if sinks is not None:
+        if sinks.dtype != torch.float32 or sinks.shape != (H,):
+            raise PdaError(PDA_ERR_INVALID_ARG, "extend: sinks must be a float32 [num_heads] tensor")
+        ts.append(sinks)
+    for t in ts:
+        if not t.is_contiguous():
+            raise PdaError(PDA_ERR_INVALID_ARG, "extend: tensors must be contiguous")
+    _on_device("extend", ts)
+    _check(lib.pda_extend(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                          block_tables.data_ptr(), seq_lens.data_ptr(), query_starts.data_ptr(), T, S, H, Hk, D, bs,
+                          MB, scale, k_scale, v_scale, int(window),
+                          PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE,
+                          sinks.data_ptr() if sinks is not None else None, PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16,
+                          output_scale if fp8 else 1.0, _stream_ptr(stream)), "pda_extend")
+    return out
+
+
+# ----------------------------------------------------------------- pages
+
+def _page_table(what, ref_counts, block_tables, seq_lens, block_size, *lists):
+    i32 = torch.int32
+    if block_tables.dim() != 2 or ref_counts.dim() != 1 or seq_lens.shape != (block_tables.shape[0],):
+        raise PdaError(PDA_ERR_INVALID_ARG, "%s: shapes (ref_counts [NB], block_tables [S, MB], seq_lens [S])" % what)
+    n = lists[0].shape[0] if lists and lists[0].dim() == 1 else 0
+    for t in lists:
+        if t.shape != (n,):
+            raise PdaError(PDA_ERR_INVALID_ARG, "%s: request lists must be vectors of one length" % what)
+    ts = (ref_counts, block_tables, seq_lens) + lists
+    for t in ts:
+        if t.dtype != i32 or not t.is_contiguous():
+            raise PdaError(PDA_ERR_INVALID_ARG, "%s: tables, counts, lengths and lists must be contiguous int32" % what)
+    _on_device(what, ts)
+    return _PageTable(ref_counts.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), ref_counts.shape[0],
+                      block_tables.shape[0], block_tables.shape[1], int(block_size))
+
+
+def _page_arrays(what, caches, num_blocks=None):
+    """(ctypes array of pda_page_array, count) of tensors ``[num_blocks, ...]``."""
+    arr = (_PageArray * max(1, len(caches)))()
+    dev = torch.cuda.current_device() if len(caches) else 0
+    for a, t in zip(arr, caches):
+        if num_blocks is None:
+            num_blocks = t.shape[0] if t.dim() else 0
+        if t.dim() < 1 or t.shape[0] != num_blocks or not t.is_contiguous() or t.get_device() != dev:
+            raise PdaError(PDA_ERR_INVALID_ARG,
+                           "%s: caches must be contiguous [num_blocks, ...] tensors on the current device" % what)
+        a.base = t.data_ptr()
+        a.bytes_per_block = t.numel() // num_blocks * t.element_size() if num_blocks else 16
+    return arr, (len(caches) if num_blocks else 0)
+
+
+def copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> None:
+    """``pda_copy_pages``: copy pages ``src[i]`` to ``dst[i]`` in every cache tensor ``[num_blocks, ...]``."""
+    lib = load()
+    if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.dim() != 1 or src.shape != dst.shape \
+            or not src.is_contiguous() or not dst.is_contiguous():
+        raise PdaError(PDA_ERR_INVALID_ARG, "copy_pages: src and dst must be contiguous int32 vectors of one length")
+    arr, n = _page_arrays("copy_pages", caches)
+    _on_device("copy_pages", (src, dst))
+    _check(lib.pda_copy_pages(ctypes.addressof(arr), n, src.data_ptr(), dst.data_ptr(), src.shape[0],
+                              caches[0].shape[0] if n else 0, _stream_ptr(stream)), "pda_copy_pages")
+
+
+def grow_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, rows: torch.Tensor,
+               add: torch.Tensor, block_size: int, *, stream=None) -> None:
+    """``pda_grow_pages``: row ``rows[i]`` takes ``add[i]`` more tokens, with fresh pages where it needs them."""
+    lib = load()
+    tab = _page_table("grow_pages", ref_counts, block_tables, seq_lens, block_size, rows, add)
+    _check(lib.pda_grow_pages(ctypes.addressof(tab), rows.data_ptr(), add.data_ptr(), rows.shape[0],
+                              _stream_ptr(stream)), "pda_grow_pages")
+
+
+def fork_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
+               children: torch.Tensor, block_size: int, caches=(), *, stream=None) -> None:
+    """``pda_fork_pages``: empty row ``children[i]`` becomes a copy of row ``parents[i]``.
+
+    Full pages are shared; a partly filled last page is copied to a fresh one
+    in every tensor of ``caches`` (``[num_blocks, ...]`` each).
+    """
+    lib = load()
+    tab = _page_table("fork_pages", ref_counts, block_tables, seq_lens, block_size, parents, children)
+    arr, n = _page_arrays("fork_pages", caches, ref_counts.shape[0])
+    _check(lib.pda_fork_pages(ctypes.addressof(tab), parents.data_ptr(), children.data_ptr(), parents.shape[0],
+                              ctypes.addressof(arr), n, _stream_ptr(stream)), "pda_fork_pages")
+
+
+def free_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, rows: torch.Tensor,
+               block_size: int, *, stream=None) -> None:
+    """``pda_free_pages``: rows become empty and give their pages up."""
+    lib = load()
+    tab = _page_table("free_pages", ref_counts, block_tables, seq_lens, block_size, rows)
+    _check(lib.pda_free_pages(ctypes.addressof(tab), rows.data_ptr(), rows.shape[0], _stream_ptr(stream)),
+           "pda_free_pages")
+
+
+def compact_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, block_size: int,
+                  caches=(), *, stream=None) -> None:
+    """``pda_compact_pages``: move the held pages to the lowest ids, in every cache, count and table entry."""
+    lib = load()
+    tab = _page_table("compact_pages", ref_counts, block_tables, seq_lens, block_size)
+    arr, n = _page_arrays("compact_pages", caches, ref_counts.shape[0])
+    _check(lib.pda_compact_pages(ctypes.addressof(tab), ctypes.addressof(arr), n, _stream_ptr(stream)),
+           "pda_compact_pages")
+
+
+def reserve_pages(num_blocks: int, num_rows: int, max_requests: int, stream=None) -> None:
+    """``pda_reserve_pages``: size the page calls' workspace (before a stream capture)."""
+    _check(load().pda_reserve_pages(int(num_blocks), int(num_rows), int(max_requests), _stream_ptr(stream)),
+           "pda_reserve_pages")

@@ -14,7 +14,10 @@
 #include <vector>
 
 #include "../../include/pda.h"
+#include "pda_extend.cuh"
 #include "pda_kernels.cuh"
+#include "pda_pages.cuh"
+#include "pda_rope.cuh"
 
 namespace {
 
@@ -82,6 +85,8 @@ std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 // Staging buffers of pda_decode_host, per (device, stream); under g_ws_mu.
 std::map<std::pair<int, cudaStream_t>, Workspace> g_stage;
+// Workspaces of the page calls, per (device, stream); under g_ws_mu.
+std::map<std::pair<int, cudaStream_t>, Workspace> g_page_ws;
 
 // Ring geometry for a block size: a stage holds max(16 * consumer warps, bs)
 // tokens of K and V (whole pages); about kRingBytes of stages per CTA.
@@ -675,13 +680,15 @@ WsLayout ws_layout(int num_seqs, int num_heads, const Plan& pl) {
   return w;
 }
 
-// Returns the workspace pointer for (device, stream), growing it with
-// stream-ordered allocation when not capturing.
-pda_status get_workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
+// Returns the workspace pointer of `map` for (device, stream), growing it
+// with stream-ordered allocation when not capturing; the first zero_bytes of
+// a new buffer are zeroed.
+pda_status grow_workspace(std::map<std::pair<int, cudaStream_t>, Workspace>& map, int dev, cudaStream_t stream,
+                          size_t bytes, size_t zero_bytes, void** out) {
   *out = nullptr;
   if (bytes == 0) return PDA_OK;
   std::lock_guard<std::mutex> lk(g_ws_mu);
-  Workspace& ws = g_ws[{dev, stream}];
+  Workspace& ws = map[{dev, stream}];
   if (ws.bytes >= bytes) {
     *out = ws.ptr;
     return PDA_OK;
@@ -693,7 +700,7 @@ pda_status get_workspace(int dev, cudaStream_t stream, size_t bytes, void** out)
   want = (want + 255) & ~(size_t)255;
   void* p = nullptr;
   if (cudaMallocAsync(&p, want, stream) != cudaSuccess) return PDA_ERR_CUDA;
-  if (cudaMemsetAsync(p, 0, kQueueBytes, stream) != cudaSuccess) {
+  if (zero_bytes && cudaMemsetAsync(p, 0, zero_bytes, stream) != cudaSuccess) {
     cudaFreeAsync(p, stream);
     return PDA_ERR_CUDA;
   }
@@ -702,6 +709,11 @@ pda_status get_workspace(int dev, cudaStream_t stream, size_t bytes, void** out)
   ws.bytes = want;
   *out = p;
   return PDA_OK;
+}
+
+// The decode workspace of (device, stream), its queue words zero when new.
+pda_status get_workspace(int dev, cudaStream_t stream, size_t bytes, void** out) {
+  return grow_workspace(g_ws, dev, stream, bytes, kQueueBytes, out);
 }
 
 // Launch the merge kernel for partials of nsplit splits (one warp per row up
@@ -1137,7 +1149,7 @@ pda_status pda_release(void) {
   int prev = 0;
   cudaGetDevice(&prev);
   pda_status st = PDA_OK;
-  for (auto* m : {&g_ws, &g_stage}) {
+  for (auto* m : {&g_ws, &g_stage, &g_page_ws}) {
     for (auto& kv : *m) {
       if (!kv.second.ptr) continue;
       if (cudaSetDevice(kv.first.first) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
@@ -1151,6 +1163,7 @@ pda_status pda_release(void) {
   }
   g_ws.clear();
   g_stage.clear();
+  g_page_ws.clear();
   cudaSetDevice(prev);
   // Per-device set-up (SM counts, occupancy, shared-memory opt-ins, the
   // no-allocation scratch address) is taken again on the next call, so a
@@ -1512,3 +1525,5 @@ extern "C" pda_status pda_decode_noalloc(void* out, const void* q, const void* k
   }
   return PDA_OK;
 }
+
+#include "pda_ops_api.cuh"

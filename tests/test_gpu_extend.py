@@ -1,0 +1,209 @@
+"""Attention of new tokens over the paged cache (pda_extend) against the 64-bit reference."""
+
+import pytest
+import torch
+
+import paged_kv_decode_pda_gb300 as pda
+from tests import ops_util as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def run(c, **kw):
+    out = pda.extend(**c.to(DEV), **kw)
+    assert pda.query_device_status() == 0
+    return out
+
+
+def check(c, label="", **kw):
+    ref, spread = c.exact(window=kw.get("window", 0), sinks=kw.get("sinks"))
+    dev = {k: (v.to(DEV) if isinstance(v, torch.Tensor) else v) for k, v in kw.items()}
+    got = run(c, **dev)
+    O.check_rows(got, ref, spread, label)
+    return got, ref
+
+
+@pytest.mark.parametrize("seqs", [
+    [(1, 1)], [(1, 17)], [(2, 2)], [(16, 512)], [(5, 5), (1, 300), (0, 40), (0, 0), (33, 64)],
+    [(130, 131), (64, 1000)], [(3, 129), (127, 127), (128, 128), (129, 129)], [(1, 128 * k + d) for k in (1, 2) for d in (-1, 0, 1)],
+    [(300, 700), (1, 2000), (257, 257)]])
+@pytest.mark.parametrize("H,Hk", [(4, 1), (8, 8), (16, 2)])
+def test_lengths(seqs, H, Hk):
+    check(O.Chunk(seqs, H, Hk, seed=len(seqs)))
+
+
+@pytest.mark.parametrize("g", [1, 2, 3, 4, 5, 6, 7, 8])
+def test_groups(g):
+    check(O.Chunk([(45, 200), (7, 90), (1, 33)], 2 * g, 2, seed=g))
+
+
+@pytest.mark.parametrize("shuffled", [False, True])
+@pytest.mark.parametrize("bs", [16, 32, 48, 64, 80, 96, 112, 128])
+def test_block_sizes_and_layouts(bs, shuffled):
+    check(O.Chunk([(70, 333), (2, bs + 1), (9, 9), (140, 140)], 8, 2, bs, seed=bs, shuffled=shuffled))
+
+
+@pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 100, 128, 300, 5000])
+def test_windows(window):
+    check(O.Chunk([(200, 450), (1, 600), (4, 4), (130, 1000)], 8, 2, 32, seed=window), window=window)
+
+
+@pytest.mark.parametrize("seqs", [[(1, 777)], [(90, 400), (1, 5)]])
+@pytest.mark.parametrize("value", [-40.0, 0.0, 3.0, 60.0])
+def test_sinks(seqs, value):
+    sinks = torch.linspace(value - 2, value + 2, 8)
+    check(O.Chunk(seqs, 8, 2, seed=1), sinks=sinks)
+
+
+def test_more_rows_than_tokens_gives_zeros():
+    c = O.Chunk([(6, 4), (5, 0), (200, 150), (1, 1)], 8, 2, seed=4)
+    for sinks in (None, torch.zeros(8)):
+        got, ref = check(c, sinks=sinks)
+        for s, (n, L) in enumerate(c.seqs):
+            none = max(0, n - L)
+            assert (got[c.starts[s]:c.starts[s] + none] == 0).all()
+
+
+def test_rows_of_no_sequence_stay_as_they_were():
+    c = O.Chunk([(3, 70), (0, 8), (140, 150)], 8, 2, seed=6, pad_front=5, pad_back=131)
+    mark = torch.full((c.T, 8, 128), -3.0, dtype=torch.bfloat16, device=DEV)
+    run(c, out=mark)
+    assert (mark[:5] == -3).all() and (mark[c.starts[-1]:] == -3).all()
+    ref, spread = c.exact()
+    O.check_rows(mark, ref, spread)
+
+
+def test_e4m3_output():
+    c = O.Chunk([(20, 300), (1, 64)], 8, 2, seed=8)
+    ref, spread = c.exact()
+    scale = 0.01
+    got = run(c, output_scale=scale)
+    assert got.dtype == torch.float8_e4m3fn
+    want = (ref / scale).clamp(-448, 448)
+    # half an e4m3 step (2^-4 relative, 2^-10 below the normal range) and the kernel's own error
+    bound = torch.maximum(2.0 ** -4 * want.abs(), torch.tensor(2.0 ** -10, dtype=torch.float64)) + (1 + 2.0 ** -4) * O.WEIGHT_ERR * spread / scale
+    assert ((got.cpu().double() - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("power", [-100, -20, 40, 100])
+def test_query_rows_of_any_magnitude(power):
+    c = O.Chunk([(40, 200), (1, 150)], 8, 2, seed=12)
+    c.q = (c.q.float() * 2.0 ** power).to(torch.bfloat16)
+    c.scale *= 2.0 ** -power
+    check(c)
+
+
+def test_a_dominant_token_leaves_room_for_the_rest():
+    # one key far above all the others, many values of small weight behind it
+    c = O.Chunk([(2, 1500)], 4, 1, seed=13)
+    b = int(c.tables[0, 0])
+    c.q = torch.full_like(c.q, 0.5)
+    c.k_cache.view(torch.uint8)[b, :, :, 0, :] = torch.tensor(150.0).to(O.FP8).view(torch.uint8)
+    check(c)
+
+
+def test_pages_no_row_attends_to_are_not_read():
+    # entries in front of the window name a block of NaN codes
+    c = O.Chunk([(10, 1000)], 4, 1, seed=14)
+    w = 60
+    lo = max(0, 990 - w + 1) // c.bs
+    ref, spread = c.exact(window=w)
+    free = [b for b in range(c.NB) if b not in c.tables[0, :-(-1000 // c.bs)].tolist()][0]
+    c.k_cache.view(torch.uint8)[free] = 0x7F
+    c.v_cache.view(torch.uint8)[free] = 0xFF
+    c.tables[0, :lo] = free
+    O.check_rows(run(c, window=w), ref, spread)
+
+
+def test_a_long_context_split_over_the_gpu():
+    c = O.Chunk([(2, 20000)], 8, 1, seed=15)
+    check(c)
+    c = O.Chunk([(3, 9000), (1, 17)], 8, 2, seed=16)
+    check(c)
+    check(c, sinks=torch.linspace(-3, 6, 8))
+    check(c, window=5000)
+
+
+def test_a_cache_past_2_31_bytes():
+    bs, Hk, NB = 16, 8, 140_000
+    kc = torch.zeros(NB, Hk, 8, bs, 16, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    vc = torch.zeros(NB, Hk, 128, bs, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+    assert kc.numel() > 1 << 31
+    c = O.Chunk([(5, 100)], 16, Hk, bs, seed=17, garbage=False)
+    n = -(-100 // bs)
+    far = torch.arange(NB - n, NB)
+    kc.view(torch.uint8)[far] = c.k_cache.view(torch.uint8)[c.tables[0, :n].long()].to(DEV)
+    vc.view(torch.uint8)[far] = c.v_cache.view(torch.uint8)[c.tables[0, :n].long()].to(DEV)
+    d = c.to(DEV)
+    d.update(k_cache=kc, v_cache=vc)
+    d["block_tables"][0, :n] = far.to(torch.int32)
+    ref, spread = c.exact()
+    O.check_rows(pda.extend(**d), ref, spread)
+
+
+def test_single_tokens_agree_with_decode():
+    c = O.Chunk([(1, n) for n in (1, 16, 100, 1000, 333)], 16, 2, seed=18)
+    d = c.to(DEV)
+    a = pda.extend(**d)
+    b = pda.decode(d["q"], d["k_cache"], d["v_cache"], d["block_tables"], d["seq_lens"], c.scale, c.ks, c.vs)
+    ref, spread = c.exact()
+    O.check_rows(a, ref, spread)
+    assert ((a.double() - b.double()).abs().cpu() <= 2.0 ** -7 * ref.abs() + 2 * O.WEIGHT_ERR * spread).all()
+
+
+def test_the_same_call_gives_the_same_bits():
+    c = O.Chunk([(200, 900), (1, 3000), (7, 50)], 8, 2, seed=19)
+    d = c.to(DEV)
+    a = pda.extend(**d)
+    for _ in range(3):
+        assert torch.equal(pda.extend(**d), a)
+
+
+def test_two_batches_in_turn_on_one_stream():
+    big, small = O.Chunk([(2, 9000), (2, 8000)], 8, 2, seed=20), O.Chunk([(3, 4000)], 8, 2, seed=21)
+    outs = [(run(c), c) for c in (big, small, big)]
+    for got, c in outs:
+        ref, spread = c.exact()
+        O.check_rows(got, ref, spread)
+
+
+@pytest.mark.parametrize("seqs", [[(40, 100), (1, 30)], [(2, 9000)]])
+def test_captured_and_on_another_stream(seqs):
+    c = O.Chunk(seqs, 8, 2, seed=22)
+    d = c.to(DEV)
+    ref, spread = c.exact()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(d["q"])
+    with torch.cuda.stream(s):
+        pda.extend(**d, out=out)                       # sizes this stream's workspace
+        gr = torch.cuda.CUDAGraph()
+        s.synchronize()
+        out.zero_()
+        with torch.cuda.graph(gr, stream=s):
+            pda.extend(**d, out=out)
+        gr.replay()
+        gr.replay()
+    s.synchronize()
+    O.check_rows(out, ref, spread)
+    assert pda.query_device_status() == 0
+
+
+def test_block_check_keeps_reads_in_the_pool():
+    c = O.Chunk([(4, 100)], 4, 1, seed=23)
+    c.tables[0, 1] = c.NB + 5
+    pda.set_block_check(c.NB)
+    try:
+        d = c.to(DEV)
+        pda.extend(**d)
+        assert pda.query_device_status() == 64
+    finally:
+        pda.set_block_check(0)
+
+
+def test_nothing_to_do():
+    c = O.Chunk([(0, 5), (0, 0)], 4, 1, seed=24, pad_back=3)
+    mark = torch.full((c.T, 4, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    run(c, out=mark)
+    assert (mark == 7).all()

@@ -1,0 +1,211 @@
+"""Page bookkeeping on the device against a plain Python reference: every table, count, length and page byte."""
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_decode_pda_gb300 as pda
+from tests import ops_util as O
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+class Both:
+    """The reference pool and the device's, moved in step."""
+
+    def __init__(self, NB, rows, cols, bs=16, arrays=((64,), (48,)), seed=0):
+        self.ref = O.Pool(NB, rows, cols, bs)
+        self.bs = bs
+        self.dev = self.ref.tensors(DEV)
+        rng = np.random.default_rng(seed)
+        self.pages = [rng.integers(0, 256, (NB,) + tuple(s), dtype=np.uint8) for s in arrays]
+        self.caches = [torch.from_numpy(p.copy()).to(DEV) for p in self.pages]
+
+    def i32(self, x):
+        return torch.tensor(x, dtype=torch.int32, device=DEV).view(-1)
+
+    def step(self, what, *lists, copies=True, status=None):
+        getattr(self.ref, what)(*lists)
+        fn = getattr(pda, what + "_pages")
+        args = [self.i32(x) for x in lists]
+        if what in ("fork", "compact"):
+            fn(*self.dev, *args, self.bs, self.caches if copies else ())
+            if copies:
+                for p in self.pages:
+                    self.ref.apply_moves(p)
+        else:
+            fn(*self.dev, *args, self.bs)
+        want = (128 if self.ref.refused else 0) if status is None else status
+        assert pda.query_device_status() == want, what
+        self.same(what)
+
+    def same(self, what=""):
+        refs, tables, lens = (x.cpu() for x in self.dev)
+        assert refs.tolist() == self.ref.refs, what
+        assert lens.tolist() == self.ref.lens, what
+        assert tables.tolist() == self.ref.tables, what
+        for p, c in zip(self.pages, self.caches):
+            assert np.array_equal(c.cpu().numpy(), p), what
+
+
+def test_a_small_walk():
+    b = Both(40, 6, 8)
+    b.step("grow", [0, 1], [33, 16])
+    b.step("fork", [0, 1], [2, 3])
+    b.step("grow", [2, 0, 3], [20, 0, 1])
+    b.step("free", [0])
+    b.step("grow", [4], [100])
+    b.step("compact")
+    b.step("free", [1, 2, 3, 4])
+    assert b.ref.refs == [0] * 40
+
+
+@pytest.mark.parametrize("seed,NB,rows,cols,bs,arrays", [
+    (0, 60, 10, 12, 16, ((64,),)), (1, 300, 40, 20, 32, ((8, 128, 32), (8, 32, 4))),
+    (2, 9000, 300, 70, 16, ((16,), (32,))), (3, 20000, 64, 400, 48, ()), (4, 33, 33, 3, 128, ((20000,),)),
+    (5, 5000, 1500, 5, 64, ((160,),) * 3)])
+def test_random_walks(seed, NB, rows, cols, bs, arrays):
+    rng = random.Random(seed)
+    b = Both(NB, rows, cols, bs, arrays, seed)
+    for step in range(24):
+        used = [r for r in range(rows) if b.ref.lens[r]]
+        empty = [r for r in range(rows) if not b.ref.lens[r]]
+        what = rng.choice(["grow", "grow", "grow", "fork", "fork", "free", "compact"])
+        if what == "grow":
+            pick = rng.sample(range(rows), rng.randint(1, rows)) + [-1] * rng.randrange(3)
+            most = max(2, int(2.2 * NB * bs / len(pick) / 3))
+            b.step("grow", pick, [rng.randrange(min(most, cols * bs)) for _ in pick])
+        elif what == "fork" and used and empty:
+            kids = rng.sample(empty, rng.randint(1, len(empty)))
+            b.step("fork", [rng.choice(used + [-1] if rng.random() < 0.2 else used) for _ in kids], kids)
+        elif what == "free" and used:
+            b.step("free", rng.sample(used, rng.randint(1, len(used))) + [-1])
+        elif what == "compact":
+            b.step("compact")
+
+
+def test_more_requests_than_a_block_of_threads():
+    b = Both(5000, 3000, 4, arrays=())
+    b.step("grow", list(range(2500)), [1 + i % 40 for i in range(2500)])
+    b.step("free", list(range(0, 2500, 3)))
+    b.step("fork", list(range(1, 400, 3)) * 3, list(range(2500, 2899)))
+
+
+def test_refusals_leave_the_state_alone():
+    b = Both(4, 5, 4)
+    b.step("grow", [0, 0, 9, 1, 2], [20, 5, 1, 70, -1])        # a repeat, no such row, past the row, less than nothing
+    assert b.ref.refused == 4 and b.ref.lens == [20, 0, 0, 0, 0]
+    b.step("grow", [1, 2, 3], [20, 30, 0])                      # the second finds no page; nothing is needed for the third
+    assert b.ref.lens == [20, 20, 0, 0, 0]
+    b.step("fork", [0, 1], [2, 3])                              # no page left for a partly filled one
+    assert b.ref.refused == 2
+    b.step("free", [1, 1, 77, -3])                              # twice: freed once; 77: no such row
+    b.step("fork", [0, 0, 0, 2, 4], [1, 1, 0, 3, 4])            # a repeat, a child that holds tokens and is a parent, ...
+    b.step("fork", [0], [9])
+
+
+def test_ids_outside_the_pool_are_flagged_and_skipped():
+    b = Both(8, 3, 4)
+    b.step("grow", [0], [40])
+    b.dev[1][0, 1] = 99
+    pda.free_pages(*b.dev, b.i32([0]), 16)
+    assert pda.query_device_status() == 64
+    assert b.dev[0].tolist() == [0, 1, 0, 0, 0, 0, 0, 0] and b.dev[2].tolist() == [0, 0, 0]
+
+
+def test_freeing_a_free_page_is_flagged():
+    b = Both(8, 2, 4)
+    b.step("grow", [0], [20])
+    b.dev[0][1] = 0
+    pda.free_pages(*b.dev, b.i32([0]), 16)
+    assert pda.query_device_status() == 128
+    assert b.dev[0].tolist() == [0] * 8
+
+
+def test_copy_pages():
+    NB = 50
+    rng = np.random.default_rng(0)
+    pages = [rng.integers(0, 256, (NB,) + s, dtype=np.uint8) for s in ((16,), (8, 2048), (16400,), (2, 3, 16))]
+    caches = [torch.from_numpy(p.copy()).to(DEV) for p in pages]
+    src, dst = [3, -1, 7, 3, 9, 60, 2, 5], [40, 41, -2, 42, 9, 43, 99, 0]
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    pda.copy_pages(caches, t(src), t(dst))
+    assert pda.query_device_status() == 64
+    for p, c in zip(pages, caches):
+        for s, d in ((3, 40), (3, 42), (5, 0)):
+            p[d] = p[s]
+        assert np.array_equal(c.cpu().numpy(), p)
+
+
+def test_more_arrays_than_a_launch_takes():
+    b = Both(30, 4, 6, arrays=((32,),) * 131)
+    b.step("grow", [0, 1], [40, 50])
+    b.step("free", [0])
+    b.step("fork", [1], [2])
+    b.step("compact")
+
+
+def test_a_pool_past_2_31_bytes():
+    NB = 1 << 16
+    cache = torch.zeros(NB, 40000, dtype=torch.uint8, device=DEV)
+    assert cache.numel() > 1 << 31
+    cache[NB - 1] = 7
+    cache[NB - 2, ::3] = 9
+    last = cache[NB - 2].clone()
+    t = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    pda.copy_pages([cache], t([NB - 1, NB - 2]), t([1, NB - 3]))
+    assert (cache[1] == 7).all() and torch.equal(cache[NB - 3], last) and (cache[0] == 0).all()
+
+
+def test_captured_with_a_reserved_workspace():
+    b = Both(64, 6, 8)
+    b.step("grow", [0, 1], [20, 35])
+    parents, kids, rows, add = b.i32([0, 1]), b.i32([2, 3]), b.i32([0, 1, 2, 3]), b.i32([3, 14, 1, 30])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    pda.reserve_pages(64, 6, 4, stream=s)
+    s.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        pda.fork_pages(*b.dev, parents, kids, 16, b.caches)
+        pda.grow_pages(*b.dev, rows, add, 16)
+        pda.free_pages(*b.dev, kids, 16)
+        pda.compact_pages(*b.dev, 16, b.caches)
+    for _ in range(3):
+        gr.replay()
+        torch.cuda.synchronize()
+        for what, lists in (("fork", ([0, 1], [2, 3])), ("grow", ([0, 1, 2, 3], [3, 14, 1, 30])), ("free", ([2, 3],)),
+                            ("compact", ())):
+            getattr(b.ref, what)(*lists)
+            if what in ("fork", "compact"):
+                for p in b.pages:
+                    b.ref.apply_moves(p)
+        b.same()
+    assert pda.query_device_status() == 0
+
+
+def test_a_capture_that_would_grow_the_workspace_is_refused():
+    b = Both(64, 6, 8)
+    s = torch.cuda.Stream()
+    rows = b.i32([0])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        with pytest.raises(pda.PdaError) as e:
+            pda.grow_pages(*b.dev, rows, rows, 16)
+        assert e.value.status == pda.PDA_ERR_WORKSPACE
+        b.dev[2].add_(0)
+
+
+def test_empty_pools_and_lists():
+    z = torch.zeros(0, dtype=torch.int32, device=DEV)
+    b = Both(5, 2, 3)
+    pda.grow_pages(*b.dev, z, z, 16)
+    pda.fork_pages(*b.dev, z, z, 16, b.caches)
+    pda.free_pages(*b.dev, z, 16)
+    pda.copy_pages(b.caches, z, z)
+    b.step("compact")
+    pda.compact_pages(z, torch.zeros(0, 4, dtype=torch.int32, device=DEV), z, 16)
+    b.step("grow", [0, 1], [0, 0])
