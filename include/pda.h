@@ -485,13 +485,23 @@ pda_status pda_rope_frequencies(double* inv_freq, double* magnitude, int rot_dim
  * read: those of pages that hold a token some row attends to. A NaN among the
  * tokens below seq_lens[s] gives undefined output in the sequence's rows.
  *
- * Limits: as pda_decode, and num_tokens * num_heads < 2^31.
+ * Limits: as pda_decode, and num_tokens * num_heads < 2^31. A call whose
+ * tiles do not fill the GPU splits the KV range and needs a workspace per
+ * (device, stream) for the partials, grown as pda_decode's is; captured
+ * without one (pda_reserve_extend, or an earlier call of the sizes on that
+ * stream) it runs unsplit. The result may differ in the last bits with the
+ * split; for one split count it is bitwise reproducible.
  */
 pda_status pda_extend(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                       const int32_t* seq_lens, const int32_t* query_starts, int num_tokens, int num_seqs,
                       int num_heads, int num_kv_heads, int head_size, int block_size, int max_num_blocks_per_seq,
                       float scale, float k_scale, float v_scale, int window, int kv_layout, const float* sinks,
                       int out_dtype, float output_scale, cudaStream_t stream);
+
+/* pda_reserve_extend -- size the workspace of (current device, stream) for
+ * pda_extend calls of these sizes. It is the page calls' workspace too. */
+pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                              int max_num_blocks_per_seq, int block_size, cudaStream_t stream);
 
 /*
  * Pages. The calls below keep a block table, its lengths and a reference

@@ -78,6 +78,7 @@ SIGNATURES = {
                                 _P]),
     "pda_rope_frequencies": (_I, [_P, _P, _I, _D, _I, _D, _D, _D, _D]),
     "pda_extend": (_I, [_P] * 7 + [_I] * 7 + [_F, _F, _F, _I, _I, _P, _I, _F, _P]),
+    "pda_reserve_extend": (_I, [_I, _I, _I, _I, _I, _I, _P]),
     "pda_copy_pages": (_I, [_P, _I, _P, _P, _I, ctypes.c_longlong, _P]),
     "pda_grow_pages": (_I, [_P, _P, _P, _I, _P]),
     "pda_fork_pages": (_I, [_P, _P, _P, _I, _P, _I, _P]),
@@ -665,6 +666,13 @@ def extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
                           sinks.data_ptr() if sinks is not None else None, PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16,
                           output_scale if fp8 else 1.0, _stream_ptr(stream)), "pda_extend")
     return out
+
+
+def reserve_extend(num_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq, block_size,
+                   stream=None) -> None:
+    """``pda_reserve_extend``: size the workspace for ``extend`` calls of these sizes (before a stream capture)."""
+    _check(load().pda_reserve_extend(num_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq,
+                                     block_size, _stream_ptr(stream)), "pda_reserve_extend")
 
 
 # ----------------------------------------------------------------- pages

@@ -62,6 +62,8 @@ struct DeviceInfo {
   int cluster_launch = -1;                // cudaDevAttrClusterLaunch (-1: not read yet)
   int ctas_per_sm[kNumKinds][9] = {{0}};  // [instance][bs/16 (1..8)]
   bool smem_attr_set = false;
+  bool extend_set = false;                // pda_extend_kernel checked and opted in
+  int extend_sms = 0;
   // co-resident clusters of n split CTAs: [instance][bs/16][n] (-1: not asked yet)
   int max_clusters[kNumKinds][9][17];
   DeviceInfo() {
@@ -85,8 +87,9 @@ std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 // Staging buffers of pda_decode_host, per (device, stream); under g_ws_mu.
 std::map<std::pair<int, cudaStream_t>, Workspace> g_stage;
-// Workspaces of the page calls, per (device, stream); under g_ws_mu.
-std::map<std::pair<int, cudaStream_t>, Workspace> g_page_ws;
+// Workspaces of pda_extend's split partials and of the page calls, per
+// (device, stream); under g_ws_mu.
+std::map<std::pair<int, cudaStream_t>, Workspace> g_ops_ws;
 
 // Ring geometry for a block size: a stage holds max(16 * consumer warps, bs)
 // tokens of K and V (whole pages); about kRingBytes of stages per CTA.
@@ -1149,7 +1152,7 @@ pda_status pda_release(void) {
   int prev = 0;
   cudaGetDevice(&prev);
   pda_status st = PDA_OK;
-  for (auto* m : {&g_ws, &g_stage, &g_page_ws}) {
+  for (auto* m : {&g_ws, &g_stage, &g_ops_ws}) {
     for (auto& kv : *m) {
       if (!kv.second.ptr) continue;
       if (cudaSetDevice(kv.first.first) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
@@ -1163,7 +1166,7 @@ pda_status pda_release(void) {
   }
   g_ws.clear();
   g_stage.clear();
-  g_page_ws.clear();
+  g_ops_ws.clear();
   cudaSetDevice(prev);
   // Per-device set-up (SM counts, occupancy, shared-memory opt-ins, the
   // no-allocation scratch address) is taken again on the next call, so a

@@ -1,5 +1,36 @@
 // Attention of a chunk of new tokens per sequence over the paged e4m3 cache
-// (pda_extend): one warp per (new token, query head).
+// (pda_extend), on the fifth-generation tensor cores.
+//
+// One CTA holds up to 256 query rows of one (sequence, kv head): the g heads
+// of a group share K and V, so row r is token r / g, head r % g of the tile.
+// With S = Q K^T scaled to log2 units, each row keeps a reference m and
+//   P = 2^(S - m + 7),  l = sum P,  O += P V,   out = v_scale O / l.
+// The reference follows the running maximum lazily: while the maximum grows
+// by at most 2^8 over it, O stays as it is and P grows (P <= 2^15 fits f16;
+// the offset of 7 leaves f16 31 binades below the maximum for small weights);
+// only a larger step rescales O and l. S, l, O and the references are fp32;
+// P rounds once to f16 (2^-11 relative), Q is exact in f16 after a shift of
+// its row by a power of two, K and V are exact in f16.
+//
+// Roles (20 warps):
+//   warps 0-3, 4-7    softmax of rows 0..127 (block A) and 128..255 (block B):
+//                     thread = row, a row of S read from tensor memory into
+//                     registers, P written back over it
+//   warps 8-11        K: 16-byte loads through the block table, e4m3 -> f16 in
+//                     registers, stores in the matrix units' layout
+//   warps 12-15       V likewise
+//   warp 16           one thread issues the products (17-19 idle: registers are
+//                     traded by groups of four warps)
+// Tensor memory (512 columns): S_A, S_B (128 each; P takes the last 64 of
+// its block's), O_A, O_B. Shared memory: Q 64 KiB, two K stages and three V
+// stages of 128 tokens, 32 KiB each, in the layout without swizzle: 8 x 16
+// byte core matrices, 16-byte column c of row r at c * 2048 + r * 16, which
+// lanes with consecutive rows store without bank conflicts.
+// While block A is in its softmax the tensor core works for block B.
+//
+// With at most 128 rows in the tile (a few tokens per sequence) both blocks
+// take the same rows, A the even and B the odd tiles of 128 tokens, and their
+// (O, m, l) are joined at the end, so the two softmax groups still overlap.
 #pragma once
 
 #include "pda_kernels.cuh"
@@ -22,16 +53,54 @@ struct ExtendParams {
   int block_size;
   int max_blocks;
   int window;
-  float logit_scale_log2;       // scale * k_scale * log2(e)
+  float logit_scale_log2;       // |scale * k_scale| * log2(e)
+  int negate;                   // scale * k_scale < 0: the queries are negated
   float v_scale;
   const float* sinks;
   int out_fp8;
   float out_scale;
   int v_shuffled;
   uint32_t block_limit;
+  int tile_tokens;              // tokens of a full tile: 256 / g
+  int tiles;                    // tile slots (grid x)
+  int nsplit;                   // KV splits (grid z)
+  float* part_o;                // [T][H][nsplit][128]   (nsplit > 1)
+  float* part_ml;               // [T][H][nsplit][2]: reference (log2 units), l
 };
 
-constexpr int kExtendWarps = 4;
+constexpr int kExtRows = 128;                         // rows of a block
+constexpr int kExtTile = 128;                         // tokens of a KV tile
+constexpr int kExtThreads = 20 * 32;
+// Registers per thread: at launch, then after the warps have traded them.
+constexpr int kExtLaunchRegs = 96;
+constexpr int kExtSoftmaxRegs = 144;
+constexpr int kExtConvertRegs = 72;
+constexpr int kExtIssueRegs = 48;
+static_assert(256 * kExtSoftmaxRegs + 256 * kExtConvertRegs + 128 * kExtIssueRegs <= kExtThreads * kExtLaunchRegs,
+              "the warps' registers come out of the CTA's own");
+constexpr int kExtKStages = 2;
+constexpr int kExtVStages = 3;
+constexpr uint32_t kExtOperand = 128u * 128u * 2u;    // one f16 operand tile: 32 KiB
+constexpr uint32_t kExtColumn = 128u * 16u;           // one 16-byte column of it
+constexpr uint32_t kExtQOff = 0;
+constexpr uint32_t kExtKOff = 2 * kExtOperand;
+constexpr uint32_t kExtVOff = kExtKOff + kExtKStages * kExtOperand;
+constexpr uint32_t kExtBarOff = kExtVOff + kExtVStages * kExtOperand;
+enum : int {                                          // barriers (8 bytes each)
+  kBarQ = 0,                                          // queries stored (8 warps)
+  kBarKFull = 1,
+  kBarKFree = kBarKFull + kExtKStages,
+  kBarVFull = kBarKFree + kExtKStages,
+  kBarVFree = kBarVFull + kExtVStages,
+  kBarS = kBarVFree + kExtVStages,                    // S of block A, B ready
+  kBarP = kBarS + 2,                                  // P of block A, B ready (4 warps)
+  kBarO = kBarP + 2,                                  // O of block A, B final
+  kBarCount = kBarO + 2
+};
+constexpr uint32_t kExtSmem = kExtBarOff + kBarCount * 8 + 16;
+static_assert(kExtSmem <= 232448, "shared memory of one CTA");
+constexpr float kExtOffset = 7.f;                     // P = 2^(S - m + kExtOffset)
+constexpr float kExtSlack = 8.f;                      // growth of the maximum that leaves m as it is
 
 // First s with query_starts[s + 1] > row, or num_seqs.
 __device__ __forceinline__ int sequence_of_row(const int32_t* starts, int num_seqs, int row) {
@@ -46,72 +115,617 @@ __device__ __forceinline__ int sequence_of_row(const int32_t* starts, int num_se
   return lo;
 }
 
-__global__ void __launch_bounds__(kExtendWarps * 32) pda_extend_row_kernel(const ExtendParams p) {
-  __shared__ float qs[kExtendWarps][kHeadDim];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * kExtendWarps + warp;
-  if (item >= (long long)p.num_tokens * p.num_heads) return;
-  const int row = (int)(item / p.num_heads), h = (int)(item % p.num_heads);
-  const int s = sequence_of_row(p.query_starts, p.num_seqs, row);
-  if (s >= p.num_seqs || row < __ldg(p.query_starts + s)) return;
-  const int start = __ldg(p.query_starts + s), n = __ldg(p.query_starts + s + 1) - start;
-  const int bs = p.block_size;
-  const int len = (int)max(0ll, min((long long)__ldg(p.seq_lens + s), (long long)p.max_blocks * bs));
-  const int pos = len - n + row - start;
-  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  const size_t o0 = ((size_t)row * p.num_heads + h) * kHeadDim;
-  for (int d = lane; d < kHeadDim; d += 32) qs[warp][d] = __bfloat162float(p.q[o0 + d]);
-  __syncwarp();
-  const int kvh = h / p.gqa;
-  const size_t page_bytes = (size_t)kHeadDim * bs;
-  float m = -INFINITY, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int t0 = lo & ~31; t0 <= pos; t0 += 32) {
-    const int t = t0 + lane;
-    const bool seen = t >= lo && t <= pos;
-    float z = -INFINITY;
-    size_t page = 0;
-    if (seen) {
-      const int b = checked_block(__ldg(p.block_tables + (size_t)s * p.max_blocks + t / bs), p.block_limit);
-      page = ((size_t)b * p.num_kv_heads + kvh) * page_bytes;
-      float a = 0.f;
-      for (int c = 0; c < kChunks; ++c) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p.k_cache + page + ((size_t)c * bs + t % bs) * 16);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t e = e4m3x2_lo_to_f16x2(w[i]), f = e4m3x2_hi_to_f16x2(w[i]);
-          const float* qq = &qs[warp][16 * c + 4 * i];
-          a += qq[0] * f16lo_f32(e) + qq[1] * f16hi_f32(e) + qq[2] * f16lo_f32(f) + qq[3] * f16hi_f32(f);
-        }
-      }
-      z = a * p.logit_scale_log2;
-    }
-    float mx = z;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float mn = fmaxf(m, mx);
-    const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
-    const float pr = seen ? fast_exp2(z - mn) : 0.f;
-    float sum = pr;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    l = l * f + sum;
-    m = mn;
-    acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-    for (int i = 0; i < 32; ++i) {
-      const int ti = t0 + i;
-      if (ti < lo || ti > pos) continue;
-      const float pi = __shfl_sync(0xffffffffu, pr, i);
-      const size_t pg = __shfl_sync(0xffffffffu, (unsigned long long)page, i);
-      const int o = ti % bs;
-      float vv[4];
-      for (int u = 0; u < 4; ++u) {
-        const int d = 4 * lane + u;
-        const size_t at = p.v_shuffled ? ((size_t)(o / 16) * kHeadDim + d) * 16 + o % 16 : (size_t)d * bs + o;
-        vv[u] = f16lo_f32(e4m3x2_lo_to_f16x2(p.v_cache[pg + at]));
-      }
-      acc.x += pi * vv[0], acc.y += pi * vv[1], acc.z += pi * vv[2], acc.w += pi * vv[3];
+// ------------------------------------------------- tensor core primitives
+
+__device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// f16 x f16 -> fp32 instruction descriptor, M = N = 128, both operands K-major.
+constexpr uint32_t kExtIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+
+// Descriptor of a K-major operand without swizzle: core matrices of 8 rows x
+// 16 bytes, the next 16-byte column kExtColumn on (low word), the next 8 rows
+// 128 bytes on (high word). The products of a tile walk the low word.
+__device__ __forceinline__ uint32_t operand_desc_lo(uint32_t addr) { return (addr >> 4) | ((kExtColumn >> 4) << 16); }
+constexpr uint32_t kExtDescHi = (128u >> 4) | (1u << 14);
+constexpr uint32_t kExtDescStep = (2u * kExtColumn) >> 4;   // 16 elements of the summed dimension
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kExtIdesc), "r"(add ? 1u : 0u), "r"(kExtDescHi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kExtIdesc), "r"(add ? 1u : 0u), "r"(kExtDescHi)
+      : "memory");
+}
+
+#define PDA_R8(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3]), "=r"(x[i + 4]), "=r"(x[i + 5]), \
+      "=r"(x[i + 6]), "=r"(x[i + 7])
+#define PDA_W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), \
+      "r"(x[i + 6]), "r"(x[i + 7])
+// 32 columns of this warp's 32 lanes <-> 32 registers per lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : PDA_R8(x, 0), PDA_R8(x, 8), PDA_R8(x, 16), PDA_R8(x, 24)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      PDA_W8(x, 0), PDA_W8(x, 8), PDA_W8(x, 16), PDA_W8(x, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 16 e4m3 bytes -> 16 f16 (two 16-byte columns' worth), exact.
+__device__ __forceinline__ void e4m3x16_to_f16(const uint4& x, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_lo_to_f16x2(x.x), e4m3x2_hi_to_f16x2(x.x), e4m3x2_lo_to_f16x2(x.y), e4m3x2_hi_to_f16x2(x.y));
+  hi = make_uint4(e4m3x2_lo_to_f16x2(x.z), e4m3x2_hi_to_f16x2(x.z), e4m3x2_lo_to_f16x2(x.w), e4m3x2_hi_to_f16x2(x.w));
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// What a tile slot covers. Tiles of 128 tokens [j0[x], j1[x]) hold what block
+// x's rows attend to.
+struct ExtendTile {
+  int seq, row0, rows;          // first query row (token) in the packing; rows (token, head) of the tile
+  int pos0;                     // position of the first token
+  int kv_lo, kv_hi;             // tokens some row attends to
+  int j0[2], j1[2];
+  int jmin, jmax;
+  bool both;                    // both blocks hold the same rows
+};
+
+__device__ __forceinline__ bool extend_tile(const ExtendParams& p, int slot, int split, ExtendTile& t) {
+  // Sequence s starts at slot starts[s] / tile_tokens + s, which leaves each
+  // sequence room for its tiles whatever the lengths are.
+  int lo = 0, hi = p.num_seqs - 1;
+  const int base = __ldg(p.query_starts);
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((__ldg(p.query_starts + mid) - base) / p.tile_tokens + mid <= slot)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int s = lo;
+  const int start = max(0, min(__ldg(p.query_starts + s), p.num_tokens));
+  const int end = max(start, min(__ldg(p.query_starts + s + 1), p.num_tokens));
+  const int n = end - start;
+  const int first = (slot - ((__ldg(p.query_starts + s) - base) / p.tile_tokens + s)) * p.tile_tokens;
+  if (first < 0 || first >= n) return false;
+  const int tokens = min(p.tile_tokens, n - first);
+  const long long cap = (long long)p.max_blocks * p.block_size;
+  const int len = (int)max(0ll, min((long long)__ldg(p.seq_lens + s), cap));
+  t.seq = s;
+  t.row0 = start + first;
+  t.rows = tokens * p.gqa;
+  t.pos0 = len - n + first;
+  t.both = t.rows <= kExtRows;
+  t.kv_lo = p.window > 0 ? max(0, t.pos0 - p.window + 1) : 0;
+  t.kv_hi = max(0, t.pos0 + tokens);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int t0 = t.both ? 0 : x * kExtRows / p.gqa;                                // first token of the block
+    const int t1 = t.both ? tokens : min(tokens, ((x + 1) * kExtRows - 1) / p.gqa + 1);  // behind its last one
+    const int p0 = t.pos0 + t0, p1 = t.pos0 + t1;
+    const int lo_x = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
+    t.j0[x] = lo_x / kExtTile;
+    t.j1[x] = p1 > 0 && t1 > t0 ? (p1 - 1) / kExtTile + 1 : t.j0[x];
+  }
+  t.jmin = t.j0[0];
+  t.jmax = t.both ? t.j1[0] : max(t.j1[0], t.j1[1]);
+  if (p.nsplit > 1) {
+    const int per = (t.jmax - t.jmin + p.nsplit - 1) / p.nsplit;
+    const int a = t.jmin + split * per, b = min(t.jmax, a + per);
+    t.jmin = min(a, t.jmax);
+    t.jmax = max(t.jmin, b);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      t.j0[x] = max(t.j0[x], t.jmin);
+      t.j1[x] = max(t.j0[x], min(t.j1[x], t.jmax));
     }
   }
-  store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, row, h, lane, pos >= 0, m, l, acc);
+  return true;
+}
+
+// The tiles block x takes: j0, j0 + step, ... below j1.
+__device__ __forceinline__ void block_tiles(const ExtendTile& t, int x, int& j0, int& j1, int& step) {
+  j0 = t.j0[x] + (t.both ? x : 0);
+  j1 = t.j1[x];
+  step = t.both ? 2 : 1;
+  if (j0 > j1) j0 = j1;
+}
+
+__global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const ExtendParams p) {
+  extern __shared__ __align__(1024) uint8_t ext_smem[];
+  uint8_t* const smem = ext_smem;
+  __shared__ volatile int abort_flag;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kvh = blockIdx.y, split = blockIdx.z;
+  ExtendTile t;
+  // later tiles of a sequence see more tokens: they go first
+  if (!extend_tile(p, p.tiles - 1 - (int)blockIdx.x, split, t)) return;   // uniform over the CTA
+
+  const uint32_t sm = smem_u32(smem);
+  const uint32_t bars = sm + kExtBarOff;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kExtBarOff + kBarCount * 8);
+  if (tid == 0) {
+    abort_flag = 0;
+    mbar_init(bar(kBarQ), 8);
+    for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 1);
+    for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 1);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + x), 4), mbar_init(bar(kBarO + x), 1);
+    fence_barrier_init();
+  }
+  if (warp == 16) tmem_alloc(smem_u32(tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  // Bounded: a wait that gives up records it and sends every role to the end.
+  auto wait = [&](int b, uint32_t parity) -> bool {
+    if (mbar_wait_bounded(bar(b), parity, &abort_flag, kWaitLimitNs)) return true;
+    if (!abort_flag) atomicOr(&g_status, kStatusFullWaitTimeout);
+    abort_flag = 1;
+    return false;
+  };
+  auto warp_wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+
+  if (warp < 8) {
+    regs_inc<kExtSoftmaxRegs>();
+    // ---------------------------------------------------------- softmax
+    const int x = warp >> 2;
+    const int row = t.both ? (tid & 127) : tid;               // of the tile
+    const int tok = row / p.gqa;
+    const bool live = row < t.rows;
+    const size_t orow = ((size_t)(t.row0 + tok) * p.num_heads + kvh * p.gqa + row % p.gqa);
+    // The row's queries: shifted by a power of two into f16 (its largest |q|
+    // in [2^14, 2^15)), stored as this row of the A operand.
+    float c;
+    {
+      uint4 v[16];
+      uint32_t mx = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kHeadDim);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        mx = __vmaxu2(mx, v[i].x & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, v[i].y & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, v[i].z & 0x7FFF7FFFu);
+        mx = __vmaxu2(mx, v[i].w & 0x7FFF7FFFu);
+      }
+      mx = max(mx & 0xFFFFu, mx >> 16);
+      const int e = mx == 0u ? 0 : min(max((int)(mx >> 7) - 127 - 14, -100), 113);
+      const float down = p.negate ? -exp2_int(-e) : exp2_int(-e);
+      c = fmaxf(p.logit_scale_log2 * exp2_int(e), 1.17549435e-38f);
+      if (x == 0 || !t.both) {
+        const uint32_t dst = sm + kExtQOff + (uint32_t)x * kExtOperand + (uint32_t)(tid & 127) * 16u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          st_shared_v4(dst + (uint32_t)i * kExtColumn,
+                       make_uint4(pack_f16x2(bf16lo_f32(v[i].x) * down, bf16hi_f32(v[i].x) * down),
+                                  pack_f16x2(bf16lo_f32(v[i].y) * down, bf16hi_f32(v[i].y) * down),
+                                  pack_f16x2(bf16lo_f32(v[i].z) * down, bf16hi_f32(v[i].z) * down),
+                                  pack_f16x2(bf16lo_f32(v[i].w) * down, bf16hi_f32(v[i].w) * down)));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarQ));
+    }
+    const int hi = live ? t.pos0 + tok : -1;                  // last token of the row
+    const int lo = p.window > 0 ? max(0, hi - p.window + 1) : 0;
+    // tiles inside [in_lo, in_hi] need no mask for any live row of the block
+    const int last_row = min(t.rows, t.both ? kExtRows : (x + 1) * kExtRows) - 1;
+    const int first_row = t.both ? 0 : x * kExtRows;
+    const int in_hi = t.pos0 + first_row / p.gqa;
+    const int in_lo = p.window > 0 ? t.pos0 + last_row / p.gqa - p.window + 1 : 0;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // lane 32 * (warp mod 4) in bits 16..
+    const uint32_t s_addr = tmem + lanes + (uint32_t)x * 128u;
+    const uint32_t o_addr = tmem + lanes + 256u + (uint32_t)x * 128u;
+    int j, j1, step;
+    block_tiles(t, x, j, j1, step);
+    const bool any = j < j1;
+    float m = -INFINITY, l = 0.f;
+    uint32_t phase = 0;
+    bool ok = true, first = true;
+    for (; j < j1; j += step, phase ^= 1, first = false) {
+      if (!warp_wait(kBarS + x, phase)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      // Columns 0..63 and 64..127 in turn, so that about 64 values are live:
+      // the first half is read again for the exponentials. P goes to columns
+      // 64..127: its second half first, when those are in registers.
+      const int t0 = j * kExtTile;
+      const bool edge = t0 < in_lo || t0 + kExtTile - 1 > in_hi;
+      const int lo_c = lo - t0, hi_c = hi - t0;
+      uint32_t u[64], v[64];
+      tmem_ld32(s_addr, u);
+      tmem_ld32(s_addr + 32u, u + 32);
+      tmem_wait_ld();
+      tmem_ld32(s_addr + 64u, v);
+      tmem_ld32(s_addr + 96u, v + 32);
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto hide = [&](uint32_t (&w)[64], int c0) {
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (c0 + i < lo_c || c0 + i > hi_c) w[i] = 0xFF800000u;   // -inf
+        }
+      };
+      hide(u, 0);
+#pragma unroll
+      for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i]));
+      tmem_wait_ld();
+      hide(v, 64);
+#pragma unroll
+      for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const bool grow = top > m + kExtSlack;     // m = -inf: the row's first visible token
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? top : m;
+        const float f = (m == -INFINITY || !grow) ? 1.f : fast_exp2(m - mn);
+        // O holds earlier tiles' sums (their product is complete: S was issued after it)
+        if (!first && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t o[32];
+            tmem_ld32(o_addr + 32u * i, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st32(o_addr + 32u * i, o);
+          }
+        }
+        l *= f;
+        m = mn;
+      }
+      const float b = m == -INFINITY ? 0.f : m - kExtOffset;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      auto weights = [&](uint32_t (&w)[64], uint32_t addr) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float a = fast_exp2(__fmaf_rn(__uint_as_float(w[2 * i]), c, -b));
+          const float e = fast_exp2(__fmaf_rn(__uint_as_float(w[2 * i + 1]), c, -b));
+          sum[i & 3] += a + e;
+          pk[i] = pack_f16x2(a, e);
+        }
+        tmem_st32(addr, pk);
+      };
+      tmem_ld32(s_addr, u);
+      tmem_ld32(s_addr + 32u, u + 32);
+      weights(v, s_addr + 96u);
+      tmem_wait_ld();
+      hide(u, 0);
+      weights(u, s_addr + 64u);
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarP + x));
+    }
+    // ---------------------------------------------------------- output
+    if (any && ok) ok = warp_wait(kBarO + x, 0);
+    tc_fence_after();
+    const float mt = m == -INFINITY ? -INFINITY : m - kExtOffset;
+    float mine = 1.f, other = 0.f;    // factors of this block's O and the other's
+    float M = mt, L = l;
+    float* swap = reinterpret_cast<float*>(smem + kExtKOff);   // [128 columns][128 rows], then m, l
+    if (t.both) {
+      // Every product has been waited for by one of the two blocks: the
+      // stages are free. B hands over, A joins.
+      const int bad = named_barrier_or(1, 256, ok ? 0 : 1);
+      if (x == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[32];
+          if (any && !bad) {
+            tmem_ld32(o_addr + 32u * i, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) swap[(32 * i + k) * 128 + row] = any && !bad ? __uint_as_float(o[k]) : 0.f;
+        }
+        swap[128 * 128 + row] = mt;
+        swap[129 * 128 + row] = l;
+      }
+      (void)named_barrier_or(1, 256, 0);
+      if (bad) ok = false;
+      if (x == 0) {
+        const float mb = swap[128 * 128 + row], lb = swap[129 * 128 + row];
+        M = fmaxf(mt, mb);
+        mine = mt == -INFINITY ? 0.f : fast_exp2(mt - M);
+        other = mb == -INFINITY ? 0.f : fast_exp2(mb - M);
+        L = l * mine + lb * other;
+      }
+    }
+    if (ok && !(t.both && x == 1)) {
+      const size_t prow = orow * p.nsplit + split;
+      float f = mine, fo = other;
+      if (p.nsplit == 1) {
+        const float zs = p.sinks && live ? __ldg(p.sinks + kvh * p.gqa + row % p.gqa) * 1.4426950408889634f : -INFINITY;
+        const float r = hi >= 0 ? finish(1.f, L, M, zs, p.v_scale) : 0.f;
+        f *= r;
+        fo *= r;
+      } else if (live) {
+        p.part_ml[prow * 2] = M;
+        p.part_ml[prow * 2 + 1] = L;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t o[32];
+        if (any) {
+          tmem_ld32(o_addr + 32u * i, o);
+          tmem_wait_ld();
+        }
+        float r[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          r[k] = any && f != 0.f ? __uint_as_float(o[k]) * f : 0.f;
+          if (t.both && fo != 0.f) r[k] += swap[(32 * i + k) * 128 + row] * fo;
+        }
+        if (!live) continue;
+        if (p.nsplit > 1) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 32 * i);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) dst[k] = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        } else if (p.out_fp8) {
+          uint32_t w[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            w[k] = f32x2_to_e4m3x2(__fdiv_rn(r[4 * k], p.out_scale), __fdiv_rn(r[4 * k + 1], p.out_scale)) |
+                   (f32x2_to_e4m3x2(__fdiv_rn(r[4 * k + 2], p.out_scale), __fdiv_rn(r[4 * k + 3], p.out_scale)) << 16);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + orow * kHeadDim + 32 * i);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHeadDim + 32 * i);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[u]) : "f"(r[8 * k + 2 * u + 1]), "f"(r[8 * k + 2 * u]));
+            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  } else if (warp < 16) {
+    regs_dec<kExtConvertRegs>();
+    // ------------------------------------------------- K and V to f16
+    const bool is_v = warp >= 12;
+    const int me = tid & 127;                                 // K: token of the tile, V: dim
+    const int bs = p.block_size;
+    const uint32_t per_page = (uint32_t)bs / 16u;             // 16-token units of a page
+    const uint32_t magic = per_page == 1 ? 0u : 0xFFFFFFFFu / per_page + 1u;
+    auto page_of = [&](uint32_t unit) { return per_page == 1 ? unit : __umulhi(unit, magic); };
+    const int32_t* table = p.block_tables + (size_t)t.seq * p.max_blocks;
+    const size_t head_bytes = (size_t)kHeadDim * bs;
+    const size_t block_bytes = head_bytes * p.num_kv_heads;
+    const uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + (size_t)kvh * head_bytes;
+    const uint32_t ring = sm + (is_v ? kExtVOff : kExtKOff);
+    const int stages = is_v ? kExtVStages : kExtKStages;
+    const int full0 = is_v ? kBarVFull : kBarKFull, free0 = is_v ? kBarVFree : kBarKFree;
+    uint4 v[8];
+    // K: the 8 chunks of 16 dims of this thread's token. V: the tile's 8
+    // units of 16 tokens of this thread's dim. What no row attends to is not
+    // read: zeros stand in (a masked weight of 0 times a NaN would be NaN).
+    auto load = [&](int j) {
+      const int t0 = j * kExtTile;
+      if (!is_v) {
+        const int tk = t0 + me;
+        const bool in = tk >= t.kv_lo && tk < t.kv_hi;
+        const uint8_t* src = nullptr;
+        if (in) {
+          const uint32_t page = page_of((uint32_t)tk >> 4);
+          const int b = checked_block(__ldg(table + page), p.block_limit);
+          src = cache + (size_t)b * block_bytes + (size_t)(tk - (int)page * bs) * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = in ? ld_nc_v4(src + (size_t)i * bs * 16) : make_uint4(0, 0, 0, 0);
+      } else {
+        // lane i mod 8 looks unit i's page up
+        const int tu = t0 + 16 * (lane & 7);
+        int b = 0;
+        if (tu + 16 > t.kv_lo && tu < t.kv_hi)
+          b = checked_block(__ldg(table + page_of((uint32_t)tu >> 4)), p.block_limit);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int ti = t0 + 16 * i;
+          const int bi = __shfl_sync(0xffffffffu, b, i);
+          if (ti + 16 > t.kv_lo && ti < t.kv_hi) {
+            const uint32_t unit = (uint32_t)ti >> 4;
+            const uint32_t u = unit - page_of(unit) * per_page;
+            const uint8_t* src = cache + (size_t)bi * block_bytes +
+                                 (p.v_shuffled ? ((size_t)u * kHeadDim + me) * 16 : (size_t)me * bs + 16 * u);
+            v[i] = ld_nc_v4(src);
+          } else {
+            v[i] = make_uint4(0, 0, 0, 0);
+          }
+        }
+      }
+    };
+    // Zeroes the tokens of unit bytes at or behind kv_hi (and in front of kv_lo).
+    auto clip = [&](uint4& x, int ti) {
+      const int a = t.kv_lo - ti, b = t.kv_hi - ti;
+      if (a <= 0 && b >= 16) return;
+      uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < a || i >= b) w[i >> 2] &= ~(0xFFu << (8 * (i & 3)));
+      x = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    int stage = 0;
+    uint32_t round = 0;
+    if (t.jmin < t.jmax) load(t.jmin);
+    for (int j = t.jmin; j < t.jmax; ++j) {
+      if (round > 0 && !warp_wait(free0 + stage, (round - 1) & 1)) break;
+      const uint32_t dst = ring + (uint32_t)stage * kExtOperand + (uint32_t)me * 16u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (is_v) clip(v[i], j * kExtTile + 16 * i);
+        uint4 a, b;
+        e4m3x16_to_f16(v[i], a, b);
+        st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
+        st_shared_v4(dst + (uint32_t)(2 * i + 1) * kExtColumn, b);
+      }
+      if (j + 1 < t.jmax) load(j + 1);
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(full0 + stage));
+      if (++stage == stages) {
+        stage = 0;
+        ++round;
+      }
+    }
+  } else {
+    regs_dec<kExtIssueRegs>();
+    // ------------------------------------------------ the products
+    if (warp == 16 && lane == 0) {
+      int j0[2], j1[2], step, prev[2] = {-1, -1}, done[2] = {0, 0};
+#pragma unroll
+      for (int x = 0; x < 2; ++x) block_tiles(t, x, j0[x], j1[x], step);
+      const int jmin = t.jmin, jmax = t.jmax, odd = step - 1;
+      const uint32_t qb = odd ? 0u : kExtOperand >> 4;     // block B's queries, in descriptor units
+      auto takes = [&](int x, int j) { return j >= j0[x] && j < j1[x] && (((j - j0[x]) & odd) == 0); };
+      bool ok = wait(kBarQ, 0);
+      int k_ready = 0, v_ready = 0;                        // tiles (from jmin) known to be there
+#pragma unroll 1
+      for (int i = 0; ok && i <= jmax - jmin; ++i) {       // the last round: what is left
+        const int j = jmin + i;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const bool mine = j < jmax && takes(x, j);
+          if (ok && prev[x] >= 0 && (mine || j >= j1[x])) {
+            // O_x += P_x V of the block's last tile
+            ok = wait(kBarP + x, (uint32_t)(done[x] - 1) & 1u);
+            for (; ok && v_ready <= prev[x]; ++v_ready)
+              ok = wait(kBarVFull + v_ready % kExtVStages, (uint32_t)(v_ready / kExtVStages) & 1u);
+            if (ok) {
+              tc_fence_after();
+              const int st = prev[x] % kExtVStages;
+              const uint32_t b = operand_desc_lo(sm + kExtVOff + (uint32_t)st * kExtOperand);
+#pragma unroll
+              for (int k = 0; k < kExtTile / 16; ++k)
+                mma_ts(tmem + 256u + x * 128u, tmem + x * 128u + 64u + 8u * k, b + k * kExtDescStep,
+                       done[x] > 1 || k > 0);
+              if (x == 1 || !takes(1, jmin + prev[0])) tc_commit(bar(kBarVFree + st));
+              if (!mine) tc_commit(bar(kBarO + x));
+              prev[x] = -1;
+            }
+          }
+          if (ok && mine) {
+            for (; ok && k_ready <= i; ++k_ready)
+              ok = wait(kBarKFull + k_ready % kExtKStages, (uint32_t)(k_ready / kExtKStages) & 1u);
+            if (ok) {
+              tc_fence_after();
+              const uint32_t a = operand_desc_lo(sm + kExtQOff) + (x ? qb : 0u);
+              const uint32_t b = operand_desc_lo(sm + kExtKOff + (uint32_t)(i % kExtKStages) * kExtOperand);
+#pragma unroll
+              for (int k = 0; k < kHeadDim / 16; ++k)
+                mma_ss(tmem + x * 128u, a + k * kExtDescStep, b + k * kExtDescStep, k > 0);
+              tc_commit(bar(kBarS + x));
+              if (x == 1 || !takes(1, j)) tc_commit(bar(kBarKFree + i % kExtKStages));
+              prev[x] = i;
+              ++done[x];
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  if (warp == 16) {
+    if (abort_flag) {
+      // products still in flight end by themselves, within this time by far
+      const unsigned long long t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 100000ull) {}
+    }
+    tc_fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// Joins the KV splits: one warp per (token, head) row.
+struct ExtendMergeParams {
+  void* out;
+  const float* part_o;
+  const float* part_ml;
+  const int32_t* query_starts;
+  int num_tokens;
+  int num_seqs;
+  int num_heads;
+  int nsplit;
+  float v_scale;
+  const float* sinks;
+  int out_fp8;
+  float out_scale;
+};
+__global__ void __launch_bounds__(kHeadDim) pda_extend_merge_kernel(const ExtendMergeParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kMergeRowsPerBlock + (threadIdx.x >> 5);
+  if (item >= (long long)p.num_tokens * p.num_heads) return;
+  const int row = (int)(item / p.num_heads), h = (int)(item % p.num_heads);
+  const int first = __ldg(p.query_starts), end = __ldg(p.query_starts + p.num_seqs);
+  grid_dependency_wait();
+  if (row < first || row >= end) return;       // a row of no sequence
+  float M = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < p.nsplit; ++i) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (item * p.nsplit + i));
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(p.part_o + (item * p.nsplit + i) * kHeadDim) + lane);
+    if (ml.x != -INFINITY) lse_fold(M, den, acc, ml.x, ml.y, o);
+  }
+  store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, row, h, lane, M != -INFINITY, M, den,
+               acc);
 }
 
 }  // namespace pda

@@ -92,10 +92,56 @@ pda_status rope_launch(pda::RopeParams& p, bool vec, cudaStream_t stream) {
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
+// ------------------------------------------------- attention of new tokens
+
+struct ExtendPlan {
+  int tile_tokens;   // new tokens of a full tile (256 rows of g heads)
+  int tiles;         // tile slots: room for every sequence's tiles, whatever the lengths
+  int nsplit;
+  size_t bytes;      // of the split partials
+};
+
+// The tiles, and how many splits of the KV range each gets: one, unless the
+// tiles of all kv heads leave SMs idle (one CTA per SM); then as many as fill
+// the SMs, of at least two 128-token tiles each at the longest context.
+// Also opts the kernel in to its shared memory, once per device.
+pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int block_size,
+                       int max_blocks, int window, ExtendPlan* pl) {
+  int sms = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    DeviceInfo& di = g_devices[dev];
+    if (!di.extend_set) {
+      // The warps trade registers inside what the CTA was launched with: a
+      // build with another count must not run.
+      cudaFuncAttributes fa;
+      if (cudaFuncGetAttributes(&fa, pda::pda_extend_kernel) != cudaSuccess || fa.numRegs != pda::kExtLaunchRegs ||
+          cudaFuncSetAttribute(pda::pda_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)pda::kExtSmem) != cudaSuccess ||
+          cudaDeviceGetAttribute(&di.extend_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return PDA_ERR_CUDA;
+      di.extend_set = true;
+    }
+    sms = di.extend_sms;
+  }
+  const int g = num_heads / num_kv_heads;
+  pl->tile_tokens = 2 * pda::kExtRows / g;
+  pl->tiles = num_tokens / pl->tile_tokens + num_seqs;
+  long long tokens = (long long)max_blocks * block_size;
+  if (window > 0 && window + pl->tile_tokens + pda::kExtTile < tokens) tokens = window + pl->tile_tokens + pda::kExtTile;
+  const long long kv_tiles = (tokens + pda::kExtTile - 1) / pda::kExtTile;
+  const long long ctas = (long long)pl->tiles * num_kv_heads;
+  long long n = sms / ctas;
+  n = n < kv_tiles / 2 ? n : kv_tiles / 2;
+  pl->nsplit = n < 1 ? 1 : (int)n;
+  pl->bytes = pl->nsplit == 1 ? 0 : (size_t)num_tokens * num_heads * pl->nsplit * (kHeadDim + 2) * sizeof(float);
+  return PDA_OK;
+}
+
 // -------------------------------------------------------------- pages
 
-// Workspace of the page calls, per (device, stream), apart from the decode
-// workspace, whose queue words have to stay as they are.
+// Workspace of a page call (in g_ops_ws, apart from the decode workspace,
+// whose queue words have to stay as they are).
 size_t page_ws_bytes(long long num_blocks, long long num_rows, long long n) {
   const size_t NB = align256((size_t)num_blocks * 4);
   return 256 + align256((size_t)num_rows * 4) + align256((size_t)n * 8) + 3 * NB;
@@ -122,7 +168,7 @@ pda::PageWs page_ws_layout(void* ptr, long long num_blocks, long long num_rows, 
 pda_status get_page_workspace(cudaStream_t stream, size_t bytes, void** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PDA_ERR_CUDA;
-  return grow_workspace(g_page_ws, dev, stream, bytes, 0, out);
+  return grow_workspace(g_ops_ws, dev, stream, bytes, 0, out);
 }
 
 pda_status page_state(const pda_page_table* t, pda::PageState* st) {
@@ -346,33 +392,101 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || misaligned(block_tables, 4) ||
       misaligned(seq_lens, 4) || misaligned(query_starts, 4))
     return PDA_ERR_INVALID_ARG;
-  pda::ExtendParams p = {};
-  p.out = out;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_cache = static_cast<const uint8_t*>(k_cache);
-  p.v_cache = static_cast<const uint8_t*>(v_cache);
-  p.block_tables = block_tables;
-  p.seq_lens = seq_lens;
-  p.query_starts = query_starts;
-  p.num_tokens = num_tokens;
-  p.num_seqs = num_seqs;
-  p.num_heads = num_heads;
-  p.num_kv_heads = num_kv_heads;
-  p.gqa = num_heads / num_kv_heads;
-  p.block_size = block_size;
-  p.max_blocks = max_num_blocks_per_seq;
-  p.window = window;
-  p.logit_scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
-  p.v_scale = v_scale;
-  p.sinks = sinks;
-  p.out_fp8 = out_dtype == PDA_OUT_E4M3;
-  p.out_scale = output_scale;
-  p.v_shuffled = kv_layout == PDA_KV_SHUFFLED_V ? 1 : 0;
-  p.block_limit = g_block_limit.load();
-  const long long blocks = ((long long)num_tokens * num_heads + pda::kExtendWarps - 1) / pda::kExtendWarps;
-  if (blocks > INT32_MAX) return PDA_ERR_UNSUPPORTED;
-  pda::pda_extend_row_kernel<<<(unsigned)blocks, pda::kExtendWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  if ((long long)num_tokens * num_heads > INT32_MAX) return PDA_ERR_UNSUPPORTED;
+  return guarded([&]() -> pda_status {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PDA_ERR_CUDA;
+    pda::ExtendParams p = {};
+    const double logit = (double)scale * (double)k_scale * 1.4426950408889634;
+    p.out = out;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k_cache = static_cast<const uint8_t*>(k_cache);
+    p.v_cache = static_cast<const uint8_t*>(v_cache);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.query_starts = query_starts;
+    p.num_tokens = num_tokens;
+    p.num_seqs = num_seqs;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.gqa = num_heads / num_kv_heads;
+    p.block_size = block_size;
+    p.max_blocks = max_num_blocks_per_seq;
+    p.window = window;
+    p.logit_scale_log2 = (float)std::fabs(logit);
+    p.negate = logit < 0.0 ? 1 : 0;
+    p.v_scale = v_scale;
+    p.sinks = sinks;
+    p.out_fp8 = out_dtype == PDA_OUT_E4M3;
+    p.out_scale = output_scale;
+    p.v_shuffled = kv_layout == PDA_KV_SHUFFLED_V ? 1 : 0;
+    p.block_limit = g_block_limit.load();
+    ExtendPlan pl;
+    pda_status st = extend_plan(dev, num_tokens, num_seqs, num_heads, num_kv_heads, block_size,
+                                max_num_blocks_per_seq, window, &pl);
+    if (st != PDA_OK) return st;
+    void* ws = nullptr;
+    st = grow_workspace(g_ops_ws, dev, stream, pl.bytes, 0, &ws);
+    if (st == PDA_ERR_WORKSPACE) {
+      // captured without pda_reserve_extend: one split needs no workspace
+      pl.nsplit = 1;
+      st = PDA_OK;
+    }
+    if (st != PDA_OK) return st;
+    p.tile_tokens = pl.tile_tokens;
+    p.tiles = pl.tiles;
+    p.nsplit = pl.nsplit;
+    if (pl.nsplit > 1) {
+      p.part_o = static_cast<float*>(ws);
+      p.part_ml = p.part_o + (size_t)num_tokens * num_heads * pl.nsplit * kHeadDim;
+    }
+    const dim3 grid((unsigned)pl.tiles, (unsigned)num_kv_heads, (unsigned)pl.nsplit);
+    pda::pda_extend_kernel<<<grid, pda::kExtThreads, pda::kExtSmem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+    if (pl.nsplit == 1) return PDA_OK;
+    pda::ExtendMergeParams m = {};
+    m.out = out;
+    m.part_o = p.part_o;
+    m.part_ml = p.part_ml;
+    m.query_starts = query_starts;
+    m.num_tokens = num_tokens;
+    m.num_seqs = num_seqs;
+    m.num_heads = num_heads;
+    m.nsplit = pl.nsplit;
+    m.v_scale = v_scale;
+    m.sinks = sinks;
+    m.out_fp8 = p.out_fp8;
+    m.out_scale = output_scale;
+    cudaLaunchConfig_t lc = {};
+    const long long rows = (long long)num_tokens * num_heads;
+    lc.gridDim = dim3((unsigned)((rows + pda::kMergeRowsPerBlock - 1) / pda::kMergeRowsPerBlock));
+    lc.blockDim = dim3(kHeadDim);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, pda::pda_extend_merge_kernel, m) == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  });
+}
+
+pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
+                              int max_num_blocks_per_seq, int block_size, cudaStream_t stream) {
+  return guarded([&]() -> pda_status {
+    pda_status st = validate_sizes(num_seqs, num_heads, num_kv_heads, kHeadDim, block_size, max_num_blocks_per_seq,
+                                   1.f, 1.f, 1.f);
+    if (st != PDA_OK) return st;
+    if (num_tokens < 0) return PDA_ERR_INVALID_ARG;
+    if ((long long)num_tokens * num_heads > INT32_MAX) return PDA_ERR_UNSUPPORTED;
+    if (num_tokens == 0 || num_seqs == 0) return PDA_OK;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PDA_ERR_CUDA;
+    ExtendPlan pl;
+    st = extend_plan(dev, num_tokens, num_seqs, num_heads, num_kv_heads, block_size, max_num_blocks_per_seq, 0, &pl);
+    void* ws = nullptr;
+    return st != PDA_OK ? st : grow_workspace(g_ops_ws, dev, stream, pl.bytes, 0, &ws);
+  });
 }
 
 pda_status pda_copy_pages(const pda_page_array* arrays, int num_arrays, const int32_t* src, const int32_t* dst,
