@@ -19,9 +19,9 @@
 //   warps 8-11        K: 16-byte loads through the block table, e4m3 -> f16 in
 //                     registers, stores in the matrix units' layout
 //   warps 12-15       V likewise
-//   warp 16           one thread issues the products (17-19 idle: registers are
-//                     traded by groups of four warps)
-// Tensor memory (512 columns): S_A, S_B (128 each; P takes the last 64 of
+//   warps 16, 17      one thread each issues the products of block A, B (18 and
+//                     19 idle: registers are traded by groups of four warps)
+// Tensor memory (512 columns): S_A, S_B (128 each; P takes the first 64 of
 // its block's), O_A, O_B. Shared memory: Q 64 KiB, two K stages and three V
 // stages of 128 tokens, 32 KiB each, in the layout without swizzle: 8 x 16
 // byte core matrices, 16-byte column c of row r at c * 2048 + r * 16, which
@@ -176,6 +176,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
       PDA_W8(x, 0), PDA_W8(x, 8), PDA_W8(x, 16), PDA_W8(x, 24)
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          addr),
+      PDA_W8(x, 0), PDA_W8(x, 8)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -203,6 +210,13 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
   return r;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Logits of columns outside [lo, hi] become -inf.
+__device__ __forceinline__ void hide(uint32_t (&w)[32], int lo, int hi) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (i < lo || i > hi) w[i] = 0xFF800000u;
+}
 
 // What a tile slot covers. Tiles of 128 tokens [j0[x], j1[x]) hold what block
 // x's rows attend to.
@@ -293,8 +307,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
   if (tid == 0) {
     abort_flag = 0;
     mbar_init(bar(kBarQ), 8);
-    for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 1);
-    for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 1);
+    for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
+    for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
     for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + x), 4), mbar_init(bar(kBarO + x), 1);
     fence_barrier_init();
   }
@@ -376,33 +390,21 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         break;
       }
       tc_fence_after();
-      // Columns 0..63 and 64..127 in turn, so that about 64 values are live:
-      // the first half is read again for the exponentials. P goes to columns
-      // 64..127: its second half first, when those are in registers.
+      // 32 columns at a time, in loops: the code stays small for the
+      // instruction cache, and reading S twice costs less than registers for
+      // all of it. P goes to the front of S, behind what has been read.
       const int t0 = j * kExtTile;
       const bool edge = t0 < in_lo || t0 + kExtTile - 1 > in_hi;
-      const int lo_c = lo - t0, hi_c = hi - t0;
-      uint32_t u[64], v[64];
-      tmem_ld32(s_addr, u);
-      tmem_ld32(s_addr + 32u, u + 32);
-      tmem_wait_ld();
-      tmem_ld32(s_addr + 64u, v);
-      tmem_ld32(s_addr + 96u, v + 32);
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      auto hide = [&](uint32_t (&w)[64], int c0) {
-        if (edge) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u[32];
+        tmem_ld32(s_addr + 32u * q, u);
+        tmem_wait_ld();
+        if (edge) hide(u, lo - t0 - 32 * q, hi - t0 - 32 * q);
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (c0 + i < lo_c || c0 + i > hi_c) w[i] = 0xFF800000u;   // -inf
-        }
-      };
-      hide(u, 0);
-#pragma unroll
-      for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i]));
-      tmem_wait_ld();
-      hide(v, 64);
-#pragma unroll
-      for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+        for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i]));
+      }
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
       const bool grow = top > m + kExtSlack;     // m = -inf: the row's first visible token
       if (__any_sync(0xffffffffu, grow)) {
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         const float f = (m == -INFINITY || !grow) ? 1.f : fast_exp2(m - mn);
         // O holds earlier tiles' sums (their product is complete: S was issued after it)
         if (!first && __any_sync(0xffffffffu, f != 1.f)) {
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < 4; ++i) {
             uint32_t o[32];
             tmem_ld32(o_addr + 32u * i, o);
@@ -425,23 +427,21 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       }
       const float b = m == -INFINITY ? 0.f : m - kExtOffset;
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      auto weights = [&](uint32_t (&w)[64], uint32_t addr) {
-        uint32_t pk[32];
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t u[32], pk[16];
+        tmem_ld32(s_addr + 32u * q, u);
+        tmem_wait_ld();
+        if (edge) hide(u, lo - t0 - 32 * q, hi - t0 - 32 * q);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float a = fast_exp2(__fmaf_rn(__uint_as_float(w[2 * i]), c, -b));
-          const float e = fast_exp2(__fmaf_rn(__uint_as_float(w[2 * i + 1]), c, -b));
+        for (int i = 0; i < 16; ++i) {
+          const float a = fast_exp2(__fmaf_rn(__uint_as_float(u[2 * i]), c, -b));
+          const float e = fast_exp2(__fmaf_rn(__uint_as_float(u[2 * i + 1]), c, -b));
           sum[i & 3] += a + e;
           pk[i] = pack_f16x2(a, e);
         }
-        tmem_st32(addr, pk);
-      };
-      tmem_ld32(s_addr, u);
-      tmem_ld32(s_addr + 32u, u + 32);
-      weights(v, s_addr + 96u);
-      tmem_wait_ld();
-      hide(u, 0);
-      weights(u, s_addr + 64u);
+        tmem_st16(s_addr + 16u * q, pk);
+      }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       tmem_wait_st();
       tc_fence_before();
@@ -595,11 +595,11 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     auto clip = [&](uint4& x, int ti) {
       const int a = t.kv_lo - ti, b = t.kv_hi - ti;
       if (a <= 0 && b >= 16) return;
-      uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < a || i >= b) w[i >> 2] &= ~(0xFFu << (8 * (i & 3)));
-      x = make_uint4(w[0], w[1], w[2], w[3]);
+      auto below = [](int n) { return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u); };
+      x.x &= below(b) & ~below(a);
+      x.y &= below(b - 4) & ~below(a - 4);
+      x.z &= below(b - 8) & ~below(a - 8);
+      x.w &= below(b - 12) & ~below(a - 12);
     };
     int stage = 0;
     uint32_t round = 0;
@@ -607,9 +607,12 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     for (int j = t.jmin; j < t.jmax; ++j) {
       if (round > 0 && !warp_wait(free0 + stage, (round - 1) & 1)) break;
       const uint32_t dst = ring + (uint32_t)stage * kExtOperand + (uint32_t)me * 16u;
+      if (is_v && (j * kExtTile < t.kv_lo || (j + 1) * kExtTile > t.kv_hi)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if (is_v) clip(v[i], j * kExtTile + 16 * i);
         uint4 a, b;
         e4m3x16_to_f16(v[i], a, b);
         st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
@@ -627,57 +630,61 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
   } else {
     regs_dec<kExtIssueRegs>();
     // ------------------------------------------------ the products
-    if (warp == 16 && lane == 0) {
-      int j0[2], j1[2], step, prev[2] = {-1, -1}, done[2] = {0, 0};
-#pragma unroll
-      for (int x = 0; x < 2; ++x) block_tiles(t, x, j0[x], j1[x], step);
-      const int jmin = t.jmin, jmax = t.jmax, odd = step - 1;
-      const uint32_t qb = odd ? 0u : kExtOperand >> 4;     // block B's queries, in descriptor units
-      auto takes = [&](int x, int j) { return j >= j0[x] && j < j1[x] && (((j - j0[x]) & odd) == 0); };
-      bool ok = wait(kBarQ, 0);
-      int k_ready = 0, v_ready = 0;                        // tiles (from jmin) known to be there
+    const int x = warp - 16;
+    if (x < 2 && lane == 0) {
+      int j0, j1, step;
+      block_tiles(t, x, j0, j1, step);
+      const uint32_t s_tm = tmem + (uint32_t)x * 128u, p_tm = s_tm, o_tm = s_tm + 256u;
+      const uint32_t qd = operand_desc_lo(sm + kExtQOff + (t.both ? 0u : (uint32_t)x * kExtOperand));
+      int prev = -1;          // tile (from jmin) whose P V is due
+      int made = 0;           // S products so far
+      // O += P V of tile prev; frees its V
+      auto pv = [&]() -> bool {
+        const int st = prev % kExtVStages;
+        if (!wait(kBarP + x, (uint32_t)(made - 1) & 1u) ||
+            !wait(kBarVFull + st, (uint32_t)(prev / kExtVStages) & 1u))
+          return false;
+        tc_fence_after();
+        uint32_t b = operand_desc_lo(sm + kExtVOff + (uint32_t)st * kExtOperand), a = p_tm;
+        // loops, not straight lines: every role's code shares the
+        // instruction cache, and a line of it missed costs more than a product
 #pragma unroll 1
-      for (int i = 0; ok && i <= jmax - jmin; ++i) {       // the last round: what is left
-        const int j = jmin + i;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const bool mine = j < jmax && takes(x, j);
-          if (ok && prev[x] >= 0 && (mine || j >= j1[x])) {
-            // O_x += P_x V of the block's last tile
-            ok = wait(kBarP + x, (uint32_t)(done[x] - 1) & 1u);
-            for (; ok && v_ready <= prev[x]; ++v_ready)
-              ok = wait(kBarVFull + v_ready % kExtVStages, (uint32_t)(v_ready / kExtVStages) & 1u);
-            if (ok) {
-              tc_fence_after();
-              const int st = prev[x] % kExtVStages;
-              const uint32_t b = operand_desc_lo(sm + kExtVOff + (uint32_t)st * kExtOperand);
-#pragma unroll
-              for (int k = 0; k < kExtTile / 16; ++k)
-                mma_ts(tmem + 256u + x * 128u, tmem + x * 128u + 64u + 8u * k, b + k * kExtDescStep,
-                       done[x] > 1 || k > 0);
-              if (x == 1 || !takes(1, jmin + prev[0])) tc_commit(bar(kBarVFree + st));
-              if (!mine) tc_commit(bar(kBarO + x));
-              prev[x] = -1;
-            }
-          }
-          if (ok && mine) {
-            for (; ok && k_ready <= i; ++k_ready)
-              ok = wait(kBarKFull + k_ready % kExtKStages, (uint32_t)(k_ready / kExtKStages) & 1u);
-            if (ok) {
-              tc_fence_after();
-              const uint32_t a = operand_desc_lo(sm + kExtQOff) + (x ? qb : 0u);
-              const uint32_t b = operand_desc_lo(sm + kExtKOff + (uint32_t)(i % kExtKStages) * kExtOperand);
-#pragma unroll
-              for (int k = 0; k < kHeadDim / 16; ++k)
-                mma_ss(tmem + x * 128u, a + k * kExtDescStep, b + k * kExtDescStep, k > 0);
-              tc_commit(bar(kBarS + x));
-              if (x == 1 || !takes(1, j)) tc_commit(bar(kBarKFree + i % kExtKStages));
-              prev[x] = i;
-              ++done[x];
-            }
-          }
+        for (int k = 0; k < kExtTile / 16; ++k, a += 8u, b += kExtDescStep) mma_ts(o_tm, a, b, made > 1 || k > 0);
+        tc_commit(bar(kBarVFree + st));
+        prev = -1;
+        return true;
+      };
+      bool ok = wait(kBarQ, 0);
+      const int tiles = t.jmax - t.jmin;
+#pragma unroll 1
+      for (int i = 0; ok && i < tiles; ++i) {
+        const int j = t.jmin + i, st = i % kExtKStages;
+        const bool mine = j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0);
+        if (prev >= 0 && (mine || j >= j1)) {
+          ok = pv();
+          if (ok && j >= j1) tc_commit(bar(kBarO + x));
+          if (!ok) break;
+        }
+        ok = wait(kBarKFull + st, (uint32_t)(i / kExtKStages) & 1u);
+        if (!ok) break;
+        if (mine) {
+          tc_fence_after();
+          uint32_t a = qd, b = operand_desc_lo(sm + kExtKOff + (uint32_t)st * kExtOperand);
+#pragma unroll 1
+          for (int k = 0; k < kHeadDim / 16; ++k, a += kExtDescStep, b += kExtDescStep) mma_ss(s_tm, a, b, k > 0);
+          tc_commit(bar(kBarS + x));
+          tc_commit(bar(kBarKFree + st));
+          prev = i;
+          ++made;
+        } else {
+          // the other block's tile: a stage is free when both have let go of it
+          mbar_arrive(bar(kBarKFree + st));
+          const int vs = i % kExtVStages;
+          ok = wait(kBarVFull + vs, (uint32_t)(i / kExtVStages) & 1u);
+          if (ok) mbar_arrive(bar(kBarVFree + vs));
         }
       }
+      if (ok && prev >= 0 && pv()) tc_commit(bar(kBarO + x));
     }
   }
   __syncwarp();
