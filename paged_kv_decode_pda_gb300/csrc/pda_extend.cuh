@@ -12,15 +12,14 @@
 // P rounds once to f16 (2^-11 relative), Q is exact in f16 after a shift of
 // its row by a power of two, K and V are exact in f16.
 //
-// Roles (20 warps):
+// Roles (16 warps):
 //   warps 0-3, 4-7    softmax of rows 0..127 (block A) and 128..255 (block B):
 //                     thread = row, a row of S read from tensor memory into
 //                     registers, P written back over it
-//   warps 8-11        K: 16-byte loads through the block table, e4m3 -> f16 in
-//                     registers, stores in the matrix units' layout
-//   warps 12-15       V likewise
-//   warps 16, 17      one thread each issues the products of block A, B (18 and
-//                     19 idle: registers are traded by groups of four warps)
+//   warps 8-11        K and V: 16-byte loads through the block table, e4m3 ->
+//                     f16 in registers, stores in the matrix units' layout
+//   warps 12, 13      issue the products of block A, B (14 and 15 idle:
+//                     registers are traded by groups of four warps)
 // Tensor memory (512 columns): S_A, S_B (128 each; P takes the first 64 of
 // its block's), O_A, O_B. Shared memory: Q 64 KiB, two K stages and three V
 // stages of 128 tokens, 32 KiB each, in the layout without swizzle: 8 x 16
@@ -70,13 +69,13 @@ struct ExtendParams {
 
 constexpr int kExtRows = 128;                         // rows of a block
 constexpr int kExtTile = 128;                         // tokens of a KV tile
-constexpr int kExtThreads = 20 * 32;
+constexpr int kExtThreads = 16 * 32;
 // Registers per thread: at launch, then after the warps have traded them.
-constexpr int kExtLaunchRegs = 96;
-constexpr int kExtSoftmaxRegs = 144;
-constexpr int kExtConvertRegs = 72;
+constexpr int kExtLaunchRegs = 128;
+constexpr int kExtSoftmaxRegs = 184;
+constexpr int kExtConvertRegs = 96;
 constexpr int kExtIssueRegs = 48;
-static_assert(256 * kExtSoftmaxRegs + 256 * kExtConvertRegs + 128 * kExtIssueRegs <= kExtThreads * kExtLaunchRegs,
+static_assert(256 * kExtSoftmaxRegs + 128 * kExtConvertRegs + 128 * kExtIssueRegs <= kExtThreads * kExtLaunchRegs,
               "the warps' registers come out of the CTA's own");
 constexpr int kExtKStages = 2;
 constexpr int kExtVStages = 3;
@@ -95,7 +94,8 @@ enum : int {                                          // barriers (8 bytes each)
   kBarS = kBarVFree + kExtVStages,                    // S of block A, B ready
   kBarP = kBarS + 2,                                  // P of block A, B ready (4 warps)
   kBarO = kBarP + 2,                                  // O of block A, B final
-  kBarCount = kBarO + 2
+  kBarTurn = kBarO + 2,                               // block A's, B's turn to issue
+  kBarCount = kBarTurn + 2
 };
 constexpr uint32_t kExtSmem = kExtBarOff + kBarCount * 8 + 16;
 static_assert(kExtSmem <= 232448, "shared memory of one CTA");
@@ -127,8 +127,12 @@ __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Arrives on `bar` once every product this warp's elected lane has issued is done.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+      : "memory");
 }
 
 // f16 x f16 -> fp32 instruction descriptor, M = N = 128, both operands K-major.
@@ -140,19 +144,37 @@ constexpr uint32_t kExtIdesc = (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) <<
 __device__ __forceinline__ uint32_t operand_desc_lo(uint32_t addr) { return (addr >> 4) | ((kExtColumn >> 4) << 16); }
 constexpr uint32_t kExtDescHi = (128u >> 4) | (1u << 14);
 constexpr uint32_t kExtDescStep = (2u * kExtColumn) >> 4;   // 16 elements of the summed dimension
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, bool add) {
+// One tile's product, eight instructions of 16 elements of the summed
+// dimension each, issued by the warp's elected lane (all lanes call). One
+// block of assembly, so that the descriptors are made by adding constants:
+// with the instructions issued one by one the issue took longer than the
+// products.
+#define PDA_MMA_SS(k)                                                                         \
+  "add.u32 x, %1, " #k "*256;\n\tadd.u32 y, %2, " #k "*256;\n\tmov.b64 a, {x, %5};\n\t"     \
+  "mov.b64 b, {y, %5};\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+#define PDA_MMA_TS(k)                                                                         \
+  "add.u32 x, %1, " #k "*8;\n\tadd.u32 y, %2, " #k "*256;\n\tmov.b64 b, {y, %5};\n\t"       \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, q;\n\t"
+// d = A B^T, both operands' tiles in shared memory.
+__device__ __forceinline__ void mma_tile_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo) {
+  static_assert(kExtDescStep == 256u, "descriptor step of PDA_MMA_SS and PDA_MMA_TS");
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(kExtIdesc), "r"(add ? 1u : 0u), "r"(kExtDescHi)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t" PDA_MMA_SS(1) PDA_MMA_SS(2) PDA_MMA_SS(3)
+          PDA_MMA_SS(4) PDA_MMA_SS(5) PDA_MMA_SS(6) PDA_MMA_SS(7) "}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kExtIdesc), "r"(0u), "r"(kExtDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
+// d (+)= A B^T, A in tensor memory.
+__device__ __forceinline__ void mma_tile_ts(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b64 b;\n\t.reg .b32 x, y;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t" PDA_MMA_TS(1) PDA_MMA_TS(2) PDA_MMA_TS(3)
+          PDA_MMA_TS(4) PDA_MMA_TS(5) PDA_MMA_TS(6) PDA_MMA_TS(7) "}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(kExtIdesc), "r"(add ? 1u : 0u), "r"(kExtDescHi)
       : "memory");
 }
@@ -175,6 +197,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* x) {
       "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
       PDA_W8(x, 0), PDA_W8(x, 8), PDA_W8(x, 16), PDA_W8(x, 24)
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : PDA_R8(x, 0), PDA_R8(x, 8)
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* x) {
   asm volatile(
@@ -204,18 +232,38 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
-__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+// 16 bytes from p, or zeros where `in` is false, without a branch.
+__device__ __forceinline__ uint4 ld_nc_v4_if(const void* p, bool in) {
   uint4 r;
-  asm volatile("ld.global.nc.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@q ld.global.nc.L1::no_allocate.L2::128B.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
+      : "l"(p), "r"((uint32_t)in));
   return r;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// Logits of columns outside [lo, hi] become -inf.
-__device__ __forceinline__ void hide(uint32_t (&w)[32], int lo, int hi) {
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (i < lo || i > hi) w[i] = 0xFF800000u;
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // What a tile slot covers. Tiles of 128 tokens [j0[x], j1[x]) hold what block
@@ -284,8 +332,8 @@ __device__ __forceinline__ bool extend_tile(const ExtendParams& p, int slot, int
 
 // The tiles block x takes: j0, j0 + step, ... below j1.
 __device__ __forceinline__ void block_tiles(const ExtendTile& t, int x, int& j0, int& j1, int& step) {
-  j0 = t.j0[x] + (t.both ? x : 0);
-  j1 = t.j1[x];
+  j0 = (x ? t.j0[1] : t.j0[0]) + (t.both ? x : 0);   // selects: an index would put t in local memory
+  j1 = x ? t.j1[1] : t.j1[0];
   step = t.both ? 2 : 1;
   if (j0 > j1) j0 = j1;
 }
@@ -309,10 +357,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     mbar_init(bar(kBarQ), 8);
     for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
     for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
-    for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + x), 4), mbar_init(bar(kBarO + x), 1);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + x), 4), mbar_init(bar(kBarO + x), 1), mbar_init(bar(kBarTurn + x), 1);
     fence_barrier_init();
   }
-  if (warp == 16) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 12) tmem_alloc(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -390,21 +438,26 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         break;
       }
       tc_fence_after();
-      // 32 columns at a time, in loops: the code stays small for the
-      // instruction cache, and reading S twice costs less than registers for
-      // all of it. P goes to the front of S, behind what has been read.
       const int t0 = j * kExtTile;
-      const bool edge = t0 < in_lo || t0 + kExtTile - 1 > in_hi;
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t u[32];
-        tmem_ld32(s_addr + 32u * q, u);
-        tmem_wait_ld();
-        if (edge) hide(u, lo - t0 - 32 * q, hi - t0 - 32 * q);
+      uint32_t s[128];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(u[i]));
+      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32u * q, s + 32 * q);
+      tmem_wait_ld();
+      if (t0 < in_lo || t0 + kExtTile - 1 > in_hi) {
+        const int first_c = lo - t0, last_c = hi - t0;
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if (i < first_c || i > last_c) s[i] = 0xFF800000u;   // -inf
       }
+      float mx[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+      for (int i = 4; i < 128; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mx[k] = i + k + 4 < 128 ? fmaxf(mx[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[(i + k + 4) & 127])))
+                                  : fmaxf(mx[k], __uint_as_float(s[i + k]));
       const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
       const bool grow = top > m + kExtSlack;     // m = -inf: the row's first visible token
       if (__any_sync(0xffffffffu, grow)) {
@@ -413,36 +466,40 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         // O holds earlier tiles' sums (their product is complete: S was issued after it)
         if (!first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + 32u * i, o);
+          for (int i = 0; i < 8; ++i) {
+            uint32_t o[16];
+            tmem_ld16(o_addr + 16u * i, o);
             tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st32(o_addr + 32u * i, o);
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(o_addr + 16u * i, o);
           }
         }
         l *= f;
         m = mn;
       }
       const float b = m == -INFINITY ? 0.f : m - kExtOffset;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t u[32], pk[16];
-        tmem_ld32(s_addr + 32u * q, u);
-        tmem_wait_ld();
-        if (edge) hide(u, lo - t0 - 32 * q, hi - t0 - 32 * q);
+      const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(-b, -b);
+      uint64_t s0 = 0, s1 = 0;                         // two fp32 sums each
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = fast_exp2(__fmaf_rn(__uint_as_float(u[2 * i]), c, -b));
-          const float e = fast_exp2(__fmaf_rn(__uint_as_float(u[2 * i + 1]), c, -b));
-          sum[i & 3] += a + e;
-          pk[i] = pack_f16x2(a, e);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint32_t* w = s + 64 * h + 2 * i;
+          const float2 z = unpack_f32x2(
+              fma_f32x2(pack_f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])), cc, bb));
+          const float pa = fast_exp2(z.x), pe = fast_exp2(z.y);
+          if (i & 1)
+            s1 = add_f32x2(s1, pack_f32x2(pa, pe));
+          else
+            s0 = add_f32x2(s0, pack_f32x2(pa, pe));
+          pk[i] = pack_f16x2(pa, pe);
         }
-        tmem_st16(s_addr + 16u * q, pk);
+        tmem_st32(s_addr + 32u * h, pk);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      const float2 both_sums = unpack_f32x2(add_f32x2(s0, s1));
+      l += both_sums.x + both_sums.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -536,64 +593,62 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       }
     }
     tc_fence_before();
-  } else if (warp < 16) {
+  } else if (warp < 12) {
     regs_dec<kExtConvertRegs>();
     // ------------------------------------------------- K and V to f16
-    const bool is_v = warp >= 12;
-    const int me = tid & 127;                                 // K: token of the tile, V: dim
-    const int bs = p.block_size;
-    const uint32_t per_page = (uint32_t)bs / 16u;             // 16-token units of a page
+    const int kv_lo = t.kv_lo, kv_hi = t.kv_hi, jmin = t.jmin, jmax = t.jmax;
+    const int me = tid & 127;                                 // token of the tile (K), dim (V)
+    const uint32_t bs = (uint32_t)p.block_size;
+    const uint32_t per_page = bs / 16u;                       // 16-token units of a page
     const uint32_t magic = per_page == 1 ? 0u : 0xFFFFFFFFu / per_page + 1u;
     auto page_of = [&](uint32_t unit) { return per_page == 1 ? unit : __umulhi(unit, magic); };
     const int32_t* table = p.block_tables + (size_t)t.seq * p.max_blocks;
-    const size_t head_bytes = (size_t)kHeadDim * bs;
-    const size_t block_bytes = head_bytes * p.num_kv_heads;
-    const uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + (size_t)kvh * head_bytes;
-    const uint32_t ring = sm + (is_v ? kExtVOff : kExtKOff);
-    const int stages = is_v ? kExtVStages : kExtKStages;
-    const int full0 = is_v ? kBarVFull : kBarKFull, free0 = is_v ? kBarVFree : kBarKFree;
-    uint4 v[8];
+    const uint32_t block_bytes = (uint32_t)kHeadDim * bs * (uint32_t)p.num_kv_heads;   // < 2^31: bs <= 128, 65535 heads
+    const uint8_t* k_cache = p.k_cache + (size_t)kvh * kHeadDim * bs;
+    const uint8_t* v_cache = p.v_cache + (size_t)kvh * kHeadDim * bs + (uint32_t)me * (p.v_shuffled ? 16u : bs);
+    const uint32_t unit_bytes = p.v_shuffled ? kHeadDim * 16u : 16u;   // V: from a page's unit to the next
     // K: the 8 chunks of 16 dims of this thread's token. V: the tile's 8
     // units of 16 tokens of this thread's dim. What no row attends to is not
     // read: zeros stand in (a masked weight of 0 times a NaN would be NaN).
-    auto load = [&](int j) {
+    // The block ids are looked up a tile ahead, by every thread for itself:
+    // handing them round with shuffles would wait behind the stores to shared
+    // memory, in whose queue shuffles stand.
+    uint4 k[8], v[8];
+    int k_id, v_id[8];
+    auto look_up = [&](int j) {
       const int t0 = j * kExtTile;
-      if (!is_v) {
-        const int tk = t0 + me;
-        const bool in = tk >= t.kv_lo && tk < t.kv_hi;
-        const uint8_t* src = nullptr;
-        if (in) {
-          const uint32_t page = page_of((uint32_t)tk >> 4);
-          const int b = checked_block(__ldg(table + page), p.block_limit);
-          src = cache + (size_t)b * block_bytes + (size_t)(tk - (int)page * bs) * 16;
-        }
+      k_id = t0 + me >= kv_lo && t0 + me < kv_hi ? __ldg(table + page_of((uint32_t)(t0 + me) >> 4)) : -1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = in ? ld_nc_v4(src + (size_t)i * bs * 16) : make_uint4(0, 0, 0, 0);
-      } else {
-        // lane i mod 8 looks unit i's page up
-        const int tu = t0 + 16 * (lane & 7);
-        int b = 0;
-        if (tu + 16 > t.kv_lo && tu < t.kv_hi)
-          b = checked_block(__ldg(table + page_of((uint32_t)tu >> 4)), p.block_limit);
+      for (int i = 0; i < 8; ++i) {
+        const int tk = t0 + 16 * i;
+        v_id[i] = tk + 16 > kv_lo && tk < kv_hi ? __ldg(table + page_of((uint32_t)tk >> 4)) : -1;
+      }
+    };
+    const bool check = p.block_limit != 0u;
+    auto load_k = [&](int j) {
+      const uint32_t tk = (uint32_t)(j * kExtTile + me);
+      if (check && k_id != -1) k_id = checked_block(k_id, p.block_limit);
+      const bool in = k_id != -1;
+      const uint8_t* src = k_cache + (in ? (uint64_t)(uint32_t)k_id * block_bytes + (tk - page_of(tk >> 4) * bs) * 16u : 0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int ti = t0 + 16 * i;
-          const int bi = __shfl_sync(0xffffffffu, b, i);
-          if (ti + 16 > t.kv_lo && ti < t.kv_hi) {
-            const uint32_t unit = (uint32_t)ti >> 4;
-            const uint32_t u = unit - page_of(unit) * per_page;
-            const uint8_t* src = cache + (size_t)bi * block_bytes +
-                                 (p.v_shuffled ? ((size_t)u * kHeadDim + me) * 16 : (size_t)me * bs + 16 * u);
-            v[i] = ld_nc_v4(src);
-          } else {
-            v[i] = make_uint4(0, 0, 0, 0);
-          }
-        }
+      for (int i = 0; i < 8; ++i) k[i] = ld_nc_v4_if(src + i * bs * 16u, in);
+    };
+    auto load_v = [&](int j) {
+      if (check) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (v_id[i] != -1) v_id[i] = checked_block(v_id[i], p.block_limit);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t unit = (uint32_t)(j * (kExtTile / 16) + i);
+        const uint32_t at = (unit - page_of(unit) * per_page) * unit_bytes;
+        v[i] = ld_nc_v4_if(v_cache + ((uint64_t)(uint32_t)v_id[i] * block_bytes + at), v_id[i] != -1);
       }
     };
     // Zeroes the tokens of unit bytes at or behind kv_hi (and in front of kv_lo).
     auto clip = [&](uint4& x, int ti) {
-      const int a = t.kv_lo - ti, b = t.kv_hi - ti;
+      const int a = kv_lo - ti, b = kv_hi - ti;
       if (a <= 0 && b >= 16) return;
       auto below = [](int n) { return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u); };
       x.x &= below(b) & ~below(a);
@@ -601,95 +656,103 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       x.z &= below(b - 8) & ~below(a - 8);
       x.w &= below(b - 12) & ~below(a - 12);
     };
-    int stage = 0;
-    uint32_t round = 0;
-    if (t.jmin < t.jmax) load(t.jmin);
-    for (int j = t.jmin; j < t.jmax; ++j) {
-      if (round > 0 && !warp_wait(free0 + stage, (round - 1) & 1)) break;
-      const uint32_t dst = ring + (uint32_t)stage * kExtOperand + (uint32_t)me * 16u;
-      if (is_v && (j * kExtTile < t.kv_lo || (j + 1) * kExtTile > t.kv_hi)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i);
-      }
+    auto store = [&](const uint4 (&x)[8], uint32_t dst) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         uint4 a, b;
-        e4m3x16_to_f16(v[i], a, b);
+        e4m3x16_to_f16(x[i], a, b);
         st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
         st_shared_v4(dst + (uint32_t)(2 * i + 1) * kExtColumn, b);
       }
-      if (j + 1 < t.jmax) load(j + 1);
+    };
+    auto publish = [&](int b) {
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(full0 + stage));
-      if (++stage == stages) {
-        stage = 0;
-        ++round;
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    if (jmin < jmax) {
+      look_up(jmin);
+      load_k(jmin);
+      load_v(jmin);
+      if (jmin + 1 < jmax) look_up(jmin + 1);
+    }
+    int ks = 0, vs = 0;
+    uint32_t kr = 0, vr = 0;                                  // rounds of the rings
+    for (int j = jmin; j < jmax; ++j) {
+      const bool more = j + 1 < jmax;
+      if (kr > 0 && !warp_wait(kBarKFree + ks, (kr - 1) & 1)) break;
+      store(k, sm + kExtKOff + (uint32_t)ks * kExtOperand + (uint32_t)me * 16u);
+      if (more) load_k(j + 1);
+      publish(kBarKFull + ks);
+      if (++ks == kExtKStages) ks = 0, ++kr;
+      if (vr > 0 && !warp_wait(kBarVFree + vs, (vr - 1) & 1)) break;
+      if (j * kExtTile < kv_lo || (j + 1) * kExtTile > kv_hi) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i);
       }
+      store(v, sm + kExtVOff + (uint32_t)vs * kExtOperand + (uint32_t)me * 16u);
+      if (more) load_v(j + 1);
+      publish(kBarVFull + vs);
+      if (++vs == kExtVStages) vs = 0, ++vr;
+      if (j + 2 < jmax) look_up(j + 2);
     }
   } else {
     regs_dec<kExtIssueRegs>();
     // ------------------------------------------------ the products
-    const int x = warp - 16;
-    if (x < 2 && lane == 0) {
+    const int x = __shfl_sync(0xffffffffu, warp - 12, 0);    // uniform, for the compiler too
+    if (x < 2) {
       int j0, j1, step;
       block_tiles(t, x, j0, j1, step);
-      const uint32_t s_tm = tmem + (uint32_t)x * 128u, p_tm = s_tm, o_tm = s_tm + 256u;
+      const uint32_t s_tm = tmem + (uint32_t)x * 128u, o_tm = s_tm + 256u;
       const uint32_t qd = operand_desc_lo(sm + kExtQOff + (t.both ? 0u : (uint32_t)x * kExtOperand));
       int prev = -1;          // tile (from jmin) whose P V is due
       int made = 0;           // S products so far
-      // O += P V of tile prev; frees its V
-      auto pv = [&]() -> bool {
-        const int st = prev % kExtVStages;
-        if (!wait(kBarP + x, (uint32_t)(made - 1) & 1u) ||
-            !wait(kBarVFull + st, (uint32_t)(prev / kExtVStages) & 1u))
-          return false;
-        tc_fence_after();
-        uint32_t b = operand_desc_lo(sm + kExtVOff + (uint32_t)st * kExtOperand), a = p_tm;
-        // loops, not straight lines: every role's code shares the
-        // instruction cache, and a line of it missed costs more than a product
-#pragma unroll 1
-        for (int k = 0; k < kExtTile / 16; ++k, a += 8u, b += kExtDescStep) mma_ts(o_tm, a, b, made > 1 || k > 0);
-        tc_commit(bar(kBarVFree + st));
-        prev = -1;
-        return true;
-      };
-      bool ok = wait(kBarQ, 0);
+      bool ok = warp_wait(kBarQ, 0);
       const int tiles = t.jmax - t.jmin;
 #pragma unroll 1
-      for (int i = 0; ok && i < tiles; ++i) {
-        const int j = t.jmin + i, st = i % kExtKStages;
-        const bool mine = j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0);
-        if (prev >= 0 && (mine || j >= j1)) {
-          ok = pv();
-          if (ok && j >= j1) tc_commit(bar(kBarO + x));
-          if (!ok) break;
-        }
-        ok = wait(kBarKFull + st, (uint32_t)(i / kExtKStages) & 1u);
+      for (int i = 0; ok && i <= tiles; ++i) {               // the last round: what is left
+        const int j = t.jmin + i;
+        const bool mine = i < tiles && j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0);
+        const bool due = prev >= 0 && (mine || j >= j1);
+        const int ks = i % kExtKStages, vs = prev % kExtVStages;
+        // P last: it is the one that the products wait for
+        if (due) ok = warp_wait(kBarVFull + vs, (uint32_t)(prev / kExtVStages) & 1u);
+        if (ok && mine) ok = warp_wait(kBarKFull + ks, (uint32_t)(i / kExtKStages) & 1u);
+        // The blocks issue in turn. Left to themselves they fall into step:
+        // both wait for both products, then both are in their softmax.
+        const bool turns = step == 1 && i < tiles;
+        if (ok && turns && (x || i)) ok = warp_wait(kBarTurn + x, (uint32_t)(x ? i : i - 1) & 1u);
+        if (ok && due) ok = warp_wait(kBarP + x, (uint32_t)(made - 1) & 1u);
         if (!ok) break;
+        tc_fence_after();
+        if (due) {
+          mma_tile_ts(o_tm, s_tm, operand_desc_lo(sm + kExtVOff + (uint32_t)vs * kExtOperand), made > 1);
+          tc_commit(bar(kBarVFree + vs));
+          if (!mine) tc_commit(bar(kBarO + x));
+          prev = -1;
+        }
         if (mine) {
-          tc_fence_after();
-          uint32_t a = qd, b = operand_desc_lo(sm + kExtKOff + (uint32_t)st * kExtOperand);
-#pragma unroll 1
-          for (int k = 0; k < kHeadDim / 16; ++k, a += kExtDescStep, b += kExtDescStep) mma_ss(s_tm, a, b, k > 0);
+          mma_tile_ss(s_tm, qd, operand_desc_lo(sm + kExtKOff + (uint32_t)ks * kExtOperand));
           tc_commit(bar(kBarS + x));
-          tc_commit(bar(kBarKFree + st));
+          tc_commit(bar(kBarKFree + ks));
           prev = i;
           ++made;
-        } else {
+        }
+        if (turns && lane == 0) mbar_arrive(bar(kBarTurn + 1 - x));
+        if (!mine && i < tiles) {
           // the other block's tile: a stage is free when both have let go of it
-          mbar_arrive(bar(kBarKFree + st));
-          const int vs = i % kExtVStages;
-          ok = wait(kBarVFull + vs, (uint32_t)(i / kExtVStages) & 1u);
-          if (ok) mbar_arrive(bar(kBarVFree + vs));
+          const int v2 = i % kExtVStages;
+          ok = warp_wait(kBarKFull + ks, (uint32_t)(i / kExtKStages) & 1u);
+          if (ok && lane == 0) mbar_arrive(bar(kBarKFree + ks));
+          ok = ok && warp_wait(kBarVFull + v2, (uint32_t)(i / kExtVStages) & 1u);
+          if (ok && lane == 0) mbar_arrive(bar(kBarVFree + v2));
         }
       }
-      if (ok && prev >= 0 && pv()) tc_commit(bar(kBarO + x));
     }
   }
   __syncwarp();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == 12) {
     if (abort_flag) {
       // products still in flight end by themselves, within this time by far
       const unsigned long long t0 = globaltimer_ns();
