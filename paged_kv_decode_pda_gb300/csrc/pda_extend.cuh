@@ -92,8 +92,8 @@ enum : int {                                          // barriers (8 bytes each)
   kBarVFull = kBarKFree + kExtKStages,
   kBarVFree = kBarVFull + kExtVStages,
   kBarS = kBarVFree + kExtVStages,                    // S of block A, B ready
-  kBarP = kBarS + 2,                                  // P of block A, B ready (4 warps)
-  kBarO = kBarP + 2,                                  // O of block A, B final
+  kBarP = kBarS + 2,                                  // P's halves, of block A, B ready (4 warps)
+  kBarO = kBarP + 4,                                  // O of block A, B final
   kBarTurn = kBarO + 2,                               // block A's, B's turn to issue
   kBarCount = kBarTurn + 2
 };
@@ -167,14 +167,14 @@ __device__ __forceinline__ void mma_tile_ss(uint32_t d, uint32_t a_lo, uint32_t 
       "r"(a_lo), "r"(b_lo), "r"(kExtIdesc), "r"(0u), "r"(kExtDescHi)
       : "memory");
 }
-// d (+)= A B^T, A in tensor memory.
-__device__ __forceinline__ void mma_tile_ts(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
+// d (+)= A B^T over half the summed dimension, A in tensor memory.
+__device__ __forceinline__ void mma_half_ts(uint32_t d, uint32_t a, uint32_t b_lo, bool add) {
   asm volatile(
       "{\n\t.reg .pred p, q, e;\n\t.reg .b64 b;\n\t.reg .b32 x, y;\n\t"
       "elect.sync _|e, 0xffffffff;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.eq.u32 q, 0, 0;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t" PDA_MMA_TS(1) PDA_MMA_TS(2) PDA_MMA_TS(3)
-          PDA_MMA_TS(4) PDA_MMA_TS(5) PDA_MMA_TS(6) PDA_MMA_TS(7) "}" ::"r"(d),
+      "}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(kExtIdesc), "r"(add ? 1u : 0u), "r"(kExtDescHi)
       : "memory");
 }
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     mbar_init(bar(kBarQ), 8);
     for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
     for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
-    for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + x), 4), mbar_init(bar(kBarO + x), 1), mbar_init(bar(kBarTurn + x), 1);
+    for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + 2 * x), 4), mbar_init(bar(kBarP + 2 * x + 1), 4), mbar_init(bar(kBarO + x), 1), mbar_init(bar(kBarTurn + x), 1);
     fence_barrier_init();
   }
   if (warp == 12) tmem_alloc(smem_u32(tmem_slot), 512);
@@ -366,13 +366,16 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
   // Bounded: a wait that gives up records it and sends every role to the end.
-  auto wait = [&](int b, uint32_t parity) -> bool {
-    if (mbar_wait_bounded(bar(b), parity, &abort_flag, kWaitLimitNs)) return true;
-    if (!abort_flag) atomicOr(&g_status, kStatusFullWaitTimeout);
-    abort_flag = 1;
-    return false;
+  // The whole warp calls; the common case is the first line alone.
+  auto warp_wait = [&](int i, uint32_t parity) -> bool {
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity)), 1)) return true;
+    const bool got = mbar_wait_bounded(bar(i), parity, &abort_flag, kWaitLimitNs);
+    if (!got) {
+      if (!abort_flag) atomicOr(&g_status, kStatusFullWaitTimeout);
+      abort_flag = 1;
+    }
+    return __all_sync(0xffffffffu, got) != 0;
   };
-  auto warp_wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
 
   if (warp < 8) {
     regs_inc<kExtSoftmaxRegs>();
@@ -497,13 +500,13 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
           pk[i] = pack_f16x2(pa, pe);
         }
         tmem_st32(s_addr + 32u * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarP + 2 * x + h));   // its product starts under the other half's weights
       }
       const float2 both_sums = unpack_f32x2(add_f32x2(s0, s1));
       l += both_sums.x + both_sums.y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarP + x));
     }
     // ---------------------------------------------------------- output
     if (any && ok) ok = warp_wait(kBarO + x, 0);
@@ -715,18 +718,23 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         const bool mine = i < tiles && j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0);
         const bool due = prev >= 0 && (mine || j >= j1);
         const int ks = i % kExtKStages, vs = prev % kExtVStages;
-        // P last: it is the one that the products wait for
         if (due) ok = warp_wait(kBarVFull + vs, (uint32_t)(prev / kExtVStages) & 1u);
         if (ok && mine) ok = warp_wait(kBarKFull + ks, (uint32_t)(i / kExtKStages) & 1u);
         // The blocks issue in turn. Left to themselves they fall into step:
         // both wait for both products, then both are in their softmax.
+        const uint32_t p_phase = (uint32_t)(made - 1) & 1u;
+        const uint32_t vd = operand_desc_lo(sm + kExtVOff + (uint32_t)vs * kExtOperand);
+        if (ok && due && (ok = warp_wait(kBarP + 2 * x, p_phase))) {
+          tc_fence_after();
+          mma_half_ts(o_tm, s_tm, vd, made > 1);
+        }
         const bool turns = step == 1 && i < tiles;
         if (ok && turns && (x || i)) ok = warp_wait(kBarTurn + x, (uint32_t)(x ? i : i - 1) & 1u);
-        if (ok && due) ok = warp_wait(kBarP + x, (uint32_t)(made - 1) & 1u);
+        if (ok && due) ok = warp_wait(kBarP + 2 * x + 1, p_phase);
         if (!ok) break;
         tc_fence_after();
         if (due) {
-          mma_tile_ts(o_tm, s_tm, operand_desc_lo(sm + kExtVOff + (uint32_t)vs * kExtOperand), made > 1);
+          mma_half_ts(o_tm, s_tm + 32u, vd + 4u * kExtDescStep, true);
           tc_commit(bar(kBarVFree + vs));
           if (!mine) tc_commit(bar(kBarO + x));
           prev = -1;
