@@ -495,12 +495,24 @@ def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Ten
            "pda_reshape_and_cache")
 
 
-def _on_device(what: str, tensors) -> None:
-    """Every tensor must lie on the current CUDA device, whose streams the calls use."""
-    dev = torch.cuda.current_device()
+def _refuse(what: str):
+    raise PdaError(PDA_ERR_INVALID_ARG, what)
+
+
+def _on_device(what: str, tensors) -> int:
+    """Every tensor must lie on the current CUDA device, whose streams the calls use; returns its index."""
+    dev = tensors[0].get_device()
     for t in tensors:
         if t.get_device() != dev:
-            raise PdaError(PDA_ERR_INVALID_ARG, "%s: tensors must be on the current CUDA device" % what)
+            _refuse(what + ": tensors must be on one CUDA device")
+    if dev < 0 or dev != torch.cuda.current_device():
+        _refuse(what + ": tensors must be on the current CUDA device")
+    return dev
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The raw handle of ``stream``, or of the current stream of device ``dev``."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
 
 
 # ---------------------------------------------------------------- rotary
@@ -524,34 +536,23 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: int = PDA_
     return f, mag.value
 
 
-def _rope_inputs(what, q, k, positions, inv_freq):
-    if q.dim() != 3 or q.dtype != torch.bfloat16 or (k is not None and (k.dim() != 3 or k.dtype != torch.bfloat16)):
-        raise PdaError(PDA_ERR_INVALID_ARG, "%s: q and k must be bf16 [T, heads, 128]" % what)
-    T, _, D = q.shape
-    if (k is not None and (k.shape[0] != T or k.shape[2] != D)) or positions.dtype != torch.int64 \
-            or positions.shape != (T,) or not positions.is_contiguous():
-        raise PdaError(PDA_ERR_INVALID_ARG, "%s: shapes (positions: contiguous int64 [T])" % what)
-    if (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.is_cuda or not inv_freq.is_contiguous()):
-        raise PdaError(PDA_ERR_INVALID_ARG, "%s: inv_freq must be a contiguous CPU float64 [rot_dim/2]" % what)
-    for t in (q, k):
-        if t is not None and t.stride(2) != 1 and t.numel():
-            raise PdaError(PDA_ERR_INVALID_ARG, "%s: the 128 dims of a head must be contiguous" % what)
+def _rope_refuse(what, heads, positions, inv_freq):
+    """Says what is wrong with a call whose quick checks failed."""
+    for x in heads:
+        if x.dtype != torch.bfloat16 or x.dim() != 3:
+            _refuse(what + ": heads must be bf16 [T, heads, 128]")
+        if x.stride(2) != 1:
+            _refuse(what + ": the 128 dims of a head must be contiguous")
+    if positions.dtype != torch.int64 or positions.dim() != 1 or not positions.is_contiguous():
+        _refuse(what + ": positions must be contiguous int64 [T]")
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1 or inv_freq.is_cuda or not inv_freq.is_contiguous():
+        _refuse(what + ": inv_freq must be a contiguous CPU float64 [rot_dim/2]")
+    _refuse(what + ": tokens, head sizes, shapes or devices do not agree (all on the current CUDA device)")
 
 
-def _rope_heads(src, dst):
-    s0, s1, _ = src.stride()
-    if dst is None:
-        return _RopeHeads(src.data_ptr(), None, s0, s1, 0, 0, src.shape[1])
-    d0, d1, _ = dst.stride()
-    return _RopeHeads(src.data_ptr(), dst.data_ptr(), s0, s1, d0, d1, src.shape[1])
-
-
-def _rope_out(what, x, out):
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or (out.stride(2) != 1 and out.numel()):
-        raise PdaError(PDA_ERR_INVALID_ARG, "%s: out must be bf16, shaped like its input, heads contiguous" % what)
-    return out
+_BF16, _I64, _I32, _F64 = torch.bfloat16, torch.int64, torch.int32, torch.float64
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_device = torch.cuda.current_device
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor, *,
@@ -563,17 +564,39 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
     (``rope_frequencies``). k may be None. Returns (q_out, k_out), allocated
     contiguous when not given; ``q_out=q`` rotates in place.
     """
-    lib = load()
-    _rope_inputs("rope", q, k, positions, inv_freq)
-    qo = _rope_out("rope", q, q_out)
-    ko = _rope_out("rope", k, k_out) if k is not None else None
-    _on_device("rope", (q, positions, qo) if k is None else (q, positions, qo, k, ko))
-    hq = _rope_heads(q, qo)
-    hk = _rope_heads(k, ko) if k is not None else None
-    _check(lib.pda_rope(ctypes.addressof(hq), ctypes.addressof(hk) if hk is not None else None, positions.data_ptr(),
-                        q.shape[0], q.shape[2], inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
-                        magnitude, _stream_ptr(stream)), "pda_rope")
-    return qo, ko
+    lib = _lib or load()
+    # One condition: a decode step spends more time in these checks than on the GPU.
+    heads = [q] if k is None else [q, k]
+    dev = q.get_device()
+    if not (positions.dtype is _I64 and positions.dim() == 1 and positions.is_contiguous()
+            and positions.get_device() == dev and inv_freq.dtype is _F64 and inv_freq.dim() == 1
+            and inv_freq.get_device() == -1 and inv_freq.is_contiguous() and q.dim() == 3):
+        _rope_refuse("rope", heads, positions, inv_freq)
+    T, D, done = positions.shape[0], q.shape[2], []
+    for x, out in zip(heads, (q_out, k_out)):
+        if x.dim() != 3 or x.dtype is not _BF16 or x.get_device() != dev:
+            _rope_refuse("rope", heads, positions, inv_freq)
+        n, h, d = x.shape
+        s0, s1, s2 = x.stride()
+        if out is None:
+            out = x.new_empty((n, h, d))
+            o0, o1, o2 = h * d, d, 1
+        elif out.shape != x.shape or out.dtype is not _BF16 or out.get_device() != dev:
+            _refuse("rope: out must be bf16, shaped like its input, on its device")
+        else:
+            o0, o1, o2 = out.stride()
+        if n != T or d != D or ((s2 != 1 or o2 != 1) and n * h):
+            _rope_refuse("rope", heads + [out], positions, inv_freq)
+        done.append(out)
+        done.append(_RopeHeads(x.data_ptr(), out.data_ptr(), s0, s1, o0, o1, h))
+    if dev != _device():
+        _rope_refuse("rope", heads, positions, inv_freq)
+    st = lib.pda_rope(ctypes.addressof(done[1]), None if k is None else ctypes.addressof(done[3]),
+                      positions.data_ptr(), T, D, inv_freq.data_ptr(), 2 * inv_freq.shape[0], 1 if interleaved else 0,
+                      magnitude, _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_rope")
+    return done[0], None if k is None else done[2]
 
 
 def rope_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
@@ -586,32 +609,57 @@ def rope_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     strides; slot_mapping and the caches as for ``reshape_and_cache``. Returns
     the rotated queries (``q_out``, allocated contiguous when not given).
     """
-    lib = load()
-    _rope_inputs("rope_and_cache", q, k, positions, inv_freq)
-    if v.shape != k.shape or v.dtype != torch.bfloat16 or (v.stride(2) != 1 and v.numel()):
-        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: v must be shaped and typed like k")
-    T, Hk, D = k.shape
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
-        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: slot_mapping must be contiguous int64 [T]")
+    lib = _lib or load()
+    what = "rope_and_cache"
+    dev = q.get_device()
+    if not (positions.dtype is _I64 and positions.dim() == 1 and positions.is_contiguous()
+            and positions.get_device() == dev and inv_freq.dtype is _F64 and inv_freq.dim() == 1
+            and inv_freq.get_device() == -1 and inv_freq.is_contiguous() and q.dim() == 3 and k.dim() == 3
+            and v.dim() == 3 and q.dtype is _BF16 and k.dtype is _BF16 and v.dtype is _BF16):
+        _rope_refuse(what, (q, k, v), positions, inv_freq)
+    T, H, D = q.shape
+    Hk = k.shape[1]
+    q0, q1, q2 = q.stride()
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if (k.shape != (T, Hk, D) or v.shape != (T, Hk, D) or positions.shape[0] != T
+            or ((q2 != 1 or k2 != 1 or v2 != 1) and T) or k.get_device() != dev or v.get_device() != dev
+            or dev != _device()):
+        _rope_refuse(what, (q, k, v), positions, inv_freq)
+    if (slot_mapping.dtype is not _I64 or slot_mapping.shape != (T,) or not slot_mapping.is_contiguous()
+            or slot_mapping.get_device() != dev):
+        _refuse(what + ": slot_mapping must be contiguous int64 [T] on q's device")
     for t in (k_cache, v_cache):
-        if t.dtype not in (torch.float8_e4m3fn, torch.uint8) or not t.is_contiguous():
-            raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: caches must be contiguous float8_e4m3fn")
+        if t.dtype not in _CACHE_TYPES or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(what + ": caches must be contiguous float8_e4m3fn on q's device")
     if k_cache.dim() != 5:
-        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: shapes")
+        _refuse(what + ": shapes")
     NB, Hk2, D16, bs, sixteen = k_cache.shape
-    v_want = (NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs)
-    if Hk2 != Hk or D16 * 16 != D or sixteen != 16 or tuple(v_cache.shape) != v_want:
-        raise PdaError(PDA_ERR_INVALID_ARG, "rope_and_cache: shapes")
-    qo = _rope_out("rope_and_cache", q, q_out)
-    _on_device("rope_and_cache", (q, k, v, positions, slot_mapping, k_cache, v_cache, qo))
-    hq, hk, hv = _rope_heads(q, qo), _rope_heads(k, None), _rope_heads(v, None)
-    _check(lib.pda_rope_and_cache(ctypes.addressof(hq), ctypes.addressof(hk), ctypes.addressof(hv),
-                                  positions.data_ptr(), slot_mapping.data_ptr(), T, D, inv_freq.data_ptr(),
-                                  2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude, k_cache.data_ptr(),
-                                  v_cache.data_ptr(), bs, NB, k_scale, v_scale,
-                                  PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE, _stream_ptr(stream)),
-           "pda_rope_and_cache")
-    return qo
+    if Hk2 != Hk or D16 * 16 != D or sixteen != 16 \
+            or v_cache.shape != ((NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs)):
+        _refuse(what + ": shapes")
+    if q_out is None:
+        q_out = q.new_empty((T, H, D))
+        o0, o1, o2 = H * D, D, 1
+    else:
+        o0, o1, o2 = q_out.stride() if q_out.dim() == 3 else (0, 0, 0)
+        if q_out.shape != q.shape or q_out.dtype is not _BF16 or q_out.get_device() != dev or (o2 != 1 and T):
+            _refuse(what + ": q_out must be bf16 and shaped like q, heads contiguous, on its device")
+    hq = _RopeHeads(q.data_ptr(), q_out.data_ptr(), q0, q1, o0, o1, H)
+    hk = _RopeHeads(k.data_ptr(), None, k0, k1, 0, 0, Hk)
+    hv = _RopeHeads(v.data_ptr(), None, v0, v1, 0, 0, Hk)
+    st = lib.pda_rope_and_cache(ctypes.addressof(hq), ctypes.addressof(hk), ctypes.addressof(hv),
+                                positions.data_ptr(), slot_mapping.data_ptr(), T, D, inv_freq.data_ptr(),
+                                2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude, k_cache.data_ptr(),
+                                v_cache.data_ptr(), bs, NB, k_scale, v_scale,
+                                PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE,
+                                _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_rope_and_cache")
+    return q_out
+
+
+_CACHE_TYPES = (torch.float8_e4m3fn, torch.uint8)
 
 
 # ------------------------------------------------- attention of new tokens
@@ -628,43 +676,42 @@ def extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     v_shuffled as for ``decode_ex``. Rows of no sequence are left as they are
     in ``out`` (uninitialised when ``out`` is not given).
     """
-    lib = load()
+    lib = _lib or load()
     if q.dim() != 3 or k_cache.dim() != 5 or block_tables.dim() != 2:
-        raise PdaError(PDA_ERR_INVALID_ARG, "extend: tensor ranks")
+        _refuse("extend: tensor ranks")
     T, H, D = q.shape
     NB, Hk, D16, bs, sixteen = k_cache.shape
     S, MB = block_tables.shape
     i32 = torch.int32
-    if (q.dtype != torch.bfloat16 or block_tables.dtype != i32 or seq_lens.dtype != i32 or query_starts.dtype != i32):
-        raise PdaError(PDA_ERR_INVALID_ARG, "extend: dtypes (q bf16, tables / seq_lens / query_starts int32)")
+    if q.dtype != torch.bfloat16 or block_tables.dtype != i32 or seq_lens.dtype != i32 or query_starts.dtype != i32:
+        _refuse("extend: dtypes (q bf16, tables / seq_lens / query_starts int32)")
     f8 = (torch.float8_e4m3fn, torch.uint8)
     if k_cache.dtype not in f8 or v_cache.dtype not in f8:
-        raise PdaError(PDA_ERR_INVALID_ARG, "extend: cache dtype must be float8_e4m3fn")
-    v_want = (NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs)
-    if (sixteen != 16 or D16 * 16 != D or tuple(v_cache.shape) != v_want or seq_lens.shape != (S,)
-            or query_starts.shape != (S + 1,)):
-        raise PdaError(PDA_ERR_INVALID_ARG, "extend: shapes")
+        _refuse("extend: cache dtype must be float8_e4m3fn")
+    if (sixteen != 16 or D16 * 16 != D
+            or v_cache.shape != ((NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs))
+            or seq_lens.shape != (S,) or query_starts.shape != (S + 1,)):
+        _refuse("extend: shapes")
     fp8 = output_scale is not None
     want = torch.float8_e4m3fn if fp8 else torch.bfloat16
     if out is None:
-        out = torch.empty(q.shape, dtype=want, device=q.device)
+        out = q.new_empty((T, H, D), dtype=want)
     elif out.shape != q.shape or out.dtype not in ((want, torch.uint8) if fp8 else (want,)):
-        raise PdaError(PDA_ERR_INVALID_ARG, "extend: out")
-    ts = [q, k_cache, v_cache, block_tables, seq_lens, query_starts, out]
+        _refuse("extend: out")
+    ts = (q, k_cache, v_cache, block_tables, seq_lens, query_starts, out)
     if sinks is not None:
         if sinks.dtype != torch.float32 or sinks.shape != (H,):
-            raise PdaError(PDA_ERR_INVALID_ARG, "extend: sinks must be a float32 [num_heads] tensor")
-        ts.append(sinks)
+            _refuse("extend: sinks must be a float32 [num_heads] tensor")
+        ts += (sinks,)
     for t in ts:
         if not t.is_contiguous():
-            raise PdaError(PDA_ERR_INVALID_ARG, "extend: tensors must be contiguous")
-    _on_device("extend", ts)
+            _refuse("extend: tensors must be contiguous")
+    dev = _on_device("extend", ts)
     _check(lib.pda_extend(out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                           block_tables.data_ptr(), seq_lens.data_ptr(), query_starts.data_ptr(), T, S, H, Hk, D, bs,
-                          MB, scale, k_scale, v_scale, int(window),
-                          PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE,
-                          sinks.data_ptr() if sinks is not None else None, PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16,
-                          output_scale if fp8 else 1.0, _stream_ptr(stream)), "pda_extend")
+                          MB, scale, k_scale, v_scale, window, PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE,
+                          None if sinks is None else sinks.data_ptr(), PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16,
+                          output_scale if fp8 else 1.0, _stream_on(stream, dev)), "pda_extend")
     return out
 
 
@@ -678,56 +725,64 @@ def reserve_extend(num_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks
 # ----------------------------------------------------------------- pages
 
 def _page_table(what, ref_counts, block_tables, seq_lens, block_size, *lists):
-    i32 = torch.int32
-    if block_tables.dim() != 2 or ref_counts.dim() != 1 or seq_lens.shape != (block_tables.shape[0],):
-        raise PdaError(PDA_ERR_INVALID_ARG, "%s: shapes (ref_counts [NB], block_tables [S, MB], seq_lens [S])" % what)
-    n = lists[0].shape[0] if lists and lists[0].dim() == 1 else 0
+    """(ctypes pda_page_table, device index) of the checked state and request lists."""
+    dev = ref_counts.get_device()
+    if block_tables.dim() != 2 or ref_counts.dim() != 1:
+        _refuse(what + ": shapes (ref_counts [NB], block_tables [S, MB], seq_lens [S])")
+    S, MB = block_tables.shape
+    if seq_lens.shape != (S,):
+        _refuse(what + ": shapes (ref_counts [NB], block_tables [S, MB], seq_lens [S])")
+    for t in (ref_counts, block_tables, seq_lens) + lists:
+        if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(what + ": tables, counts, lengths and lists must be contiguous int32 on one CUDA device")
     for t in lists:
-        if t.shape != (n,):
-            raise PdaError(PDA_ERR_INVALID_ARG, "%s: request lists must be vectors of one length" % what)
-    ts = (ref_counts, block_tables, seq_lens) + lists
-    for t in ts:
-        if t.dtype != i32 or not t.is_contiguous():
-            raise PdaError(PDA_ERR_INVALID_ARG, "%s: tables, counts, lengths and lists must be contiguous int32" % what)
-    _on_device(what, ts)
-    return _PageTable(ref_counts.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), ref_counts.shape[0],
-                      block_tables.shape[0], block_tables.shape[1], int(block_size))
+        if t.dim() != 1 or t.shape != lists[0].shape:
+            _refuse(what + ": request lists must be vectors of one length")
+    if dev < 0 or dev != _device():
+        _refuse(what + ": tensors must be on the current CUDA device")
+    return _PageTable(ref_counts.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), ref_counts.shape[0], S, MB,
+                      block_size), dev
 
 
-def _page_arrays(what, caches, num_blocks=None):
-    """(ctypes array of pda_page_array, count) of tensors ``[num_blocks, ...]``."""
-    arr = (_PageArray * max(1, len(caches)))()
-    dev = torch.cuda.current_device() if len(caches) else 0
-    for a, t in zip(arr, caches):
-        if num_blocks is None:
-            num_blocks = t.shape[0] if t.dim() else 0
+_page_array_types = {}     # ctypes array types by length (making one takes longer than filling it)
+
+
+def _page_arrays(what, caches, num_blocks, dev):
+    """(ctypes array of pda_page_array, count) of tensors ``[num_blocks, ...]`` on device ``dev``."""
+    n = len(caches)
+    kind = _page_array_types.get(n)
+    if kind is None:
+        kind = _page_array_types[n] = _PageArray * n
+    if not num_blocks:
+        return kind(), 0
+    flat = []
+    for t in caches:
         if t.dim() < 1 or t.shape[0] != num_blocks or not t.is_contiguous() or t.get_device() != dev:
-            raise PdaError(PDA_ERR_INVALID_ARG,
-                           "%s: caches must be contiguous [num_blocks, ...] tensors on the current device" % what)
-        a.base = t.data_ptr()
-        a.bytes_per_block = t.numel() // num_blocks * t.element_size() if num_blocks else 16
-    return arr, (len(caches) if num_blocks else 0)
+            _refuse(what + ": caches must be contiguous [num_blocks, ...] tensors on the current device")
+        flat.append((t.data_ptr(), t.nbytes // num_blocks))
+    return kind(*flat), n
 
 
 def copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> None:
     """``pda_copy_pages``: copy pages ``src[i]`` to ``dst[i]`` in every cache tensor ``[num_blocks, ...]``."""
-    lib = load()
+    lib = _lib or load()
     if src.dtype != torch.int32 or dst.dtype != torch.int32 or src.dim() != 1 or src.shape != dst.shape \
             or not src.is_contiguous() or not dst.is_contiguous():
-        raise PdaError(PDA_ERR_INVALID_ARG, "copy_pages: src and dst must be contiguous int32 vectors of one length")
-    arr, n = _page_arrays("copy_pages", caches)
-    _on_device("copy_pages", (src, dst))
-    _check(lib.pda_copy_pages(ctypes.addressof(arr), n, src.data_ptr(), dst.data_ptr(), src.shape[0],
-                              caches[0].shape[0] if n else 0, _stream_ptr(stream)), "pda_copy_pages")
+        _refuse("copy_pages: src and dst must be contiguous int32 vectors of one length")
+    dev = _on_device("copy_pages", (src, dst))
+    NB = caches[0].shape[0] if len(caches) and caches[0].dim() else 0
+    arr, n = _page_arrays("copy_pages", caches, NB, dev)
+    _check(lib.pda_copy_pages(ctypes.addressof(arr), n, src.data_ptr(), dst.data_ptr(), src.shape[0], NB,
+                              _stream_on(stream, dev)), "pda_copy_pages")
 
 
 def grow_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, rows: torch.Tensor,
                add: torch.Tensor, block_size: int, *, stream=None) -> None:
     """``pda_grow_pages``: row ``rows[i]`` takes ``add[i]`` more tokens, with fresh pages where it needs them."""
-    lib = load()
-    tab = _page_table("grow_pages", ref_counts, block_tables, seq_lens, block_size, rows, add)
+    lib = _lib or load()
+    tab, dev = _page_table("grow_pages", ref_counts, block_tables, seq_lens, block_size, rows, add)
     _check(lib.pda_grow_pages(ctypes.addressof(tab), rows.data_ptr(), add.data_ptr(), rows.shape[0],
-                              _stream_ptr(stream)), "pda_grow_pages")
+                              _stream_on(stream, dev)), "pda_grow_pages")
 
 
 def fork_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
@@ -737,29 +792,29 @@ def fork_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     Full pages are shared; a partly filled last page is copied to a fresh one
     in every tensor of ``caches`` (``[num_blocks, ...]`` each).
     """
-    lib = load()
-    tab = _page_table("fork_pages", ref_counts, block_tables, seq_lens, block_size, parents, children)
-    arr, n = _page_arrays("fork_pages", caches, ref_counts.shape[0])
+    lib = _lib or load()
+    tab, dev = _page_table("fork_pages", ref_counts, block_tables, seq_lens, block_size, parents, children)
+    arr, n = _page_arrays("fork_pages", caches, ref_counts.shape[0], dev)
     _check(lib.pda_fork_pages(ctypes.addressof(tab), parents.data_ptr(), children.data_ptr(), parents.shape[0],
-                              ctypes.addressof(arr), n, _stream_ptr(stream)), "pda_fork_pages")
+                              ctypes.addressof(arr), n, _stream_on(stream, dev)), "pda_fork_pages")
 
 
 def free_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, rows: torch.Tensor,
                block_size: int, *, stream=None) -> None:
     """``pda_free_pages``: rows become empty and give their pages up."""
-    lib = load()
-    tab = _page_table("free_pages", ref_counts, block_tables, seq_lens, block_size, rows)
-    _check(lib.pda_free_pages(ctypes.addressof(tab), rows.data_ptr(), rows.shape[0], _stream_ptr(stream)),
+    lib = _lib or load()
+    tab, dev = _page_table("free_pages", ref_counts, block_tables, seq_lens, block_size, rows)
+    _check(lib.pda_free_pages(ctypes.addressof(tab), rows.data_ptr(), rows.shape[0], _stream_on(stream, dev)),
            "pda_free_pages")
 
 
 def compact_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, block_size: int,
                   caches=(), *, stream=None) -> None:
     """``pda_compact_pages``: move the held pages to the lowest ids, in every cache, count and table entry."""
-    lib = load()
-    tab = _page_table("compact_pages", ref_counts, block_tables, seq_lens, block_size)
-    arr, n = _page_arrays("compact_pages", caches, ref_counts.shape[0])
-    _check(lib.pda_compact_pages(ctypes.addressof(tab), ctypes.addressof(arr), n, _stream_ptr(stream)),
+    lib = _lib or load()
+    tab, dev = _page_table("compact_pages", ref_counts, block_tables, seq_lens, block_size)
+    arr, n = _page_arrays("compact_pages", caches, ref_counts.shape[0], dev)
+    _check(lib.pda_compact_pages(ctypes.addressof(tab), ctypes.addressof(arr), n, _stream_on(stream, dev)),
            "pda_compact_pages")
 
 
