@@ -61,8 +61,9 @@ struct ExtendParams {
   int v_shuffled;
   uint32_t block_limit;
   int tile_tokens;              // tokens of a full tile: 256 / g
-  int tiles;                    // tile slots (grid x)
-  int nsplit;                   // KV splits (grid z)
+  int tiles;                    // tile slots
+  int nsplit;                   // KV splits
+  unsigned* queue;              // next work item, CTAs done (both left at zero); nullptr: items dealt out in turn
   float* part_o;                // [T][H][nsplit][128]   (nsplit > 1)
   float* part_ml;               // [T][H][nsplit][2]: reference (log2 units), l
 };
@@ -72,9 +73,9 @@ constexpr int kExtTile = 128;                         // tokens of a KV tile
 constexpr int kExtThreads = 16 * 32;
 // Registers per thread: at launch, then after the warps have traded them.
 constexpr int kExtLaunchRegs = 128;
-constexpr int kExtSoftmaxRegs = 184;
-constexpr int kExtConvertRegs = 96;
-constexpr int kExtIssueRegs = 48;
+constexpr int kExtSoftmaxRegs = 192;
+constexpr int kExtConvertRegs = 88;
+constexpr int kExtIssueRegs = 40;
 static_assert(256 * kExtSoftmaxRegs + 128 * kExtConvertRegs + 128 * kExtIssueRegs <= kExtThreads * kExtLaunchRegs,
               "the warps' registers come out of the CTA's own");
 constexpr int kExtKStages = 2;
@@ -85,9 +86,13 @@ constexpr uint32_t kExtQOff = 0;
 constexpr uint32_t kExtKOff = 2 * kExtOperand;
 constexpr uint32_t kExtVOff = kExtKOff + kExtKStages * kExtOperand;
 constexpr uint32_t kExtBarOff = kExtVOff + kExtVStages * kExtOperand;
+constexpr int kExtAhead = 4;                          // tiles before an item's end that the next one is taken
+constexpr int kExtSlots = 2;                          // work items known ahead
 enum : int {                                          // barriers (8 bytes each)
-  kBarQ = 0,                                          // queries stored (8 warps)
-  kBarKFull = 1,
+  kBarItemFull = 0,                                   // a work item described
+  kBarItemFree = kBarItemFull + kExtSlots,            // read by the 14 warps that work on it
+  kBarQ = kBarItemFree + kExtSlots,                   // queries of block A, B stored (4 warps)
+  kBarKFull = kBarQ + 2,
   kBarKFree = kBarKFull + kExtKStages,
   kBarVFull = kBarKFree + kExtKStages,
   kBarVFree = kBarVFull + kExtVStages,
@@ -95,9 +100,15 @@ enum : int {                                          // barriers (8 bytes each)
   kBarP = kBarS + 2,                                  // P's halves, of block A, B ready (4 warps)
   kBarO = kBarP + 4,                                  // O of block A, B final
   kBarTurn = kBarO + 2,                               // block A's, B's turn to issue
-  kBarCount = kBarTurn + 2
+  kBarSums = kBarTurn + 2,                            // both blocks' (m, l) exchanged (8 warps)
+  kBarJoined = kBarSums + 1,                          // both blocks' O read (8 warps)
+  kBarAhead = kBarJoined + 1,                         // the item's end is near: the next one may be taken (4 warps)
+  kBarCount = kBarAhead + 1
 };
-constexpr uint32_t kExtSmem = kExtBarOff + kBarCount * 8 + 16;
+constexpr uint32_t kExtItemOff = kExtBarOff + ((kBarCount * 8u + 15u) & ~15u);
+constexpr uint32_t kExtSumsOff = kExtItemOff + kExtSlots * 64u;
+constexpr uint32_t kExtMiscOff = kExtSumsOff + 2u * 128u * 8u;   // tensor memory base, abort flag
+constexpr uint32_t kExtSmem = kExtMiscOff + 16u;
 static_assert(kExtSmem <= 232448, "shared memory of one CTA");
 constexpr float kExtOffset = 7.f;                     // P = 2^(S - m + kExtOffset)
 constexpr float kExtSlack = 8.f;                      // growth of the maximum that leaves m as it is
@@ -228,6 +239,12 @@ __device__ __forceinline__ void e4m3x16_to_f16(const uint4& x, uint4& lo, uint4&
   lo = make_uint4(e4m3x2_lo_to_f16x2(x.x), e4m3x2_hi_to_f16x2(x.x), e4m3x2_lo_to_f16x2(x.y), e4m3x2_hi_to_f16x2(x.y));
   hi = make_uint4(e4m3x2_lo_to_f16x2(x.z), e4m3x2_hi_to_f16x2(x.z), e4m3x2_lo_to_f16x2(x.w), e4m3x2_hi_to_f16x2(x.w));
 }
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -266,38 +283,45 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// What a tile slot covers. Tiles of 128 tokens [j0[x], j1[x]) hold what block
-// x's rows attend to.
-struct ExtendTile {
+// A work item: a tile of query rows, a kv head and a share of the KV range.
+// Tiles of 128 tokens [j0, j1) hold what block A's and B's rows attend to.
+struct __align__(16) ExtendItem {
+  int more;                     // 0: no further item
   int seq, row0, rows;          // first query row (token) in the packing; rows (token, head) of the tile
   int pos0;                     // position of the first token
   int kv_lo, kv_hi;             // tokens some row attends to
-  int j0[2], j1[2];
+  int j0a, j1a, j0b, j1b;
   int jmin, jmax;
-  bool both;                    // both blocks hold the same rows
+  int both;                     // both blocks hold the same rows
+  int kvh, split;
 };
+static_assert(sizeof(ExtendItem) == 64, "one slot");
 
-__device__ __forceinline__ bool extend_tile(const ExtendParams& p, int slot, int split, ExtendTile& t) {
-  // Sequence s starts at slot starts[s] / tile_tokens + s, which leaves each
-  // sequence room for its tiles whatever the lengths are.
-  int lo = 0, hi = p.num_seqs - 1;
+// The tile of `slot`, found by the whole warp. Sequence s starts at slot
+// starts[s] / tile_tokens + s, which leaves each sequence room for its tiles
+// whatever the lengths are; the search probes 32 sequences at a time.
+__device__ __forceinline__ bool extend_item(const ExtendParams& p, int slot, ExtendItem& t) {
+  const int lane = threadIdx.x & 31;
   const int base = __ldg(p.query_starts);
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((__ldg(p.query_starts + mid) - base) / p.tile_tokens + mid <= slot)
-      lo = mid;
-    else
-      hi = mid - 1;
+  auto first_slot = [&](int s) { return (__ldg(p.query_starts + s) - base) / p.tile_tokens + s; };
+  int s = 0;
+  for (int n = p.num_seqs; n > 1;) {
+    const int step = (n + 31) / 32, probe = lane * step;
+    const unsigned hit = __ballot_sync(0xffffffffu, probe < n && first_slot(s + probe) <= slot);
+    const int k = hit ? (31 - __clz(hit)) * step : 0;
+    s += k;
+    n = min(step, n - k);
   }
-  const int s = lo;
-  const int start = max(0, min(__ldg(p.query_starts + s), p.num_tokens));
+  const int raw = __ldg(p.query_starts + s);
+  const int start = max(0, min(raw, p.num_tokens));
   const int end = max(start, min(__ldg(p.query_starts + s + 1), p.num_tokens));
+  const int len0 = __ldg(p.seq_lens + s);
   const int n = end - start;
-  const int first = (slot - ((__ldg(p.query_starts + s) - base) / p.tile_tokens + s)) * p.tile_tokens;
+  const int first = (slot - ((raw - base) / p.tile_tokens + s)) * p.tile_tokens;
   if (first < 0 || first >= n) return false;
   const int tokens = min(p.tile_tokens, n - first);
-  const long long cap = (long long)p.max_blocks * p.block_size;
-  const int len = (int)max(0ll, min((long long)__ldg(p.seq_lens + s), cap));
+  const int len = (int)max(0ll, min((long long)len0, (long long)p.max_blocks * p.block_size));
+  t.more = 1;
   t.seq = s;
   t.row0 = start + first;
   t.rows = tokens * p.gqa;
@@ -305,455 +329,604 @@ __device__ __forceinline__ bool extend_tile(const ExtendParams& p, int slot, int
   t.both = t.rows <= kExtRows;
   t.kv_lo = p.window > 0 ? max(0, t.pos0 - p.window + 1) : 0;
   t.kv_hi = max(0, t.pos0 + tokens);
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int t0 = t.both ? 0 : x * kExtRows / p.gqa;                                // first token of the block
-    const int t1 = t.both ? tokens : min(tokens, ((x + 1) * kExtRows - 1) / p.gqa + 1);  // behind its last one
+  // tiles of the block of tokens [t0, t1)
+  auto tiles_of = [&](int t0, int t1, int& j0, int& j1) {
     const int p0 = t.pos0 + t0, p1 = t.pos0 + t1;
-    const int lo_x = p.window > 0 ? max(0, p0 - p.window + 1) : 0;
-    t.j0[x] = lo_x / kExtTile;
-    t.j1[x] = p1 > 0 && t1 > t0 ? (p1 - 1) / kExtTile + 1 : t.j0[x];
-  }
-  t.jmin = t.j0[0];
-  t.jmax = t.both ? t.j1[0] : max(t.j1[0], t.j1[1]);
+    j0 = (p.window > 0 ? max(0, p0 - p.window + 1) : 0) / kExtTile;
+    j1 = p1 > 0 && t1 > t0 ? (p1 - 1) / kExtTile + 1 : j0;
+  };
+  tiles_of(0, t.both ? tokens : min(tokens, (kExtRows - 1) / p.gqa + 1), t.j0a, t.j1a);
+  tiles_of(t.both ? 0 : kExtRows / p.gqa, tokens, t.j0b, t.j1b);
+  t.jmin = t.j0a;
+  t.jmax = max(t.j1a, t.j1b);
   if (p.nsplit > 1) {
     const int per = (t.jmax - t.jmin + p.nsplit - 1) / p.nsplit;
-    const int a = t.jmin + split * per, b = min(t.jmax, a + per);
+    const int a = t.jmin + t.split * per, b = min(t.jmax, a + per);
     t.jmin = min(a, t.jmax);
     t.jmax = max(t.jmin, b);
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      t.j0[x] = max(t.j0[x], t.jmin);
-      t.j1[x] = max(t.j0[x], min(t.j1[x], t.jmax));
-    }
+    t.j0a = max(t.j0a, t.jmin), t.j1a = max(t.j0a, min(t.j1a, t.jmax));
+    t.j0b = max(t.j0b, t.jmin), t.j1b = max(t.j0b, min(t.j1b, t.jmax));
   }
   return true;
 }
 
 // The tiles block x takes: j0, j0 + step, ... below j1.
-__device__ __forceinline__ void block_tiles(const ExtendTile& t, int x, int& j0, int& j1, int& step) {
-  j0 = (x ? t.j0[1] : t.j0[0]) + (t.both ? x : 0);   // selects: an index would put t in local memory
-  j1 = x ? t.j1[1] : t.j1[0];
+__device__ __forceinline__ void block_tiles(const ExtendItem& t, int x, int& j0, int& j1, int& step) {
+  j0 = (x ? t.j0b : t.j0a) + (t.both ? x : 0);
+  j1 = x ? t.j1b : t.j1a;
   step = t.both ? 2 : 1;
   if (j0 > j1) j0 = j1;
 }
 
+// Persistent: one CTA per SM works through items; every role goes from one
+// item to the next by itself, so K and V of the next item arrive, and its
+// queries, under the end of this one.
 __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const ExtendParams p) {
   extern __shared__ __align__(1024) uint8_t ext_smem[];
   uint8_t* const smem = ext_smem;
-  __shared__ volatile int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kvh = blockIdx.y, split = blockIdx.z;
-  ExtendTile t;
-  // later tiles of a sequence see more tokens: they go first
-  if (!extend_tile(p, p.tiles - 1 - (int)blockIdx.x, split, t)) return;   // uniform over the CTA
-
   const uint32_t sm = smem_u32(smem);
   const uint32_t bars = sm + kExtBarOff;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kExtBarOff + kBarCount * 8);
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + kExtMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kExtMiscOff + 4);
   if (tid == 0) {
-    abort_flag = 0;
-    mbar_init(bar(kBarQ), 8);
+    *abort_flag = 0;
+    for (int i = 0; i < kExtSlots; ++i) mbar_init(bar(kBarItemFull + i), 1), mbar_init(bar(kBarItemFree + i), 14);
     for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
     for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
-    for (int x = 0; x < 2; ++x) mbar_init(bar(kBarS + x), 1), mbar_init(bar(kBarP + 2 * x), 4), mbar_init(bar(kBarP + 2 * x + 1), 4), mbar_init(bar(kBarO + x), 1), mbar_init(bar(kBarTurn + x), 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(kBarQ + x), 4);
+      mbar_init(bar(kBarS + x), 1);
+      mbar_init(bar(kBarP + 2 * x), 4);
+      mbar_init(bar(kBarP + 2 * x + 1), 4);
+      mbar_init(bar(kBarO + x), 1);
+      mbar_init(bar(kBarTurn + x), 1);
+    }
+    mbar_init(bar(kBarSums), 8);
+    mbar_init(bar(kBarJoined), 8);
+    mbar_init(bar(kBarAhead), 4);
     fence_barrier_init();
   }
-  if (warp == 12) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 12) tmem_alloc(sm + kExtMiscOff, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  const uint32_t tmem = *tmem_slot;
   // Bounded: a wait that gives up records it and sends every role to the end.
   // The whole warp calls; the common case is the first line alone.
   auto warp_wait = [&](int i, uint32_t parity) -> bool {
     if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar(i), parity)), 1)) return true;
-    const bool got = mbar_wait_bounded(bar(i), parity, &abort_flag, kWaitLimitNs);
+    const bool got = mbar_wait_bounded(bar(i), parity, const_cast<volatile int*>(abort_flag), kWaitLimitNs);
     if (!got) {
-      if (!abort_flag) atomicOr(&g_status, kStatusFullWaitTimeout);
-      abort_flag = 1;
+      if (!*abort_flag) atomicOr(&g_status, kStatusFullWaitTimeout);
+      *abort_flag = 1;
     }
     return __all_sync(0xffffffffu, got) != 0;
+  };
+  auto read_item = [&](int it, ExtendItem& t) {
+    const uint32_t src = sm + kExtItemOff + (uint32_t)(it % kExtSlots) * 64u;
+    int4* dst = reinterpret_cast<int4*>(&t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm volatile("ld.shared.v4.s32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(dst[i].x), "=r"(dst[i].y), "=r"(dst[i].z), "=r"(dst[i].w)
+                   : "r"(src + 16u * i));
+  };
+  auto release_item = [&](int it) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarItemFree + it % kExtSlots));
+  };
+  // Item number it, or false at the end (or on abort).
+  auto next_item = [&](int it, ExtendItem& t) -> bool {
+    if (!warp_wait(kBarItemFull + it % kExtSlots, (uint32_t)(it / kExtSlots) & 1u)) return false;
+    read_item(it, t);
+    return t.more != 0;
   };
 
   if (warp < 8) {
     regs_inc<kExtSoftmaxRegs>();
     // ---------------------------------------------------------- softmax
     const int x = warp >> 2;
-    const int row = t.both ? (tid & 127) : tid;               // of the tile
-    const int tok = row / p.gqa;
-    const bool live = row < t.rows;
-    const size_t orow = ((size_t)(t.row0 + tok) * p.num_heads + kvh * p.gqa + row % p.gqa);
-    // The row's queries: shifted by a power of two into f16 (its largest |q|
-    // in [2^14, 2^15)), stored as this row of the A operand.
-    float c;
-    {
-      uint4 v[16];
-      uint32_t mx = 0;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + orow * kHeadDim);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = live ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        mx = __vmaxu2(mx, v[i].x & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, v[i].y & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, v[i].z & 0x7FFF7FFFu);
-        mx = __vmaxu2(mx, v[i].w & 0x7FFF7FFFu);
-      }
-      mx = max(mx & 0xFFFFu, mx >> 16);
-      const int e = mx == 0u ? 0 : min(max((int)(mx >> 7) - 127 - 14, -100), 113);
-      const float down = p.negate ? -exp2_int(-e) : exp2_int(-e);
-      c = fmaxf(p.logit_scale_log2 * exp2_int(e), 1.17549435e-38f);
-      if (x == 0 || !t.both) {
-        const uint32_t dst = sm + kExtQOff + (uint32_t)x * kExtOperand + (uint32_t)(tid & 127) * 16u;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          st_shared_v4(dst + (uint32_t)i * kExtColumn,
-                       make_uint4(pack_f16x2(bf16lo_f32(v[i].x) * down, bf16hi_f32(v[i].x) * down),
-                                  pack_f16x2(bf16lo_f32(v[i].y) * down, bf16hi_f32(v[i].y) * down),
-                                  pack_f16x2(bf16lo_f32(v[i].z) * down, bf16hi_f32(v[i].z) * down),
-                                  pack_f16x2(bf16lo_f32(v[i].w) * down, bf16hi_f32(v[i].w) * down)));
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarQ));
-    }
-    const int hi = live ? t.pos0 + tok : -1;                  // last token of the row
-    const int lo = p.window > 0 ? max(0, hi - p.window + 1) : 0;
-    // tiles inside [in_lo, in_hi] need no mask for any live row of the block
-    const int last_row = min(t.rows, t.both ? kExtRows : (x + 1) * kExtRows) - 1;
-    const int first_row = t.both ? 0 : x * kExtRows;
-    const int in_hi = t.pos0 + first_row / p.gqa;
-    const int in_lo = p.window > 0 ? t.pos0 + last_row / p.gqa - p.window + 1 : 0;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // lane 32 * (warp mod 4) in bits 16..
     const uint32_t s_addr = tmem + lanes + (uint32_t)x * 128u;
-    const uint32_t o_addr = tmem + lanes + 256u + (uint32_t)x * 128u;
-    int j, j1, step;
-    block_tiles(t, x, j, j1, step);
-    const bool any = j < j1;
-    float m = -INFINITY, l = 0.f;
-    uint32_t phase = 0;
-    bool ok = true, first = true;
-    for (; j < j1; j += step, phase ^= 1, first = false) {
-      if (!warp_wait(kBarS + x, phase)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const int t0 = j * kExtTile;
-      uint32_t s[128];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32u * q, s + 32 * q);
-      tmem_wait_ld();
-      if (t0 < in_lo || t0 + kExtTile - 1 > in_hi) {
-        const int first_c = lo - t0, last_c = hi - t0;
-#pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if (i < first_c || i > last_c) s[i] = 0xFF800000u;   // -inf
-      }
-      float mx[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
-#pragma unroll
-      for (int i = 4; i < 128; i += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mx[k] = i + k + 4 < 128 ? fmaxf(mx[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[(i + k + 4) & 127])))
-                                  : fmaxf(mx[k], __uint_as_float(s[i + k]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      const bool grow = top > m + kExtSlack;     // m = -inf: the row's first visible token
-      if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? top : m;
-        const float f = (m == -INFINITY || !grow) ? 1.f : fast_exp2(m - mn);
-        // O holds earlier tiles' sums (their product is complete: S was issued after it)
-        if (!first && __any_sync(0xffffffffu, f != 1.f)) {
+    const uint32_t o_addr = s_addr + 256u;
+    // the warp's 32 rows of its block's query tile
+    const uint32_t own = sm + kExtQOff + (uint32_t)x * kExtOperand + (uint32_t)(warp & 3) * 512u;
+    float2* sums = reinterpret_cast<float2*>(smem + kExtSumsOff);   // [block][row]: reference, l
+    uint32_t s_phase = 0, o_phase = 0, join_phase = 0;
+    bool ok = true;
+    ExtendItem t;
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
-            uint32_t o[16];
-            tmem_ld16(o_addr + 16u * i, o);
-            tmem_wait_ld();
+    for (int it = 0; ok && next_item(it, t); ++it) {
+      const int row = t.both ? (tid & 127) : tid;             // of the tile
+      const int tok = row / p.gqa;
+      const bool live = row < t.rows;
+      // The row's queries: shifted by a power of two into f16 (its largest |q|
+      // in [2^14, 2^15)), stored as this row of the A operand. The products
+      // that read the last item's are complete: its O has been waited for.
+      // Lanes are 8 rows x 4 pieces of 16 bytes: a load touches 8 rows' 64
+      // bytes instead of 32 rows' 16 (an eighth of the cache lines per load of
+      // a row per lane), and 8 lanes' stores to one column have no conflicts.
+      float c = 0.f;
+      {
+        const int r8 = lane & 7, piece = lane >> 3;
+        const int wrow = (t.both ? (tid & 96) : tid & ~31);    // the warp's first row
+        uint4 vv[4][4];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st16(o_addr + 16u * i, o);
+        for (int q = 0; q < 4; ++q) {
+          const int r = wrow + 8 * q + r8, rt = r / p.gqa;
+          const uint4* src = reinterpret_cast<const uint4*>(
+              p.q + ((size_t)(t.row0 + rt) * p.num_heads + t.kvh * p.gqa + r - rt * p.gqa) * kHeadDim) + piece;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vv[q][i] = r < t.rows ? __ldg(src + 4 * i) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4(&v)[4] = vv[q];
+          uint32_t mx = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mx = __vmaxu2(mx, v[i].x & 0x7FFF7FFFu);
+            mx = __vmaxu2(mx, v[i].y & 0x7FFF7FFFu);
+            mx = __vmaxu2(mx, v[i].z & 0x7FFF7FFFu);
+            mx = __vmaxu2(mx, v[i].w & 0x7FFF7FFFu);
+          }
+          mx = max(mx & 0xFFFFu, mx >> 16);
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const int e = mx == 0u ? 0 : min(max((int)(mx >> 7) - 127 - 14, -100), 113);
+          const float down = p.negate ? -exp2_int(-e) : exp2_int(-e);
+          // row `lane` of the warp is this thread's own
+          if (piece == q) c = fmaxf(p.logit_scale_log2 * exp2_int(e), 1.17549435e-38f);
+          if (x == 0 || !t.both) {
+            const uint32_t dst = own + (uint32_t)(8 * q + r8) * 16u + (uint32_t)piece * kExtColumn;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              st_shared_v4(dst + (uint32_t)(4 * i) * kExtColumn,
+                           make_uint4(pack_f16x2(bf16lo_f32(v[i].x) * down, bf16hi_f32(v[i].x) * down),
+                                      pack_f16x2(bf16lo_f32(v[i].y) * down, bf16hi_f32(v[i].y) * down),
+                                      pack_f16x2(bf16lo_f32(v[i].z) * down, bf16hi_f32(v[i].z) * down),
+                                      pack_f16x2(bf16lo_f32(v[i].w) * down, bf16hi_f32(v[i].w) * down)));
           }
         }
-        l *= f;
-        m = mn;
-      }
-      const float b = m == -INFINITY ? 0.f : m - kExtOffset;
-      const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(-b, -b);
-      uint64_t s0 = 0, s1 = 0;                         // two fp32 sums each
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t* w = s + 64 * h + 2 * i;
-          const float2 z = unpack_f32x2(
-              fma_f32x2(pack_f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])), cc, bb));
-          const float pa = fast_exp2(z.x), pe = fast_exp2(z.y);
-          if (i & 1)
-            s1 = add_f32x2(s1, pack_f32x2(pa, pe));
-          else
-            s0 = add_f32x2(s0, pack_f32x2(pa, pe));
-          pk[i] = pack_f16x2(pa, pe);
-        }
-        tmem_st32(s_addr + 32u * h, pk);
-        tmem_wait_st();
-        tc_fence_before();
+        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarP + 2 * x + h));   // its product starts under the other half's weights
+        if (lane == 0) mbar_arrive(bar(kBarQ + x));
       }
-      const float2 both_sums = unpack_f32x2(add_f32x2(s0, s1));
-      l += both_sums.x + both_sums.y;
-    }
-    // ---------------------------------------------------------- output
-    if (any && ok) ok = warp_wait(kBarO + x, 0);
-    tc_fence_after();
-    const float mt = m == -INFINITY ? -INFINITY : m - kExtOffset;
-    float mine = 1.f, other = 0.f;    // factors of this block's O and the other's
-    float M = mt, L = l;
-    float* swap = reinterpret_cast<float*>(smem + kExtKOff);   // [128 columns][128 rows], then m, l
-    if (t.both) {
-      // Every product has been waited for by one of the two blocks: the
-      // stages are free. B hands over, A joins.
-      const int bad = named_barrier_or(1, 256, ok ? 0 : 1);
-      if (x == 1) {
+      const int hi = live ? t.pos0 + tok : -1;                // last token of the row
+      const int lo = p.window > 0 ? max(0, hi - p.window + 1) : 0;
+      // tiles inside [in_lo, in_hi] need no mask for any live row of the block
+      const int last_row = min(t.rows, t.both ? kExtRows : (x + 1) * kExtRows) - 1;
+      const int first_row = t.both ? 0 : x * kExtRows;
+      const int in_hi = t.pos0 + first_row / p.gqa;
+      const int in_lo = p.window > 0 ? t.pos0 + last_row / p.gqa - p.window + 1 : 0;
+      int j, j1, step;
+      block_tiles(t, x, j, j1, step);
+      const bool any = j < j1;
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+#pragma unroll 1
+      for (; j < j1; j += step, first = false) {
+        if (!warp_wait(kBarS + x, s_phase)) {
+          ok = false;
+          break;
+        }
+        s_phase ^= 1;
+        tc_fence_after();
+        const int t0 = j * kExtTile;
+        uint32_t s[128];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[32];
-          if (any && !bad) {
-            tmem_ld32(o_addr + 32u * i, o);
-            tmem_wait_ld();
+        for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32u * q, s + 32 * q);
+        tmem_wait_ld();
+        if (t0 < in_lo || t0 + kExtTile - 1 > in_hi) {
+          const int first_c = lo - t0, last_c = hi - t0;
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i < first_c || i > last_c) s[i] = 0xFF800000u;   // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+        for (int i = 4; i < 128; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = i + k + 4 < 128 ? fmaxf(mx[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[(i + k + 4) & 127])))
+                                    : fmaxf(mx[k], __uint_as_float(s[i + k]));
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        const bool grow = top > m + kExtSlack;     // m = -inf: the row's first visible token
+        if (__any_sync(0xffffffffu, grow)) {
+          const float mn = grow ? top : m;
+          const float f = (m == -INFINITY || !grow) ? 1.f : fast_exp2(m - mn);
+          // O holds earlier tiles' sums (their product is complete: S was issued after it)
+          if (!first && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + 16u * i, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(o_addr + 16u * i, o);
+            }
           }
-#pragma unroll
-          for (int k = 0; k < 32; ++k) swap[(32 * i + k) * 128 + row] = any && !bad ? __uint_as_float(o[k]) : 0.f;
+          l *= f;
+          m = mn;
         }
-        swap[128 * 128 + row] = mt;
-        swap[129 * 128 + row] = l;
+        const float b = m == -INFINITY ? 0.f : m - kExtOffset;
+        const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(-b, -b);
+        uint64_t s0 = 0, s1 = 0;                         // two fp32 sums each
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t* w = s + 64 * h + 2 * i;
+            const float2 z = unpack_f32x2(
+                fma_f32x2(pack_f32x2(__uint_as_float(w[0]), __uint_as_float(w[1])), cc, bb));
+            const float pa = fast_exp2(z.x), pe = fast_exp2(z.y);
+            if (i & 1)
+              s1 = add_f32x2(s1, pack_f32x2(pa, pe));
+            else
+              s0 = add_f32x2(s0, pack_f32x2(pa, pe));
+            pk[i] = pack_f16x2(pa, pe);
+          }
+          tmem_st32(s_addr + 32u * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarP + 2 * x + h));   // its product starts under the other half's weights
+        }
+        const float2 both_sums = unpack_f32x2(add_f32x2(s0, s1));
+        l += both_sums.x + both_sums.y;
       }
-      (void)named_barrier_or(1, 256, 0);
-      if (bad) ok = false;
-      if (x == 0) {
-        const float mb = swap[128 * 128 + row], lb = swap[129 * 128 + row];
-        M = fmaxf(mt, mb);
-        mine = mt == -INFINITY ? 0.f : fast_exp2(mt - M);
-        other = mb == -INFINITY ? 0.f : fast_exp2(mb - M);
-        L = l * mine + lb * other;
+      // -------------------------------------------------------- output
+      if (any && ok) {
+        ok = warp_wait(kBarO + x, o_phase);
+        o_phase ^= 1;
       }
-    }
-    if (ok && !(t.both && x == 1)) {
-      const size_t prow = orow * p.nsplit + split;
-      float f = mine, fo = other;
+      if (!ok) break;
+      tc_fence_after();
+      // read again rather than held in registers through the tiles
+      read_item(it, t);
+      release_item(it);
+      const int row2 = t.both ? (tid & 127) : tid, tok2 = row2 / p.gqa;
+      const bool live2 = row2 < t.rows;
+      const int head2 = t.kvh * p.gqa + row2 - tok2 * p.gqa;
+      const size_t orow2 = (size_t)(t.row0 + tok2) * p.num_heads + head2;
+      const float mt = m == -INFINITY ? -INFINITY : m - kExtOffset;
+      float M = mt, L = l, fa = 1.f, fb = 0.f;                // factors of this block's O and the other's
+      if (t.both) {
+        // Both blocks hold the rows: they exchange (m, l), and each reads
+        // half the columns of both O's.
+        sums[x * 128 + row2] = make_float2(mt, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarSums));
+        if (!warp_wait(kBarSums, join_phase)) break;
+        const float2 o = sums[(1 - x) * 128 + row2];
+        M = fmaxf(mt, o.x);
+        fa = mt == -INFINITY ? 0.f : fast_exp2(mt - M);
+        fb = o.x == -INFINITY ? 0.f : fast_exp2(o.x - M);
+        L = l * fa + o.y * fb;
+        tc_fence_after();
+      }
+      if (mt == -INFINITY) fa = 0.f;
+      const size_t prow = orow2 * p.nsplit + t.split;
       if (p.nsplit == 1) {
-        const float zs = p.sinks && live ? __ldg(p.sinks + kvh * p.gqa + row % p.gqa) * 1.4426950408889634f : -INFINITY;
-        const float r = hi >= 0 ? finish(1.f, L, M, zs, p.v_scale) : 0.f;
-        f *= r;
-        fo *= r;
-      } else if (live) {
-        p.part_ml[prow * 2] = M;
-        p.part_ml[prow * 2 + 1] = L;
+        const float zs = p.sinks && live2 ? __ldg(p.sinks + head2) * 1.4426950408889634f : -INFINITY;
+        const float r = live2 && t.pos0 + tok2 >= 0 ? finish(1.f, L, M, zs, p.v_scale) : 0.f;
+        fa *= r;
+        fb *= r;
+      } else if (live2 && (x == 0 || !t.both)) {
+        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, L);
       }
+      const int i0 = t.both ? 4 * x : 0, i1 = t.both ? 4 * x + 4 : 8;
+#pragma unroll 1
+      for (int i = i0; i < i1; ++i) {
+        uint32_t o[16], u[16];
+        __syncwarp();
+        tmem_ld16(o_addr + 16u * i, o);
+        if (t.both) tmem_ld16((o_addr ^ 128u) + 16u * i, u);
+        tmem_wait_ld();
+        float r[16];
+        // a factor of 0: that block saw nothing, and its O may be anything
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t o[32];
-        if (any) {
-          tmem_ld32(o_addr + 32u * i, o);
-          tmem_wait_ld();
+        for (int k = 0; k < 16; ++k) {
+          r[k] = fa != 0.f ? __uint_as_float(o[k]) * fa : 0.f;
+          if (t.both && fb != 0.f) r[k] += __uint_as_float(u[k]) * fb;
         }
-        float r[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          r[k] = any && f != 0.f ? __uint_as_float(o[k]) * f : 0.f;
-          if (t.both && fo != 0.f) r[k] += swap[(32 * i + k) * 128 + row] * fo;
-        }
-        if (!live) continue;
         if (p.nsplit > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 32 * i);
+          if (live2) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 16 * i);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            for (int k = 0; k < 4; ++k) dst[k] = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+          }
         } else if (p.out_fp8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            w[k] = f32x2_to_e4m3x2(__fdiv_rn(r[4 * k], p.out_scale), __fdiv_rn(r[4 * k + 1], p.out_scale)) |
+                   (f32x2_to_e4m3x2(__fdiv_rn(r[4 * k + 2], p.out_scale), __fdiv_rn(r[4 * k + 3], p.out_scale)) << 16);
+          st_shared_v4(own + lane * 16u + (uint32_t)i * kExtColumn, make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
           uint32_t w[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            w[k] = f32x2_to_e4m3x2(__fdiv_rn(r[4 * k], p.out_scale), __fdiv_rn(r[4 * k + 1], p.out_scale)) |
-                   (f32x2_to_e4m3x2(__fdiv_rn(r[4 * k + 2], p.out_scale), __fdiv_rn(r[4 * k + 3], p.out_scale)) << 16);
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + orow * kHeadDim + 32 * i);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kHeadDim + 32 * i);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[u]) : "f"(r[8 * k + 2 * u + 1]), "f"(r[8 * k + 2 * u]));
-            dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(r[2 * k + 1]), "f"(r[2 * k]));
+          st_shared_v4(own + lane * 16u + (uint32_t)(2 * i) * kExtColumn, make_uint4(w[0], w[1], w[2], w[3]));
+          st_shared_v4(own + lane * 16u + (uint32_t)(2 * i + 1) * kExtColumn, make_uint4(w[4], w[5], w[6], w[7]));
+        }
+      }
+      if (p.nsplit == 1) {
+        // The rows went to the warp's own part of the query tile, a 16-byte
+        // column apart (its products are done), and leave from there 8 rows x
+        // 64 bytes at a time, as the queries came.
+        __syncwarp();
+        const int r8 = lane & 7, piece = lane >> 3;
+        const int wrow = (t.both ? (tid & 96) : tid & ~31);
+        const int cols = p.out_fp8 ? 8 : 16;
+        const int c0 = t.both ? cols / 2 * x : 0, c1 = t.both ? c0 + cols / 2 : cols;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const int rr = wrow + 8 * q + r8, rt = rr / p.gqa;
+          if (rr < t.rows) {
+            uint8_t* dst = static_cast<uint8_t*>(p.out) +
+                           ((size_t)(t.row0 + rt) * p.num_heads + t.kvh * p.gqa + rr - rt * p.gqa) * (size_t)(cols * 16);
+            for (int k = c0 + piece; k < c1; k += 4)
+              *reinterpret_cast<uint4*>(dst + k * 16) =
+                  ld_shared_v4(own + (uint32_t)(8 * q + r8) * 16u + (uint32_t)k * kExtColumn);
           }
         }
       }
+      __syncwarp();
+      tc_fence_before();
+      if (t.both) {
+        // the next item's products may overwrite O, and its queries Q, once both blocks are here
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kBarJoined));
+        if (!warp_wait(kBarJoined, join_phase)) break;
+        join_phase ^= 1;
+        tc_fence_after();
+      }
     }
-    tc_fence_before();
   } else if (warp < 12) {
     regs_dec<kExtConvertRegs>();
     // ------------------------------------------------- K and V to f16
-    const int kv_lo = t.kv_lo, kv_hi = t.kv_hi, jmin = t.jmin, jmax = t.jmax;
     const int me = tid & 127;                                 // token of the tile (K), dim (V)
     const uint32_t bs = (uint32_t)p.block_size;
     const uint32_t per_page = bs / 16u;                       // 16-token units of a page
     const uint32_t magic = per_page == 1 ? 0u : 0xFFFFFFFFu / per_page + 1u;
     auto page_of = [&](uint32_t unit) { return per_page == 1 ? unit : __umulhi(unit, magic); };
-    const int32_t* table = p.block_tables + (size_t)t.seq * p.max_blocks;
     const uint32_t block_bytes = (uint32_t)kHeadDim * bs * (uint32_t)p.num_kv_heads;   // < 2^31: bs <= 128, 65535 heads
-    const uint8_t* k_cache = p.k_cache + (size_t)kvh * kHeadDim * bs;
-    const uint8_t* v_cache = p.v_cache + (size_t)kvh * kHeadDim * bs + (uint32_t)me * (p.v_shuffled ? 16u : bs);
     const uint32_t unit_bytes = p.v_shuffled ? kHeadDim * 16u : 16u;   // V: from a page's unit to the next
-    // K: the 8 chunks of 16 dims of this thread's token. V: the tile's 8
-    // units of 16 tokens of this thread's dim. What no row attends to is not
-    // read: zeros stand in (a masked weight of 0 times a NaN would be NaN).
-    // The block ids are looked up a tile ahead, by every thread for itself:
-    // handing them round with shuffles would wait behind the stores to shared
-    // memory, in whose queue shuffles stand.
-    uint4 k[8], v[8];
-    int k_id, v_id[8];
-    auto look_up = [&](int j) {
-      const int t0 = j * kExtTile;
-      k_id = t0 + me >= kv_lo && t0 + me < kv_hi ? __ldg(table + page_of((uint32_t)(t0 + me) >> 4)) : -1;
+    uint32_t ks = 0, vs = 0, kr = 0, vr = 0;                  // stages, and rounds of the rings
+    bool ok = true;
+    ExtendItem t;
+#pragma unroll 1
+    for (int it = 0; ok && next_item(it, t); ++it) {
+      release_item(it);
+      const int kv_lo = t.kv_lo, kv_hi = t.kv_hi, jmin = t.jmin, jmax = t.jmax;
+      const int near = max(jmin, jmax - kExtAhead);
+      if (jmin == jmax && lane == 0) mbar_arrive(bar(kBarAhead));
+      const int32_t* table = p.block_tables + (size_t)t.seq * p.max_blocks;
+      const uint8_t* k_cache = p.k_cache + (size_t)t.kvh * kHeadDim * bs;
+      const uint8_t* v_cache = p.v_cache + (size_t)t.kvh * kHeadDim * bs + (uint32_t)me * (p.v_shuffled ? 16u : bs);
+      // K: the 8 chunks of 16 dims of this thread's token. V: the tile's 8
+      // units of 16 tokens of this thread's dim. What no row attends to is not
+      // read: zeros stand in (a masked weight of 0 times a NaN would be NaN).
+      // The block ids are looked up a tile ahead, by every thread for itself:
+      // handing them round with shuffles would wait behind the stores to shared
+      // memory, in whose queue shuffles stand.
+      uint4 k[8], v[8];
+      int k_id, v_id[8];
+      auto look_up = [&](int j) {
+        const int t0 = j * kExtTile;
+        k_id = t0 + me >= kv_lo && t0 + me < kv_hi ? __ldg(table + page_of((uint32_t)(t0 + me) >> 4)) : -1;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tk = t0 + 16 * i;
-        v_id[i] = tk + 16 > kv_lo && tk < kv_hi ? __ldg(table + page_of((uint32_t)tk >> 4)) : -1;
+        for (int i = 0; i < 8; ++i) {
+          const int tk = t0 + 16 * i;
+          v_id[i] = tk + 16 > kv_lo && tk < kv_hi ? __ldg(table + page_of((uint32_t)tk >> 4)) : -1;
+        }
+      };
+      const bool check = p.block_limit != 0u;
+      auto load_k = [&](int j) {
+        const uint32_t tk = (uint32_t)(j * kExtTile + me);
+        if (check && k_id != -1) k_id = checked_block(k_id, p.block_limit);
+        const bool in = k_id != -1;
+        const uint8_t* src = k_cache + (in ? (uint64_t)(uint32_t)k_id * block_bytes + (tk - page_of(tk >> 4) * bs) * 16u : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = ld_nc_v4_if(src + i * bs * 16u, in);
+      };
+      auto load_v = [&](int j) {
+        if (check) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (v_id[i] != -1) v_id[i] = checked_block(v_id[i], p.block_limit);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t unit = (uint32_t)(j * (kExtTile / 16) + i);
+          const uint32_t at = (unit - page_of(unit) * per_page) * unit_bytes;
+          v[i] = ld_nc_v4_if(v_cache + ((uint64_t)(uint32_t)v_id[i] * block_bytes + at), v_id[i] != -1);
+        }
+      };
+      // Zeroes the tokens of unit bytes at or behind kv_hi (and in front of kv_lo).
+      auto clip = [&](uint4& x, int ti) {
+        const int a = kv_lo - ti, b = kv_hi - ti;
+        if (a <= 0 && b >= 16) return;
+        auto below = [](int n) { return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u); };
+        x.x &= below(b) & ~below(a);
+        x.y &= below(b - 4) & ~below(a - 4);
+        x.z &= below(b - 8) & ~below(a - 8);
+        x.w &= below(b - 12) & ~below(a - 12);
+      };
+      auto store = [&](const uint4 (&x)[8], uint32_t dst) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint4 a, b;
+          e4m3x16_to_f16(x[i], a, b);
+          st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
+          st_shared_v4(dst + (uint32_t)(2 * i + 1) * kExtColumn, b);
+        }
+      };
+      auto publish = [&](int b) {
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(b));
+      };
+      if (jmin < jmax) {
+        look_up(jmin);
+        load_k(jmin);
+        load_v(jmin);
+        if (jmin + 1 < jmax) look_up(jmin + 1);
       }
-    };
-    const bool check = p.block_limit != 0u;
-    auto load_k = [&](int j) {
-      const uint32_t tk = (uint32_t)(j * kExtTile + me);
-      if (check && k_id != -1) k_id = checked_block(k_id, p.block_limit);
-      const bool in = k_id != -1;
-      const uint8_t* src = k_cache + (in ? (uint64_t)(uint32_t)k_id * block_bytes + (tk - page_of(tk >> 4) * bs) * 16u : 0);
+      for (int j = jmin; ok && j < jmax; ++j) {
+        const bool more = j + 1 < jmax;
+        if (j == near && lane == 0) mbar_arrive(bar(kBarAhead));
+        if (kr > 0) ok = warp_wait(kBarKFree + ks, (kr - 1) & 1);
+        if (!ok) break;
+        store(k, sm + kExtKOff + (uint32_t)ks * kExtOperand + (uint32_t)me * 16u);
+        if (more) load_k(j + 1);
+        publish(kBarKFull + ks);
+        if (++ks == kExtKStages) ks = 0, ++kr;
+        if (vr > 0) ok = warp_wait(kBarVFree + vs, (vr - 1) & 1);
+        if (!ok) break;
+        if (j * kExtTile < kv_lo || (j + 1) * kExtTile > kv_hi) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) k[i] = ld_nc_v4_if(src + i * bs * 16u, in);
-    };
-    auto load_v = [&](int j) {
-      if (check) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (v_id[i] != -1) v_id[i] = checked_block(v_id[i], p.block_limit);
+          for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i);
+        }
+        store(v, sm + kExtVOff + (uint32_t)vs * kExtOperand + (uint32_t)me * 16u);
+        if (more) load_v(j + 1);
+        publish(kBarVFull + vs);
+        if (++vs == kExtVStages) vs = 0, ++vr;
+        if (j + 2 < jmax) look_up(j + 2);
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t unit = (uint32_t)(j * (kExtTile / 16) + i);
-        const uint32_t at = (unit - page_of(unit) * per_page) * unit_bytes;
-        v[i] = ld_nc_v4_if(v_cache + ((uint64_t)(uint32_t)v_id[i] * block_bytes + at), v_id[i] != -1);
-      }
-    };
-    // Zeroes the tokens of unit bytes at or behind kv_hi (and in front of kv_lo).
-    auto clip = [&](uint4& x, int ti) {
-      const int a = kv_lo - ti, b = kv_hi - ti;
-      if (a <= 0 && b >= 16) return;
-      auto below = [](int n) { return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u); };
-      x.x &= below(b) & ~below(a);
-      x.y &= below(b - 4) & ~below(a - 4);
-      x.z &= below(b - 8) & ~below(a - 8);
-      x.w &= below(b - 12) & ~below(a - 12);
-    };
-    auto store = [&](const uint4 (&x)[8], uint32_t dst) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint4 a, b;
-        e4m3x16_to_f16(x[i], a, b);
-        st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
-        st_shared_v4(dst + (uint32_t)(2 * i + 1) * kExtColumn, b);
-      }
-    };
-    auto publish = [&](int b) {
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(b));
-    };
-    if (jmin < jmax) {
-      look_up(jmin);
-      load_k(jmin);
-      load_v(jmin);
-      if (jmin + 1 < jmax) look_up(jmin + 1);
-    }
-    int ks = 0, vs = 0;
-    uint32_t kr = 0, vr = 0;                                  // rounds of the rings
-    for (int j = jmin; j < jmax; ++j) {
-      const bool more = j + 1 < jmax;
-      if (kr > 0 && !warp_wait(kBarKFree + ks, (kr - 1) & 1)) break;
-      store(k, sm + kExtKOff + (uint32_t)ks * kExtOperand + (uint32_t)me * 16u);
-      if (more) load_k(j + 1);
-      publish(kBarKFull + ks);
-      if (++ks == kExtKStages) ks = 0, ++kr;
-      if (vr > 0 && !warp_wait(kBarVFree + vs, (vr - 1) & 1)) break;
-      if (j * kExtTile < kv_lo || (j + 1) * kExtTile > kv_hi) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i);
-      }
-      store(v, sm + kExtVOff + (uint32_t)vs * kExtOperand + (uint32_t)me * 16u);
-      if (more) load_v(j + 1);
-      publish(kBarVFull + vs);
-      if (++vs == kExtVStages) vs = 0, ++vr;
-      if (j + 2 < jmax) look_up(j + 2);
     }
   } else {
     regs_dec<kExtIssueRegs>();
-    // ------------------------------------------------ the products
     const int x = __shfl_sync(0xffffffffu, warp - 12, 0);    // uniform, for the compiler too
     if (x < 2) {
-      int j0, j1, step;
-      block_tiles(t, x, j0, j1, step);
+      // ---------------------------------------------- the products
       const uint32_t s_tm = tmem + (uint32_t)x * 128u, o_tm = s_tm + 256u;
-      const uint32_t qd = operand_desc_lo(sm + kExtQOff + (t.both ? 0u : (uint32_t)x * kExtOperand));
-      int prev = -1;          // tile (from jmin) whose P V is due
-      int made = 0;           // S products so far
-      bool ok = warp_wait(kBarQ, 0);
-      const int tiles = t.jmax - t.jmin;
+      uint32_t s_count = 0;     // S products so far: P's phases
+      uint32_t n0 = 0;          // tiles of earlier items: the rings' phases
+      uint32_t turn = 0;        // turns so far
+      bool ok = true;
+      ExtendItem t;
 #pragma unroll 1
-      for (int i = 0; ok && i <= tiles; ++i) {               // the last round: what is left
-        const int j = t.jmin + i;
-        const bool mine = i < tiles && j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0);
-        const bool due = prev >= 0 && (mine || j >= j1);
-        const int ks = i % kExtKStages, vs = prev % kExtVStages;
-        if (due) ok = warp_wait(kBarVFull + vs, (uint32_t)(prev / kExtVStages) & 1u);
-        if (ok && mine) ok = warp_wait(kBarKFull + ks, (uint32_t)(i / kExtKStages) & 1u);
-        // The blocks issue in turn. Left to themselves they fall into step:
-        // both wait for both products, then both are in their softmax.
-        const uint32_t p_phase = (uint32_t)(made - 1) & 1u;
-        const uint32_t vd = operand_desc_lo(sm + kExtVOff + (uint32_t)vs * kExtOperand);
-        if (ok && due && (ok = warp_wait(kBarP + 2 * x, p_phase))) {
+      for (int it = 0; ok && next_item(it, t); ++it) {
+        release_item(it);
+        int j0, j1, step;
+        block_tiles(t, x, j0, j1, step);
+        const uint32_t qd = operand_desc_lo(sm + kExtQOff + (t.both ? 0u : (uint32_t)x * kExtOperand));
+        int prev = -1;          // tile (from jmin) whose P V is due
+        bool started = false;   // O holds something
+        const int tiles = t.jmax - t.jmin;
+        ok = warp_wait(kBarQ + x, (uint32_t)it & 1u);
+        if (ok && t.both && x) ok = warp_wait(kBarQ, (uint32_t)it & 1u);
+#pragma unroll 1
+        for (int i = 0; ok && i <= tiles; ++i) {             // the last round: what is left
+          const int j = t.jmin + i;
+          const bool mine = i < tiles && j >= j0 && j < j1 && (step == 1 || ((j - j0) & 1) == 0);
+          const bool due = prev >= 0 && (mine || j >= j1);
+          const uint32_t n = n0 + (uint32_t)i, np = n0 + (uint32_t)prev;
+          const uint32_t ks = n % kExtKStages, vs = np % kExtVStages;
+          if (due) ok = warp_wait(kBarVFull + vs, (np / kExtVStages) & 1u);
+          if (ok && mine) ok = warp_wait(kBarKFull + ks, (n / kExtKStages) & 1u);
+          // The blocks issue in turn. Left to themselves they fall into step:
+          // both wait for both products, then both are in their softmax.
+          const bool turns = step == 1 && i < tiles;
+          if (ok && turns && (x || turn)) ok = warp_wait(kBarTurn + x, (x ? turn : turn - 1u) & 1u);
+          const uint32_t p_phase = (s_count - 1u) & 1u;
+          const uint32_t vd = operand_desc_lo(sm + kExtVOff + vs * kExtOperand);
+          if (ok && due && (ok = warp_wait(kBarP + 2 * x, p_phase))) {
+            tc_fence_after();
+            mma_half_ts(o_tm, s_tm, vd, started);
+          }
+          if (ok && due) ok = warp_wait(kBarP + 2 * x + 1, p_phase);
+          if (!ok) break;
           tc_fence_after();
-          mma_half_ts(o_tm, s_tm, vd, made > 1);
+          if (due) {
+            mma_half_ts(o_tm, s_tm + 32u, vd + 4u * kExtDescStep, true);
+            tc_commit(bar(kBarVFree + vs));
+            if (!mine) tc_commit(bar(kBarO + x));
+            started = true;
+            prev = -1;
+          }
+          if (mine) {
+            mma_tile_ss(s_tm, qd, operand_desc_lo(sm + kExtKOff + ks * kExtOperand));
+            tc_commit(bar(kBarS + x));
+            tc_commit(bar(kBarKFree + ks));
+            prev = i;
+            ++s_count;
+          }
+          if (turns) {
+            if (lane == 0) mbar_arrive(bar(kBarTurn + 1 - x));
+            ++turn;
+          }
+          if (!mine && i < tiles) {
+            // the other block's tile: a stage is free when both have let go of it
+            const uint32_t v2 = n % kExtVStages;
+            ok = warp_wait(kBarKFull + ks, (n / kExtKStages) & 1u);
+            if (ok && lane == 0) mbar_arrive(bar(kBarKFree + ks));
+            ok = ok && warp_wait(kBarVFull + v2, (n / kExtVStages) & 1u);
+            if (ok && lane == 0) mbar_arrive(bar(kBarVFree + v2));
+          }
         }
-        const bool turns = step == 1 && i < tiles;
-        if (ok && turns && (x || i)) ok = warp_wait(kBarTurn + x, (uint32_t)(x ? i : i - 1) & 1u);
-        if (ok && due) ok = warp_wait(kBarP + 2 * x + 1, p_phase);
+        n0 += (uint32_t)tiles;
+      }
+    } else if (x == 2) {
+      // ---------------------------------------------- the next items
+      const unsigned total = (unsigned)p.tiles * (unsigned)p.num_kv_heads * (unsigned)p.nsplit;
+      unsigned ticket = blockIdx.x;
+      auto take = [&]() {
+        if (p.queue) {
+          if (lane == 0) ticket = gridDim.x + atomicAdd(p.queue, 1u);
+          ticket = __shfl_sync(0xffffffffu, ticket, 0);
+        } else {
+          ticket += gridDim.x;
+        }
+      };
+      bool ok = true;
+      for (int it = 0; ok; ++it) {
+        // Taken late, so that no CTA sits on an item while others are idle.
+        if (it > 0 && !warp_wait(kBarAhead, (uint32_t)(it - 1) & 1u)) break;
+        if (it > 0) take();
+        ExtendItem t;
+        t.more = 0;
+        while (ticket < total) {
+          // heads, then splits, then tiles: CTAs that run together share
+          // tables; later tiles of a sequence see more tokens and go first
+#ifdef ORD
+          const unsigned sl = ticket % (unsigned)p.tiles;
+          const unsigned rest = ticket / (unsigned)p.tiles;
+          t.split = (int)(rest % (unsigned)p.nsplit);
+          t.kvh = (int)(rest / (unsigned)p.nsplit);
+          if (extend_item(p, p.tiles - 1 - (int)sl, t)) break;
+#else
+          t.kvh = (int)(ticket % (unsigned)p.num_kv_heads);
+          const unsigned rest = ticket / (unsigned)p.num_kv_heads;
+          t.split = (int)(rest % (unsigned)p.nsplit);
+          if (extend_item(p, p.tiles - 1 - (int)(rest / (unsigned)p.nsplit), t)) break;
+#endif
+          take();
+        }
+        const int slot = it % kExtSlots;
+        if (it >= kExtSlots) ok = warp_wait(kBarItemFree + slot, (uint32_t)(it / kExtSlots - 1) & 1u);
         if (!ok) break;
-        tc_fence_after();
-        if (due) {
-          mma_half_ts(o_tm, s_tm + 32u, vd + 4u * kExtDescStep, true);
-          tc_commit(bar(kBarVFree + vs));
-          if (!mine) tc_commit(bar(kBarO + x));
-          prev = -1;
+        if (lane == 0) {
+          *reinterpret_cast<ExtendItem*>(smem + kExtItemOff + slot * 64) = t;
+          mbar_arrive(bar(kBarItemFull + slot));
         }
-        if (mine) {
-          mma_tile_ss(s_tm, qd, operand_desc_lo(sm + kExtKOff + (uint32_t)ks * kExtOperand));
-          tc_commit(bar(kBarS + x));
-          tc_commit(bar(kBarKFree + ks));
-          prev = i;
-          ++made;
-        }
-        if (turns && lane == 0) mbar_arrive(bar(kBarTurn + 1 - x));
-        if (!mine && i < tiles) {
-          // the other block's tile: a stage is free when both have let go of it
-          const int v2 = i % kExtVStages;
-          ok = warp_wait(kBarKFull + ks, (uint32_t)(i / kExtKStages) & 1u);
-          if (ok && lane == 0) mbar_arrive(bar(kBarKFree + ks));
-          ok = ok && warp_wait(kBarVFull + v2, (uint32_t)(i / kExtVStages) & 1u);
-          if (ok && lane == 0) mbar_arrive(bar(kBarVFree + v2));
+        if (!t.more) break;
+      }
+      // the last CTA to stop taking items leaves the queue at zero
+      if (p.queue && lane == 0) {
+        __threadfence();
+        if (atomicAdd(p.queue + 1, 1u) == gridDim.x - 1) {
+          p.queue[0] = 0u;
+          p.queue[1] = 0u;
         }
       }
     }
@@ -761,7 +934,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
   __syncwarp();
   __syncthreads();
   if (warp == 12) {
-    if (abort_flag) {
+    if (*abort_flag) {
       // products still in flight end by themselves, within this time by far
       const unsigned long long t0 = globaltimer_ns();
       while (globaltimer_ns() - t0 < 100000ull) {}

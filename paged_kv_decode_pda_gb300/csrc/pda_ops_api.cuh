@@ -98,7 +98,8 @@ struct ExtendPlan {
   int tile_tokens;   // new tokens of a full tile (256 rows of g heads)
   int tiles;         // tile slots: room for every sequence's tiles, whatever the lengths
   int nsplit;
-  size_t bytes;      // of the split partials
+  int sms;
+  size_t bytes;      // of the work queue and the split partials
 };
 
 // The tiles, and how many splits of the KV range each gets: one, unless the
@@ -134,7 +135,9 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
   long long n = sms / ctas;
   n = n < kv_tiles / 2 ? n : kv_tiles / 2;
   pl->nsplit = n < 1 ? 1 : (int)n;
-  pl->bytes = pl->nsplit == 1 ? 0 : (size_t)num_tokens * num_heads * pl->nsplit * (kHeadDim + 2) * sizeof(float);
+  pl->sms = sms;
+  pl->bytes = kQueueBytes;
+  if (pl->nsplit > 1) pl->bytes += (size_t)num_tokens * num_heads * pl->nsplit * (kHeadDim + 2) * sizeof(float);
   return PDA_OK;
 }
 
@@ -144,12 +147,12 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
 // whose queue words have to stay as they are).
 size_t page_ws_bytes(long long num_blocks, long long num_rows, long long n) {
   const size_t NB = align256((size_t)num_blocks * 4);
-  return 256 + align256((size_t)num_rows * 4) + align256((size_t)n * 8) + 3 * NB;
+  return kQueueBytes + 256 + align256((size_t)num_rows * 4) + align256((size_t)n * 8) + 3 * NB;
 }
 
 pda::PageWs page_ws_layout(void* ptr, long long num_blocks, long long num_rows, long long n) {
   const size_t NB = align256((size_t)num_blocks * 4);
-  char* c = static_cast<char*>(ptr);
+  char* c = static_cast<char*>(ptr) + kQueueBytes;   // pda_extend's queue words stay as they are
   pda::PageWs w;
   w.head = reinterpret_cast<int32_t*>(c);
   c += 256;
@@ -168,7 +171,7 @@ pda::PageWs page_ws_layout(void* ptr, long long num_blocks, long long num_rows, 
 pda_status get_page_workspace(cudaStream_t stream, size_t bytes, void** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return PDA_ERR_CUDA;
-  return grow_workspace(g_ops_ws, dev, stream, bytes, 0, out);
+  return grow_workspace(g_ops_ws, dev, stream, bytes, kQueueBytes, out);
 }
 
 pda_status page_state(const pda_page_table* t, pda::PageState* st) {
@@ -426,9 +429,10 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
                                 max_num_blocks_per_seq, window, &pl);
     if (st != PDA_OK) return st;
     void* ws = nullptr;
-    st = grow_workspace(g_ops_ws, dev, stream, pl.bytes, 0, &ws);
+    st = grow_workspace(g_ops_ws, dev, stream, pl.bytes, kQueueBytes, &ws);
     if (st == PDA_ERR_WORKSPACE) {
-      // captured without pda_reserve_extend: one split needs no workspace
+      // captured without pda_reserve_extend: one split, and the items dealt
+      // out in turn, need no workspace
       pl.nsplit = 1;
       st = PDA_OK;
     }
@@ -436,12 +440,14 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
     p.tile_tokens = pl.tile_tokens;
     p.tiles = pl.tiles;
     p.nsplit = pl.nsplit;
+    p.queue = static_cast<unsigned*>(ws);
     if (pl.nsplit > 1) {
-      p.part_o = static_cast<float*>(ws);
+      p.part_o = reinterpret_cast<float*>(static_cast<char*>(ws) + kQueueBytes);
       p.part_ml = p.part_o + (size_t)num_tokens * num_heads * pl.nsplit * kHeadDim;
     }
-    const dim3 grid((unsigned)pl.tiles, (unsigned)num_kv_heads, (unsigned)pl.nsplit);
-    pda::pda_extend_kernel<<<grid, pda::kExtThreads, pda::kExtSmem, stream>>>(p);
+    const long long items = (long long)pl.tiles * num_kv_heads * pl.nsplit;
+    if (items > INT32_MAX / 2) return PDA_ERR_UNSUPPORTED;
+    pda::pda_extend_kernel<<<(unsigned)(items < pl.sms ? items : pl.sms), pda::kExtThreads, pda::kExtSmem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
     if (pl.nsplit == 1) return PDA_OK;
     pda::ExtendMergeParams m = {};
@@ -485,7 +491,7 @@ pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int n
     ExtendPlan pl;
     st = extend_plan(dev, num_tokens, num_seqs, num_heads, num_kv_heads, block_size, max_num_blocks_per_seq, 0, &pl);
     void* ws = nullptr;
-    return st != PDA_OK ? st : grow_workspace(g_ops_ws, dev, stream, pl.bytes, 0, &ws);
+    return st != PDA_OK ? st : grow_workspace(g_ops_ws, dev, stream, pl.bytes, kQueueBytes, &ws);
   });
 }
 
