@@ -18,7 +18,8 @@
 //                     registers, P written back over it
 //   warps 8-11        K and V: 16-byte loads through the block table, e4m3 ->
 //                     f16 in registers, stores in the matrix units' layout
-//   warps 12, 13      issue the products of block A, B (14 and 15 idle:
+//   warps 12, 13      issue the products of block A, B
+//   warp 14           takes and describes the next work item (15 idle:
 //                     registers are traded by groups of four warps)
 // Tensor memory (512 columns): S_A, S_B (128 each; P takes the first 64 of
 // its block's), O_A, O_B. Shared memory: Q 64 KiB, two K stages and three V
@@ -63,9 +64,12 @@ struct ExtendParams {
   int tile_tokens;              // tokens of a full tile: 256 / g
   int tiles;                    // tile slots
   int nsplit;                   // KV splits
+  const int2* order;            // (sequence, first token) of the tiles, longest first; nullptr: by slot
+  const int* order_count;       // tiles in it
   unsigned* queue;              // next work item, CTAs done (both left at zero); nullptr: items dealt out in turn
   float* part_o;                // [T][H][nsplit][128]   (nsplit > 1)
   float* part_ml;               // [T][H][nsplit][2]: reference (log2 units), l
+  uint32_t zero;                // 0 (see release_item)
 };
 
 constexpr int kExtRows = 128;                         // rows of a block
@@ -78,10 +82,9 @@ constexpr int kExtConvertRegs = 88;
 constexpr int kExtIssueRegs = 40;
 static_assert(256 * kExtSoftmaxRegs + 128 * kExtConvertRegs + 128 * kExtIssueRegs <= kExtThreads * kExtLaunchRegs,
               "the warps' registers come out of the CTA's own");
-constexpr int kExtKStages = 2;
-constexpr int kExtVStages = 3;
 constexpr uint32_t kExtOperand = 128u * 128u * 2u;    // one f16 operand tile: 32 KiB
-constexpr uint32_t kExtColumn = 128u * 16u;           // one 16-byte column of it
+constexpr uint32_t kExtColumn = 128u * 16u;           // one 16-byte column of an operand
+constexpr uint32_t kExtKStages = 2, kExtVStages = 3;
 constexpr uint32_t kExtQOff = 0;
 constexpr uint32_t kExtKOff = 2 * kExtOperand;
 constexpr uint32_t kExtVOff = kExtKOff + kExtKStages * kExtOperand;
@@ -92,11 +95,11 @@ enum : int {                                          // barriers (8 bytes each)
   kBarItemFull = 0,                                   // a work item described
   kBarItemFree = kBarItemFull + kExtSlots,            // read by the 14 warps that work on it
   kBarQ = kBarItemFree + kExtSlots,                   // queries of block A, B stored (4 warps)
-  kBarKFull = kBarQ + 2,
-  kBarKFree = kBarKFull + kExtKStages,
-  kBarVFull = kBarKFree + kExtKStages,
-  kBarVFree = kBarVFull + kExtVStages,
-  kBarS = kBarVFree + kExtVStages,                    // S of block A, B ready
+  kBarKFull = kBarQ + 2,                              // f16 tiles (4 warps), up to 2 stages of K, 3 of V
+  kBarKFree = kBarKFull + 2,                          // and let go of by both blocks
+  kBarVFull = kBarKFree + 2,
+  kBarVFree = kBarVFull + 3,
+  kBarS = kBarVFree + 3,                              // S of block A, B ready
   kBarP = kBarS + 2,                                  // P's halves, of block A, B ready (4 warps)
   kBarO = kBarP + 4,                                  // O of block A, B final
   kBarTurn = kBarO + 2,                               // block A's, B's turn to issue
@@ -297,10 +300,11 @@ struct __align__(16) ExtendItem {
 };
 static_assert(sizeof(ExtendItem) == 64, "one slot");
 
-// The tile of `slot`, found by the whole warp. Sequence s starts at slot
-// starts[s] / tile_tokens + s, which leaves each sequence room for its tiles
-// whatever the lengths are; the search probes 32 sequences at a time.
-__device__ __forceinline__ bool extend_item(const ExtendParams& p, int slot, ExtendItem& t) {
+// The sequence of a tile slot, and the slot's first token in it. Sequence s
+// starts at slot starts[s] / tile_tokens + s, which leaves each sequence room
+// for its tiles whatever the lengths are; `first` is past its rows where the
+// slot is spare. The whole warp searches, probing 32 sequences at a time.
+__device__ __forceinline__ int2 extend_slot(const ExtendParams& p, int slot) {
   const int lane = threadIdx.x & 31;
   const int base = __ldg(p.query_starts);
   auto first_slot = [&](int s) { return (__ldg(p.query_starts + s) - base) / p.tile_tokens + s; };
@@ -312,12 +316,16 @@ __device__ __forceinline__ bool extend_item(const ExtendParams& p, int slot, Ext
     s += k;
     n = min(step, n - k);
   }
-  const int raw = __ldg(p.query_starts + s);
-  const int start = max(0, min(raw, p.num_tokens));
+  return make_int2(s, (slot - first_slot(s)) * p.tile_tokens);
+}
+
+// Describes the tile of sequence s from token `first` on (t.kvh and t.split
+// are set); false where it has no rows.
+__device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int first, ExtendItem& t) {
+  const int start = max(0, min(__ldg(p.query_starts + s), p.num_tokens));
   const int end = max(start, min(__ldg(p.query_starts + s + 1), p.num_tokens));
   const int len0 = __ldg(p.seq_lens + s);
   const int n = end - start;
-  const int first = (slot - ((raw - base) / p.tile_tokens + s)) * p.tile_tokens;
   if (first < 0 || first >= n) return false;
   const int tokens = min(p.tile_tokens, n - first);
   const int len = (int)max(0ll, min((long long)len0, (long long)p.max_blocks * p.block_size));
@@ -373,8 +381,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kExtSlots; ++i) mbar_init(bar(kBarItemFull + i), 1), mbar_init(bar(kBarItemFree + i), 14);
-    for (int i = 0; i < kExtKStages; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
-    for (int i = 0; i < kExtVStages; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
+    for (int i = 0; i < 3; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kBarQ + x), 4);
       mbar_init(bar(kBarS + x), 1);
@@ -413,9 +421,13 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
                    : "=r"(dst[i].x), "=r"(dst[i].y), "=r"(dst[i].z), "=r"(dst[i].w)
                    : "r"(src + 16u * i));
   };
-  auto release_item = [&](int it) {
+  // Lets the slot go once the four loads have delivered: an arrival can
+  // overtake loads that still stand in the shared-memory queue, but not where
+  // its address depends on their results.
+  auto release_item = [&](int it, const ExtendItem& t) {
+    const uint32_t z = (uint32_t)(t.more | t.pos0 | t.j1a | t.split) & p.zero;
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kBarItemFree + it % kExtSlots));
+    if (lane == 0) mbar_arrive(bar(kBarItemFree + it % kExtSlots) + z);
   };
   // Item number it, or false at the end (or on abort).
   auto next_item = [&](int it, ExtendItem& t) -> bool {
@@ -506,6 +518,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       const bool any = j < j1;
       float m = -INFINITY, l = 0.f;
       bool first = true;
+      const bool idle = (row & ~31) >= t.rows;                // no row of the warp is live
 #pragma unroll 1
       for (; j < j1; j += step, first = false) {
         if (!warp_wait(kBarS + x, s_phase)) {
@@ -513,6 +526,11 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
           break;
         }
         s_phase ^= 1;
+        if (idle) {
+          // rows of P that are nobody's may hold anything: they reach their own rows of O alone
+          if (lane < 2) mbar_arrive(bar(kBarP + 2 * x + lane));
+          continue;
+        }
         tc_fence_after();
         const int t0 = j * kExtTile;
         uint32_t s[128];
@@ -590,13 +608,13 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       tc_fence_after();
       // read again rather than held in registers through the tiles
       read_item(it, t);
-      release_item(it);
+      release_item(it, t);
       const int row2 = t.both ? (tid & 127) : tid, tok2 = row2 / p.gqa;
       const bool live2 = row2 < t.rows;
       const int head2 = t.kvh * p.gqa + row2 - tok2 * p.gqa;
       const size_t orow2 = (size_t)(t.row0 + tok2) * p.num_heads + head2;
       const float mt = m == -INFINITY ? -INFINITY : m - kExtOffset;
-      float M = mt, L = l, fa = 1.f, fb = 0.f;                // factors of this block's O and the other's
+      float M = mt, den = l, fa = 1.f, fb = 0.f;                // factors of this block's O and the other's
       if (t.both) {
         // Both blocks hold the rows: they exchange (m, l), and each reads
         // half the columns of both O's.
@@ -608,18 +626,18 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         M = fmaxf(mt, o.x);
         fa = mt == -INFINITY ? 0.f : fast_exp2(mt - M);
         fb = o.x == -INFINITY ? 0.f : fast_exp2(o.x - M);
-        L = l * fa + o.y * fb;
+        den = l * fa + o.y * fb;
         tc_fence_after();
       }
       if (mt == -INFINITY) fa = 0.f;
       const size_t prow = orow2 * p.nsplit + t.split;
       if (p.nsplit == 1) {
         const float zs = p.sinks && live2 ? __ldg(p.sinks + head2) * 1.4426950408889634f : -INFINITY;
-        const float r = live2 && t.pos0 + tok2 >= 0 ? finish(1.f, L, M, zs, p.v_scale) : 0.f;
+        const float r = live2 && t.pos0 + tok2 >= 0 ? finish(1.f, den, M, zs, p.v_scale) : 0.f;
         fa *= r;
         fb *= r;
       } else if (live2 && (x == 0 || !t.both)) {
-        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, L);
+        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
       }
       const int i0 = t.both ? 4 * x : 0, i1 = t.both ? 4 * x + 4 : 8;
 #pragma unroll 1
@@ -696,47 +714,67 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     const int me = tid & 127;                                 // token of the tile (K), dim (V)
     const uint32_t bs = (uint32_t)p.block_size;
     const uint32_t per_page = bs / 16u;                       // 16-token units of a page
+    // Zeroes the tokens of 16 in front of kv_lo, at or behind kv_hi.
+    auto clip = [&](uint4& x, int ti, int kv_lo, int kv_hi) {
+      const int a = kv_lo - ti, b = kv_hi - ti;
+      if (a <= 0 && b >= 16) return;
+      auto below = [](int n) { return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u); };
+      x.x &= below(b) & ~below(a);
+      x.y &= below(b - 4) & ~below(a - 4);
+      x.z &= below(b - 8) & ~below(a - 8);
+      x.w &= below(b - 12) & ~below(a - 12);
+    };
+    auto store = [&](const uint4 (&x)[8], uint32_t dst) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint4 a, b;
+        e4m3x16_to_f16(x[i], a, b);
+        st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
+        st_shared_v4(dst + (uint32_t)(2 * i + 1) * kExtColumn, b);
+      }
+    };
+    auto signal = [&](int b) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    bool ok = true;
+    ExtendItem t;
+    // 16-byte loads through the block table, a tile ahead: K: the 8 chunks
+    // of 16 dims of a token; V: the 8 units of 16 tokens of a dim. What no
+    // row attends to is not read: zeros stand in (a masked weight of 0
+    // times a NaN would be NaN). The block ids are looked up one more tile
+    // ahead, by every thread for itself: handing them round with shuffles
+    // would wait behind the stores, in whose queue shuffles stand.
     const uint32_t magic = per_page == 1 ? 0u : 0xFFFFFFFFu / per_page + 1u;
     auto page_of = [&](uint32_t unit) { return per_page == 1 ? unit : __umulhi(unit, magic); };
     const uint32_t block_bytes = (uint32_t)kHeadDim * bs * (uint32_t)p.num_kv_heads;   // < 2^31: bs <= 128, 65535 heads
     const uint32_t unit_bytes = p.v_shuffled ? kHeadDim * 16u : 16u;   // V: from a page's unit to the next
-    uint32_t ks = 0, vs = 0, kr = 0, vr = 0;                  // stages, and rounds of the rings
-    bool ok = true;
-    ExtendItem t;
+    const bool check = p.block_limit != 0u;
+    uint32_t n = 0;                                         // tiles so far
+    uint4 k[8], v[8];
+    int k_id = -1, v_id[8];
 #pragma unroll 1
     for (int it = 0; ok && next_item(it, t); ++it) {
-      release_item(it);
+      release_item(it, t);
       const int kv_lo = t.kv_lo, kv_hi = t.kv_hi, jmin = t.jmin, jmax = t.jmax;
       const int near = max(jmin, jmax - kExtAhead);
-      if (jmin == jmax && lane == 0) mbar_arrive(bar(kBarAhead));
       const int32_t* table = p.block_tables + (size_t)t.seq * p.max_blocks;
       const uint8_t* k_cache = p.k_cache + (size_t)t.kvh * kHeadDim * bs;
       const uint8_t* v_cache = p.v_cache + (size_t)t.kvh * kHeadDim * bs + (uint32_t)me * (p.v_shuffled ? 16u : bs);
-      // K: the 8 chunks of 16 dims of this thread's token. V: the tile's 8
-      // units of 16 tokens of this thread's dim. What no row attends to is not
-      // read: zeros stand in (a masked weight of 0 times a NaN would be NaN).
-      // The block ids are looked up a tile ahead, by every thread for itself:
-      // handing them round with shuffles would wait behind the stores to shared
-      // memory, in whose queue shuffles stand.
-      uint4 k[8], v[8];
-      int k_id, v_id[8];
-      auto look_up = [&](int j) {
-        const int t0 = j * kExtTile;
-        k_id = t0 + me >= kv_lo && t0 + me < kv_hi ? __ldg(table + page_of((uint32_t)(t0 + me) >> 4)) : -1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int tk = t0 + 16 * i;
-          v_id[i] = tk + 16 > kv_lo && tk < kv_hi ? __ldg(table + page_of((uint32_t)tk >> 4)) : -1;
-        }
+      auto id_of = [&](int tk, int span) {
+        return tk + span > kv_lo && tk < kv_hi ? __ldg(table + page_of((uint32_t)tk >> 4)) : -1;
       };
-      const bool check = p.block_limit != 0u;
+      auto look_up_k = [&](int j) { k_id = id_of(j * kExtTile + me, 1); };
+      auto look_up_v = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v_id[i] = id_of(j * kExtTile + 16 * i, 16);
+      };
       auto load_k = [&](int j) {
         const uint32_t tk = (uint32_t)(j * kExtTile + me);
         if (check && k_id != -1) k_id = checked_block(k_id, p.block_limit);
-        const bool in = k_id != -1;
-        const uint8_t* src = k_cache + (in ? (uint64_t)(uint32_t)k_id * block_bytes + (tk - page_of(tk >> 4) * bs) * 16u : 0);
+        const uint8_t* src = k_cache + ((uint64_t)(uint32_t)k_id * block_bytes + (tk - page_of(tk >> 4) * bs) * 16u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) k[i] = ld_nc_v4_if(src + i * bs * 16u, in);
+        for (int i = 0; i < 8; ++i) k[i] = ld_nc_v4_if(src + i * bs * 16u, k_id != -1);
       };
       auto load_v = [&](int j) {
         if (check) {
@@ -747,60 +785,49 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t unit = (uint32_t)(j * (kExtTile / 16) + i);
-          const uint32_t at = (unit - page_of(unit) * per_page) * unit_bytes;
-          v[i] = ld_nc_v4_if(v_cache + ((uint64_t)(uint32_t)v_id[i] * block_bytes + at), v_id[i] != -1);
+          v[i] = ld_nc_v4_if(v_cache + ((uint64_t)(uint32_t)v_id[i] * block_bytes +
+                                        (unit - page_of(unit) * per_page) * unit_bytes),
+                             v_id[i] != -1);
         }
-      };
-      // Zeroes the tokens of unit bytes at or behind kv_hi (and in front of kv_lo).
-      auto clip = [&](uint4& x, int ti) {
-        const int a = kv_lo - ti, b = kv_hi - ti;
-        if (a <= 0 && b >= 16) return;
-        auto below = [](int n) { return n >= 4 ? 0xFFFFFFFFu : (n <= 0 ? 0u : (1u << (8 * n)) - 1u); };
-        x.x &= below(b) & ~below(a);
-        x.y &= below(b - 4) & ~below(a - 4);
-        x.z &= below(b - 8) & ~below(a - 8);
-        x.w &= below(b - 12) & ~below(a - 12);
-      };
-      auto store = [&](const uint4 (&x)[8], uint32_t dst) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 a, b;
-          e4m3x16_to_f16(x[i], a, b);
-          st_shared_v4(dst + (uint32_t)(2 * i) * kExtColumn, a);
-          st_shared_v4(dst + (uint32_t)(2 * i + 1) * kExtColumn, b);
-        }
-      };
-      auto publish = [&](int b) {
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(b));
       };
       if (jmin < jmax) {
-        look_up(jmin);
+        look_up_k(jmin);
+        look_up_v(jmin);
         load_k(jmin);
         load_v(jmin);
-        if (jmin + 1 < jmax) look_up(jmin + 1);
+        if (jmin + 1 < jmax) {
+          look_up_k(jmin + 1);
+          look_up_v(jmin + 1);
+        }
+      } else {
+        signal(kBarAhead);
       }
-      for (int j = jmin; ok && j < jmax; ++j) {
+#pragma unroll 1
+      for (int j = jmin; j < jmax; ++j, ++n) {
+        if (j == near) signal(kBarAhead);
         const bool more = j + 1 < jmax;
-        if (j == near && lane == 0) mbar_arrive(bar(kBarAhead));
-        if (kr > 0) ok = warp_wait(kBarKFree + ks, (kr - 1) & 1);
+        uint32_t st = n % kExtKStages;
+        if (n >= kExtKStages) ok = warp_wait(kBarKFree + (int)st, (n / kExtKStages - 1u) & 1u);
         if (!ok) break;
-        store(k, sm + kExtKOff + (uint32_t)ks * kExtOperand + (uint32_t)me * 16u);
+        store(k, sm + kExtKOff + st * kExtOperand + (uint32_t)me * 16u);
         if (more) load_k(j + 1);
-        publish(kBarKFull + ks);
-        if (++ks == kExtKStages) ks = 0, ++kr;
-        if (vr > 0) ok = warp_wait(kBarVFree + vs, (vr - 1) & 1);
+        fence_async_smem();
+        signal(kBarKFull + (int)st);
+        st = n % kExtVStages;
+        if (n >= kExtVStages) ok = warp_wait(kBarVFree + (int)st, (n / kExtVStages - 1u) & 1u);
         if (!ok) break;
         if (j * kExtTile < kv_lo || (j + 1) * kExtTile > kv_hi) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i);
+          for (int i = 0; i < 8; ++i) clip(v[i], j * kExtTile + 16 * i, kv_lo, kv_hi);
         }
-        store(v, sm + kExtVOff + (uint32_t)vs * kExtOperand + (uint32_t)me * 16u);
+        store(v, sm + kExtVOff + st * kExtOperand + (uint32_t)me * 16u);
         if (more) load_v(j + 1);
-        publish(kBarVFull + vs);
-        if (++vs == kExtVStages) vs = 0, ++vr;
-        if (j + 2 < jmax) look_up(j + 2);
+        fence_async_smem();
+        signal(kBarVFull + (int)st);
+        if (j + 2 < jmax) {
+          look_up_k(j + 2);
+          look_up_v(j + 2);
+        }
       }
     }
   } else {
@@ -816,7 +843,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       ExtendItem t;
 #pragma unroll 1
       for (int it = 0; ok && next_item(it, t); ++it) {
-        release_item(it);
+        release_item(it, t);
         int j0, j1, step;
         block_tiles(t, x, j0, j1, step);
         const uint32_t qd = operand_desc_lo(sm + kExtQOff + (t.both ? 0u : (uint32_t)x * kExtOperand));
@@ -878,7 +905,11 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       }
     } else if (x == 2) {
       // ---------------------------------------------- the next items
-      const unsigned total = (unsigned)p.tiles * (unsigned)p.num_kv_heads * (unsigned)p.nsplit;
+      // The order comes from the kernel in front, which this one does not
+      // wait for as a whole.
+      if (p.order) grid_dependency_wait();
+      const unsigned tiles = p.order ? (unsigned)__ldcg(p.order_count) : (unsigned)p.tiles;
+      const unsigned total = tiles * (unsigned)p.num_kv_heads * (unsigned)p.nsplit;
       unsigned ticket = blockIdx.x;
       auto take = [&]() {
         if (p.queue) {
@@ -897,19 +928,14 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         t.more = 0;
         while (ticket < total) {
           // heads, then splits, then tiles: CTAs that run together share
-          // tables; later tiles of a sequence see more tokens and go first
-#ifdef ORD
-          const unsigned sl = ticket % (unsigned)p.tiles;
-          const unsigned rest = ticket / (unsigned)p.tiles;
-          t.split = (int)(rest % (unsigned)p.nsplit);
-          t.kvh = (int)(rest / (unsigned)p.nsplit);
-          if (extend_item(p, p.tiles - 1 - (int)sl, t)) break;
-#else
+          // tables; without an order, later tiles of a sequence (which see
+          // more tokens) go first
           t.kvh = (int)(ticket % (unsigned)p.num_kv_heads);
           const unsigned rest = ticket / (unsigned)p.num_kv_heads;
           t.split = (int)(rest % (unsigned)p.nsplit);
-          if (extend_item(p, p.tiles - 1 - (int)(rest / (unsigned)p.nsplit), t)) break;
-#endif
+          const int i = (int)(rest / (unsigned)p.nsplit);
+          const int2 at = p.order ? __ldcg(p.order + i) : extend_slot(p, p.tiles - 1 - i);
+          if (extend_item(p, at.x, at.y, t)) break;
           take();
         }
         const int slot = it % kExtSlots;
@@ -941,6 +967,75 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     }
     tc_fence_after();
     tmem_free(tmem, 512);
+  }
+}
+
+// pda_extend_order_kernel: the tiles of a call with more work items than CTAs,
+// longest KV range first (a counting sort by 128-token tiles, one block), so
+// that the items that come last are short. GB300, us without and with it: a mixed
+// batch of 24 sequences 167 -> 160; 2 x 2048 tokens at 8192, whose 512 items are
+// of near one size, 365 -> 372.
+constexpr int kExtOrderThreads = 1024;
+constexpr int kExtMaxOrdered = 16384;                 // tile slots
+__global__ void __launch_bounds__(kExtOrderThreads) pda_extend_order_kernel(const ExtendParams p, int2* order,
+                                                                            int* count) {
+  __shared__ int hist[kExtOrderThreads], sums[32];
+  grid_dependents_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  hist[tid] = 0;
+  __syncthreads();
+  // KV tiles of a slot (-1: spare), 1023 at most; the thread's own search
+  auto size_of = [&](int slot, int2& at) -> int {
+    const int base = __ldg(p.query_starts);
+    int lo = 0, hi = p.num_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if ((__ldg(p.query_starts + mid) - base) / p.tile_tokens + mid <= slot)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    at = make_int2(lo, (slot - ((__ldg(p.query_starts + lo) - base) / p.tile_tokens + lo)) * p.tile_tokens);
+    ExtendItem t;
+    t.kvh = t.split = 0;
+    ExtendParams q = p;
+    q.nsplit = 1;
+    if (!extend_item(q, at.x, at.y, t)) return -1;
+    return min(t.jmax - t.jmin, kExtOrderThreads - 1);
+  };
+  for (int slot = tid; slot < p.tiles; slot += kExtOrderThreads) {
+    int2 at;
+    const int n = size_of(slot, at);
+    if (n >= 0) atomicAdd(&hist[kExtOrderThreads - 1 - n], 1);
+  }
+  __syncthreads();
+  // exclusive prefix over the sizes, largest first
+  const int mine = hist[tid];
+  int x = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int v = sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += y;
+    }
+    sums[lane] = v;
+  }
+  __syncthreads();
+  hist[tid] = (warp ? sums[warp - 1] : 0) + x - mine;
+  if (tid == 0) *count = sums[31];
+  __syncthreads();
+  for (int slot = tid; slot < p.tiles; slot += kExtOrderThreads) {
+    int2 at;
+    const int n = size_of(slot, at);
+    if (n >= 0) order[atomicAdd(&hist[kExtOrderThreads - 1 - n], 1)] = at;
   }
 }
 

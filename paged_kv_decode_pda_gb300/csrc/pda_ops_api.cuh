@@ -99,7 +99,8 @@ struct ExtendPlan {
   int tiles;         // tile slots: room for every sequence's tiles, whatever the lengths
   int nsplit;
   int sms;
-  size_t bytes;      // of the work queue and the split partials
+  bool ordered;      // more items than SMs: longest first
+  size_t bytes;      // of the work queue, and the order or the split partials
 };
 
 // The tiles, and how many splits of the KV range each gets: one, unless the
@@ -118,8 +119,9 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
       cudaFuncAttributes fa;
       if (cudaFuncGetAttributes(&fa, pda::pda_extend_kernel) != cudaSuccess || fa.numRegs != pda::kExtLaunchRegs ||
           cudaFuncSetAttribute(pda::pda_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)pda::kExtSmem) != cudaSuccess ||
-          cudaDeviceGetAttribute(&di.extend_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+                               (int)pda::kExtSmem) != cudaSuccess)
+        return PDA_ERR_CUDA;
+      if (cudaDeviceGetAttribute(&di.extend_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return PDA_ERR_CUDA;
       di.extend_set = true;
     }
@@ -136,7 +138,8 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
   n = n < kv_tiles / 2 ? n : kv_tiles / 2;
   pl->nsplit = n < 1 ? 1 : (int)n;
   pl->sms = sms;
-  pl->bytes = kQueueBytes;
+  pl->ordered = ctas > sms && pl->tiles <= pda::kExtMaxOrdered;   // then there is one split
+  pl->bytes = kQueueBytes + (pl->ordered ? (size_t)pl->tiles * sizeof(int2) : 0);
   if (pl->nsplit > 1) pl->bytes += (size_t)num_tokens * num_heads * pl->nsplit * (kHeadDim + 2) * sizeof(float);
   return PDA_OK;
 }
@@ -447,8 +450,25 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
     }
     const long long items = (long long)pl.tiles * num_kv_heads * pl.nsplit;
     if (items > INT32_MAX / 2) return PDA_ERR_UNSUPPORTED;
-    pda::pda_extend_kernel<<<(unsigned)(items < pl.sms ? items : pl.sms), pda::kExtThreads, pda::kExtSmem, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(items < pl.sms ? items : pl.sms));
+    lc.blockDim = dim3(pda::kExtThreads);
+    lc.dynamicSmemBytes = pda::kExtSmem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    if (pl.ordered && ws) {
+      int* count = reinterpret_cast<int*>(p.queue + 2);
+      int2* order = reinterpret_cast<int2*>(static_cast<char*>(ws) + kQueueBytes);
+      pda::pda_extend_order_kernel<<<1, pda::kExtOrderThreads, 0, stream>>>(p, order, count);
+      if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+      p.order = order;
+      p.order_count = count;
+      lc.attrs = attr;
+      lc.numAttrs = 1;
+    }
+    if (cudaLaunchKernelEx(&lc, pda::pda_extend_kernel, p) != cudaSuccess) return PDA_ERR_CUDA;
     if (pl.nsplit == 1) return PDA_OK;
     pda::ExtendMergeParams m = {};
     m.out = out;
@@ -463,14 +483,10 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
     m.sinks = sinks;
     m.out_fp8 = p.out_fp8;
     m.out_scale = output_scale;
-    cudaLaunchConfig_t lc = {};
     const long long rows = (long long)num_tokens * num_heads;
     lc.gridDim = dim3((unsigned)((rows + pda::kMergeRowsPerBlock - 1) / pda::kMergeRowsPerBlock));
     lc.blockDim = dim3(kHeadDim);
-    lc.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.dynamicSmemBytes = 0;
     lc.attrs = attr;
     lc.numAttrs = 1;
     return cudaLaunchKernelEx(&lc, pda::pda_extend_merge_kernel, m) == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
