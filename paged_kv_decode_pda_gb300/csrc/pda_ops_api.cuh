@@ -75,14 +75,23 @@ pda_status rope_launch(pda::RopeParams& p, bool vec, cudaStream_t stream) {
     pda::pda_rope_any_kernel<kCache><<<(unsigned)blocks, pda::kRopeThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
   }
-  p.groups = kCache ? p.num_kv_heads : (p.num_heads + p.num_kv_heads + 7) / 8;
-  // Tokens per CTA: 16 share a table and store whole V rows; a step's few
-  // tokens go one to a CTA, which spreads them over the SMs.
-  const long long ctas16 = (T + 15) / 16 * p.groups;
-  if (ctas16 >= 152 * 4) {
-    const dim3 grid((unsigned)((T + 15) / 16), (unsigned)p.groups);
+  // Heads of a CTA: with the cache a kv head's; else as many as leave about a
+  // wave (every CTA makes its tokens' angles anew; 4096 tokens of 40/8 heads:
+  // 25.4 us against 27.1 with twice the CTAs).
+  const int heads = p.num_heads + p.num_kv_heads;
+  const long long tiles16 = (T + 15) / 16;
+  long long groups = kCache ? p.num_kv_heads : (608 + tiles16 - 1) / tiles16;
+  if (!kCache && groups > (heads + 7) / 8) groups = (heads + 7) / 8;
+  p.groups = (int)groups;
+  // Tokens per CTA: 16 store whole V rows; a step's fewer tokens go 4 or one to
+  // a CTA, which spreads them over the SMs (GB300, us with 4 / one a CTA: 256
+  // tokens of 40/8 heads 4.5 / 6.0, with the cache 32/8 heads 8.0 / 9.4; 64
+  // tokens with the cache 6.3 / 5.6).
+  const long long ctas16 = tiles16 * groups;
+  if (ctas16 >= 608) {
+    const dim3 grid((unsigned)tiles16, (unsigned)p.groups);
     pda::pda_rope_kernel<16, kCache><<<grid, pda::kRopeThreads, 0, stream>>>(p);
-  } else if (ctas16 * 4 >= 152 * 4) {
+  } else if (ctas16 >= 64) {
     const dim3 grid((unsigned)((T + 3) / 4), (unsigned)p.groups);
     pda::pda_rope_kernel<4, kCache><<<grid, pda::kRopeThreads, 0, stream>>>(p);
   } else {

@@ -13,10 +13,13 @@
 // frequency's own 64-bit rounding, at position 1 and at position 10^6 alike.
 //
 // Bound: bytes (6 flops per 4 bytes moved). One CTA holds kTok tokens and one
-// group of heads: it computes the (cos, sin) table of its tokens once into
-// shared memory and rotates every head of the group with it, so the sincospi
-// work is shared by g + 1 heads; 16-byte loads of a batch of heads are issued
-// before the table is made.
+// group of heads: it computes the (cos, sin) table of its tokens once and
+// rotates every head of the group with it, each thread keeping its token's
+// eight pairs in registers; the first loads are issued before the table is
+// made. What counts then is how many CTAs fit an SM: 64 and 72 registers a
+// thread (8 and 7 CTAs; two heads in flight per thread) measured 75 us for
+// 16,384 tokens of 40/8 heads (5.4 TB/s) and 71 us with the cache for 8192 of
+// 64/8 (4.5 TB/s), against 87 and 79 with 92 to 96 registers and four heads.
 #pragma once
 
 #include "pda_kernels.cuh"
@@ -70,8 +73,9 @@ __device__ __forceinline__ void rope_item_dims(int j, int pairs, bool interleave
   }
 }
 
-// Rotates item j in fp32: r[0..7] vector a's dims, r[8..15] vector b's.
-__device__ __forceinline__ void rope_rotate(const RopeItem& x, int j, int pairs, bool interleaved, const float2* cs,
+// Rotates item j in fp32: r[0..7] vector a's dims, r[8..15] vector b's. t:
+// (cos, sin) of its pairs, two to a float4.
+__device__ __forceinline__ void rope_rotate(const RopeItem& x, int j, int pairs, bool interleaved, const float4 (&t)[4],
                                             float (&r)[16]) {
   const uint32_t wa[4] = {x.a.x, x.a.y, x.a.z, x.a.w}, wb[4] = {x.b.x, x.b.y, x.b.z, x.b.w};
 #pragma unroll
@@ -82,7 +86,6 @@ __device__ __forceinline__ void rope_rotate(const RopeItem& x, int j, int pairs,
     r[8 + 2 * i + 1] = bf16hi_f32(wb[i]);
   }
   if (j >= pairs / 8) return;
-  const float4* t = reinterpret_cast<const float4*>(cs + 8 * j);   // (cos, sin) of two pairs
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 c = t[i];
@@ -111,7 +114,9 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* r) {
   return make_uint4(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]), pack_bf16x2(r[4], r[5]),
                     pack_bf16x2(r[6], r[7]));
 }
-// Eight e4m3 codes of r / scale (the IEEE binary32 quotient, as the cache writers do).
+// Eight e4m3 codes of r / scale (the IEEE binary32 quotient, as the cache
+// writers do; a product with 1 / scale and the quotient only near the borders
+// between codes was slower: 78 against 72 us for 8192 tokens of 64/8 heads).
 __device__ __forceinline__ uint2 quantize8(const float* r, float scale) {
   uint32_t q[4];
 #pragma unroll
@@ -122,10 +127,12 @@ __device__ __forceinline__ uint2 quantize8(const float* r, float scale) {
 // kTok tokens x one head group per 128-thread CTA. 8 threads hold one head
 // of one token, so 16 / kTok heads go side by side.
 template <int kTok, bool kCache>
-__global__ void __launch_bounds__(kRopeThreads) pda_rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, kCache ? 7 : 8) pda_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kSide = 16 / kTok;     // heads side by side
-  constexpr int kBatch = 4;            // heads in flight per thread
-  __shared__ __align__(16) float2 cs[kTok][kRopeMaxPairs + 2];   // rows padded: 8 tokens' rows on different banks
+  constexpr int kBatch = 2;            // heads in flight per thread
+  // (cos, sin) of a token's pairs: pairs 8j + 2i, 8j + 2i + 1 are entry 8i + j,
+  // so that the 8 threads of a token read entry i of each without conflicts
+  __shared__ float4 cs[kTok][kRopeMaxPairs / 2];
   __shared__ __align__(16) uint8_t kt[kCache ? kTok : 1][kHeadDim];
   __shared__ __align__(16) uint8_t vt[kCache ? kTok : 1][kHeadDim];
   __shared__ long long slots[kTok];
@@ -160,22 +167,14 @@ __global__ void __launch_bounds__(kRopeThreads) pda_rope_kernel(const __grid_con
     }
   };
   load(0);
-  uint4 va = make_uint4(0, 0, 0, 0), vb = va;
   if constexpr (kCache) {
-    if (in && side == 0) {
-      const uint4* s = reinterpret_cast<const uint4*>(p.v + t * p.v_tok + (long long)y * p.v_head + 16 * j);
-      va = s[0];
-      vb = s[1];
-      if (j == 0) {
-        long long slot = __ldg(p.slot_mapping + t);
-        if (slot >= p.num_slots) {
-          atomicOr(&g_status, kStatusBadSlot);
-          slot = -1;
-        }
-        slots[tl] = slot;
+    if (side == 0 && j == 0) {
+      long long slot = in ? __ldg(p.slot_mapping + t) : -1;
+      if (slot >= p.num_slots) {
+        atomicOr(&g_status, kStatusBadSlot);
+        slot = -1;
       }
-    } else if (side == 0 && j == 0) {
-      slots[tl] = -1;
+      slots[tl] = slot;
     }
   }
   // Lanes run over tokens first: the 64-bit frequencies sit in constant
@@ -188,10 +187,15 @@ __global__ void __launch_bounds__(kRopeThreads) pda_rope_kernel(const __grid_con
       const int frac = (int)(uint32_t)((turn + 0x80000000ull) >> 32);
       float sn, cn;
       sincospif((float)frac * 4.656612873077393e-10f, &sn, &cn);   // 2^-31 half turns
-      cs[tt][pr] = make_float2(cn * p.magnitude, sn * p.magnitude);
+      reinterpret_cast<float2*>(&cs[tt][8 * ((pr >> 1) & 3) + (pr >> 3)])[pr & 1] =
+          make_float2(cn * p.magnitude, sn * p.magnitude);
     }
   }
   __syncthreads();
+  // a thread stays with its token and pairs through all heads
+  float4 mine[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mine[i] = cs[tl][8 * i + j];
 
   for (int h0 = 0; h0 < nh; h0 += kBatch * kSide) {
     if (h0) load(h0);
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kRopeThreads) pda_rope_kernel(const __grid_con
       const int h = h0 + u * kSide + side;
       if (!in || h >= nh) continue;
       float r[16];
-      rope_rotate(x[u], j, p.pairs, il, cs[tl], r);
+      rope_rotate(x[u], j, p.pairs, il, mine, r);
       if (kCache && h >= nq) {
         *reinterpret_cast<uint2*>(&kt[kCache ? tl : 0][da]) = quantize8(r, p.k_scale);
         *reinterpret_cast<uint2*>(&kt[kCache ? tl : 0][db]) = quantize8(r + 8, p.k_scale);
@@ -213,7 +217,10 @@ __global__ void __launch_bounds__(kRopeThreads) pda_rope_kernel(const __grid_con
     }
   }
   if constexpr (kCache) {
+    // V comes last: held through the heads, its registers cost a third of the CTAs
     if (in && side == 0) {
+      const uint4* s = reinterpret_cast<const uint4*>(p.v + t * p.v_tok + (long long)y * p.v_head + 16 * j);
+      const uint4 va = s[0], vb = s[1];
       const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
       float r[16];
 #pragma unroll
