@@ -742,14 +742,12 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     // 16-byte loads through the block table, a tile ahead: K: the 8 chunks
     // of 16 dims of a token; V: the 8 units of 16 tokens of a dim. What no
     // row attends to is not read: zeros stand in (a masked weight of 0
-    // times a NaN would be NaN). The block ids are looked up one more tile
-    // ahead, by every thread for itself: handing them round with shuffles
-    // would wait behind the stores, in whose queue shuffles stand.
+    // times a NaN would be NaN).
     const uint32_t magic = per_page == 1 ? 0u : 0xFFFFFFFFu / per_page + 1u;
     auto page_of = [&](uint32_t unit) { return per_page == 1 ? unit : __umulhi(unit, magic); };
     const uint32_t block_bytes = (uint32_t)kHeadDim * bs * (uint32_t)p.num_kv_heads;   // < 2^31: bs <= 128, 65535 heads
     const uint32_t unit_bytes = p.v_shuffled ? kHeadDim * 16u : 16u;   // V: from a page's unit to the next
-    const bool check = p.block_limit != 0u;
+    auto checked = [&](int id) { return p.block_limit ? checked_block(id, p.block_limit) : id; };
     uint32_t n = 0;                                         // tiles so far
     uint4 k[8], v[8];
     int k_id = -1, v_id[8];
@@ -761,27 +759,29 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       const int32_t* table = p.block_tables + (size_t)t.seq * p.max_blocks;
       const uint8_t* k_cache = p.k_cache + (size_t)t.kvh * kHeadDim * bs;
       const uint8_t* v_cache = p.v_cache + (size_t)t.kvh * kHeadDim * bs + (uint32_t)me * (p.v_shuffled ? 16u : bs);
-      auto id_of = [&](int tk, int span) {
-        return tk + span > kv_lo && tk < kv_hi ? __ldg(table + page_of((uint32_t)tk >> 4)) : -1;
+      // Block ids, two tiles ahead: lane i mod 8 has unit i's page. They are
+      // handed round (K: the unit of the thread's token; V: all) in front of a
+      // tile's stores: shuffles stand in the shared-memory queue too, and
+      // behind the stores they would wait for all of them. (A load of every id
+      // by every thread took 400 to 1400 cycles a tile to issue.)
+      auto look_up = [&](int j) -> int {
+        const int tk = j * kExtTile + 16 * (lane & 7);
+        return tk + 16 > kv_lo && tk < kv_hi ? checked(__ldg(table + page_of((uint32_t)tk >> 4))) : -1;
       };
-      auto look_up_k = [&](int j) { k_id = id_of(j * kExtTile + me, 1); };
-      auto look_up_v = [&](int j) {
+      auto hand_round = [&](int ids, int j) {
+        const int tk = j * kExtTile + me;
+        k_id = __shfl_sync(0xffffffffu, ids, me >> 4);
+        if (tk < kv_lo || tk >= kv_hi) k_id = -1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v_id[i] = id_of(j * kExtTile + 16 * i, 16);
+        for (int i = 0; i < 8; ++i) v_id[i] = __shfl_sync(0xffffffffu, ids, i);
       };
       auto load_k = [&](int j) {
         const uint32_t tk = (uint32_t)(j * kExtTile + me);
-        if (check && k_id != -1) k_id = checked_block(k_id, p.block_limit);
         const uint8_t* src = k_cache + ((uint64_t)(uint32_t)k_id * block_bytes + (tk - page_of(tk >> 4) * bs) * 16u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) k[i] = ld_nc_v4_if(src + i * bs * 16u, k_id != -1);
       };
       auto load_v = [&](int j) {
-        if (check) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (v_id[i] != -1) v_id[i] = checked_block(v_id[i], p.block_limit);
-        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t unit = (uint32_t)(j * (kExtTile / 16) + i);
@@ -790,15 +790,12 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
                              v_id[i] != -1);
         }
       };
+      int ids = -1;                                           // of tile j + 1
       if (jmin < jmax) {
-        look_up_k(jmin);
-        look_up_v(jmin);
+        hand_round(look_up(jmin), jmin);
         load_k(jmin);
         load_v(jmin);
-        if (jmin + 1 < jmax) {
-          look_up_k(jmin + 1);
-          look_up_v(jmin + 1);
-        }
+        if (jmin + 1 < jmax) ids = look_up(jmin + 1);
       } else {
         signal(kBarAhead);
       }
@@ -806,6 +803,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       for (int j = jmin; j < jmax; ++j, ++n) {
         if (j == near) signal(kBarAhead);
         const bool more = j + 1 < jmax;
+        hand_round(ids, j + 1);
+        if (j + 2 < jmax) ids = look_up(j + 2);
         uint32_t st = n % kExtKStages;
         if (n >= kExtKStages) ok = warp_wait(kBarKFree + (int)st, (n / kExtKStages - 1u) & 1u);
         if (!ok) break;
@@ -824,10 +823,6 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         if (more) load_v(j + 1);
         fence_async_smem();
         signal(kBarVFull + (int)st);
-        if (j + 2 < jmax) {
-          look_up_k(j + 2);
-          look_up_v(j + 2);
-        }
       }
     }
   } else {

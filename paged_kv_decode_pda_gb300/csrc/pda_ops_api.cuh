@@ -114,7 +114,9 @@ struct ExtendPlan {
 
 // The tiles, and how many splits of the KV range each gets: one, unless the
 // tiles of all kv heads leave SMs idle (one CTA per SM); then as many as fill
-// the SMs, of at least two 128-token tiles each at the longest context.
+// the SMs, of at least two 128-token tiles each at the longest context (GB300,
+// us with at least 1 / 2 / 4 tiles: 4 new tokens at 2048 16.1 / 13.2 / 14.7, 16
+// at 512 13.4 / 12.8 / 13.7).
 // Also opts the kernel in to its shared memory, once per device.
 pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int block_size,
                        int max_blocks, int window, ExtendPlan* pl) {
