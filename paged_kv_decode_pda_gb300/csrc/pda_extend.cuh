@@ -37,6 +37,15 @@
 
 namespace pda {
 
+// What the order holds. The items of the last, partial round over the CTAs
+// are cut into pieces of their KV range, so that more CTAs share them.
+struct ExtendHead {
+  int tiles;                    // tiles in the order
+  int whole;                    // work items handed out whole
+  int tail;                     // items behind them (fewer than CTAs)
+  int pieces;                   // pieces of each of those
+};
+
 struct ExtendParams {
   void* out;                    // [T][H][128]
   const __nv_bfloat16* q;       // [T][H][128]
@@ -65,7 +74,9 @@ struct ExtendParams {
   int tiles;                    // tile slots
   int nsplit;                   // KV splits
   const int2* order;            // (sequence, first token) of the tiles, longest first; nullptr: by slot
-  const int* order_count;       // tiles in it
+  const ExtendHead* head;       // with an order: what it holds
+  float* tail_o;                // pieces of the last items: [item][256 rows][pieces][128]
+  float* tail_ml;               // and their (reference, l)
   unsigned* queue;              // next work item, CTAs done (both left at zero); nullptr: items dealt out in turn
   float* part_o;                // [T][H][nsplit][128]   (nsplit > 1)
   float* part_ml;               // [T][H][nsplit][2]: reference (log2 units), l
@@ -289,14 +300,14 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 // A work item: a tile of query rows, a kv head and a share of the KV range.
 // Tiles of 128 tokens [j0, j1) hold what block A's and B's rows attend to.
 struct __align__(16) ExtendItem {
-  int more;                     // 0: no further item
+  int more;                     // 0: no further item; 1: one; 2 + i: a piece of tail item i
   int seq, row0, rows;          // first query row (token) in the packing; rows (token, head) of the tile
   int pos0;                     // position of the first token
   int kv_lo, kv_hi;             // tokens some row attends to
   int j0a, j1a, j0b, j1b;
   int jmin, jmax;
   int both;                     // both blocks hold the same rows
-  int kvh, split;
+  int kvh, split;               // split | splits << 8 of the KV range
 };
 static_assert(sizeof(ExtendItem) == 64, "one slot");
 
@@ -319,8 +330,8 @@ __device__ __forceinline__ int2 extend_slot(const ExtendParams& p, int slot) {
   return make_int2(s, (slot - first_slot(s)) * p.tile_tokens);
 }
 
-// Describes the tile of sequence s from token `first` on (t.kvh and t.split
-// are set); false where it has no rows.
+// Describes the tile of sequence s from token `first` on (t.more, t.kvh and
+// t.split are set); false where it has no rows.
 __device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int first, ExtendItem& t) {
   const int start = max(0, min(__ldg(p.query_starts + s), p.num_tokens));
   const int end = max(start, min(__ldg(p.query_starts + s + 1), p.num_tokens));
@@ -329,7 +340,6 @@ __device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int fi
   if (first < 0 || first >= n) return false;
   const int tokens = min(p.tile_tokens, n - first);
   const int len = (int)max(0ll, min((long long)len0, (long long)p.max_blocks * p.block_size));
-  t.more = 1;
   t.seq = s;
   t.row0 = start + first;
   t.rows = tokens * p.gqa;
@@ -347,9 +357,9 @@ __device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int fi
   tiles_of(t.both ? 0 : kExtRows / p.gqa, tokens, t.j0b, t.j1b);
   t.jmin = t.j0a;
   t.jmax = max(t.j1a, t.j1b);
-  if (p.nsplit > 1) {
-    const int per = (t.jmax - t.jmin + p.nsplit - 1) / p.nsplit;
-    const int a = t.jmin + t.split * per, b = min(t.jmax, a + per);
+  if (const int splits = t.split >> 8; splits > 1) {
+    const int per = (t.jmax - t.jmin + splits - 1) / splits;
+    const int a = t.jmin + (t.split & 255) * per, b = min(t.jmax, a + per);
     t.jmin = min(a, t.jmax);
     t.jmax = max(t.jmin, b);
     t.j0a = max(t.j0a, t.jmin), t.j1a = max(t.j0a, min(t.j1a, t.jmax));
@@ -630,14 +640,18 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         tc_fence_after();
       }
       if (mt == -INFINITY) fa = 0.f;
-      const size_t prow = orow2 * p.nsplit + t.split;
-      if (p.nsplit == 1) {
+      // Splits leave (O, reference, l): of a row of the call, or of the tail item's
+      const int split = t.split & 255, splits = t.split >> 8;
+      const bool partial = splits > 1;
+      const size_t prow =
+          (t.more >= 2 ? (size_t)(t.more - 2) * (2 * kExtRows) + row2 : orow2) * splits + split;
+      if (!partial) {
         const float zs = p.sinks && live2 ? __ldg(p.sinks + head2) * 1.4426950408889634f : -INFINITY;
         const float r = live2 && t.pos0 + tok2 >= 0 ? finish(1.f, den, M, zs, p.v_scale) : 0.f;
         fa *= r;
         fb *= r;
       } else if (live2 && (x == 0 || !t.both)) {
-        *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(M, den);
+        *reinterpret_cast<float2*>((t.more >= 2 ? p.tail_ml : p.part_ml) + prow * 2) = make_float2(M, den);
       }
       const int i0 = t.both ? 4 * x : 0, i1 = t.both ? 4 * x + 4 : 8;
 #pragma unroll 1
@@ -654,9 +668,9 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
           r[k] = fa != 0.f ? __uint_as_float(o[k]) * fa : 0.f;
           if (t.both && fb != 0.f) r[k] += __uint_as_float(u[k]) * fb;
         }
-        if (p.nsplit > 1) {
+        if (partial) {
           if (live2) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 16 * i);
+            float4* dst = reinterpret_cast<float4*>((t.more >= 2 ? p.tail_o : p.part_o) + prow * kHeadDim + 16 * i);
 #pragma unroll
             for (int k = 0; k < 4; ++k) dst[k] = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
           }
@@ -676,7 +690,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
           st_shared_v4(own + lane * 16u + (uint32_t)(2 * i + 1) * kExtColumn, make_uint4(w[4], w[5], w[6], w[7]));
         }
       }
-      if (p.nsplit == 1) {
+      if (!partial) {
         // The rows went to the warp's own part of the query tile, a 16-byte
         // column apart (its products are done), and leave from there 8 rows x
         // 64 bytes at a time, as the queries came.
@@ -903,8 +917,11 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       // The order comes from the kernel in front, which this one does not
       // wait for as a whole.
       if (p.order) grid_dependency_wait();
-      const unsigned tiles = p.order ? (unsigned)__ldcg(p.order_count) : (unsigned)p.tiles;
-      const unsigned total = tiles * (unsigned)p.num_kv_heads * (unsigned)p.nsplit;
+      const unsigned heads = (unsigned)p.num_kv_heads;
+      ExtendHead head = {p.tiles, 0, 0, 1};
+      if (p.order) head = *reinterpret_cast<const ExtendHead*>(p.head);
+      else head.whole = (int)((unsigned)p.tiles * heads * (unsigned)p.nsplit);
+      const unsigned total = (unsigned)head.whole + (unsigned)(head.tail * head.pieces);
       unsigned ticket = blockIdx.x;
       auto take = [&]() {
         if (p.queue) {
@@ -920,19 +937,33 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         if (it > 0 && !warp_wait(kBarAhead, (uint32_t)(it - 1) & 1u)) break;
         if (it > 0) take();
         ExtendItem t;
-        t.more = 0;
+        bool found = false;
         while (ticket < total) {
           // heads, then splits, then tiles: CTAs that run together share
           // tables; without an order, later tiles of a sequence (which see
           // more tokens) go first
-          t.kvh = (int)(ticket % (unsigned)p.num_kv_heads);
-          const unsigned rest = ticket / (unsigned)p.num_kv_heads;
-          t.split = (int)(rest % (unsigned)p.nsplit);
-          const int i = (int)(rest / (unsigned)p.nsplit);
-          const int2 at = p.order ? __ldcg(p.order + i) : extend_slot(p, p.tiles - 1 - i);
-          if (extend_item(p, at.x, at.y, t)) break;
+          unsigned item = ticket;
+          t.more = 1;
+          if (ticket >= (unsigned)head.whole) {
+            const unsigned at = ticket - (unsigned)head.whole;
+            item = (unsigned)head.whole + at / (unsigned)head.pieces;
+            t.more = 2 + (int)(at / (unsigned)head.pieces);
+            t.split = (int)(at % (unsigned)head.pieces) | head.pieces << 8;
+          }
+          t.kvh = (int)(item % heads);
+          unsigned tile = item / heads;
+          if (!p.order) {
+            t.split = (int)(tile % (unsigned)p.nsplit) | p.nsplit << 8;
+            tile /= (unsigned)p.nsplit;
+          } else if (t.more == 1) {
+            t.split = 1 << 8;
+          }
+          const int2 at = p.order ? __ldcg(p.order + tile) : extend_slot(p, p.tiles - 1 - (int)tile);
+          found = extend_item(p, at.x, at.y, t);
+          if (found) break;
           take();
         }
+        if (!found) t.more = 0;
         const int slot = it % kExtSlots;
         if (it >= kExtSlots) ok = warp_wait(kBarItemFree + slot, (uint32_t)(it / kExtSlots - 1) & 1u);
         if (!ok) break;
@@ -967,13 +998,18 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
 
 // pda_extend_order_kernel: the tiles of a call with more work items than CTAs,
 // longest KV range first (a counting sort by 128-token tiles, one block), so
-// that the items that come last are short. GB300, us without and with it: a mixed
-// batch of 24 sequences 167 -> 160; 2 x 2048 tokens at 8192, whose 512 items are
-// of near one size, 365 -> 372.
+// that the items that come last are short; the last, partial round of them is
+// cut into pieces for the CTAs it would leave idle (pda_extend_tail_kernel joins
+// them). GB300, us without either / with the order / with both: 2 x 2048
+// tokens at 8192 (3.4 items a CTA) 355 / 361 / 337, 64 x 4 tokens over
+// 2000-4000 157 / 157 / 152, a mixed batch of 24 sequences (6.9 items) 159 / 153
+// / 157.
 constexpr int kExtOrderThreads = 1024;
 constexpr int kExtMaxOrdered = 16384;                 // tile slots
+constexpr int kExtMaxPieces = 4;
+constexpr int kExtMinPiece = 4;                       // KV tiles
 __global__ void __launch_bounds__(kExtOrderThreads) pda_extend_order_kernel(const ExtendParams p, int2* order,
-                                                                            int* count) {
+                                                                            ExtendHead* head, int ctas) {
   __shared__ int hist[kExtOrderThreads], sums[32];
   grid_dependents_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -993,9 +1029,7 @@ __global__ void __launch_bounds__(kExtOrderThreads) pda_extend_order_kernel(cons
     at = make_int2(lo, (slot - ((__ldg(p.query_starts + lo) - base) / p.tile_tokens + lo)) * p.tile_tokens);
     ExtendItem t;
     t.kvh = t.split = 0;
-    ExtendParams q = p;
-    q.nsplit = 1;
-    if (!extend_item(q, at.x, at.y, t)) return -1;
+    if (!extend_item(p, at.x, at.y, t)) return -1;
     return min(t.jmax - t.jmin, kExtOrderThreads - 1);
   };
   for (int slot = tid; slot < p.tiles; slot += kExtOrderThreads) {
@@ -1024,13 +1058,61 @@ __global__ void __launch_bounds__(kExtOrderThreads) pda_extend_order_kernel(cons
     sums[lane] = v;
   }
   __syncthreads();
-  hist[tid] = (warp ? sums[warp - 1] : 0) + x - mine;
-  if (tid == 0) *count = sums[31];
+  const int before = (warp ? sums[warp - 1] : 0) + x - mine;
+  hist[tid] = before;
+  // The thread whose size holds the first item of the last, partial round
+  // (the largest of them) cuts that round: into as many pieces as leave no
+  // CTA two of them, of at least kExtMinPiece tiles for that item.
+  const int tiles = sums[31];
+  const int items = tiles * p.num_kv_heads;
+  const int rest = items > ctas ? items % ctas : 0;
+  const int cut = rest ? (items - rest) / p.num_kv_heads : 0;    // tile of that item
+  if (rest ? (before <= cut && cut < before + mine) : tid == 0) {
+    int n = rest ? min(ctas / rest, (kExtOrderThreads - 1 - tid) / kExtMinPiece) : 1;
+    n = max(1, min(n, kExtMaxPieces));
+    const int whole = n > 1 ? items - rest : items;
+    *head = ExtendHead{tiles, whole, items - whole, n};
+  }
   __syncthreads();
   for (int slot = tid; slot < p.tiles; slot += kExtOrderThreads) {
     int2 at;
     const int n = size_of(slot, at);
     if (n >= 0) order[atomicAdd(&hist[kExtOrderThreads - 1 - n], 1)] = at;
+  }
+}
+
+// Joins the pieces of the last items: a warp per row of a tail item's tile, a
+// block 8 rows at a time and kExtTailBlocks blocks an item; those past the
+// tail return at once. (Joined by the piece that is done last, in the kernel
+// itself, 2 x 2048 tokens at 8192 took 379 us against 337: the softmax loop's
+// code came out worse.)
+constexpr int kExtTailRows = 8, kExtTailBlocks = 8;
+__global__ void __launch_bounds__(kExtTailRows * 32) pda_extend_tail_kernel(const ExtendParams p) {
+  grid_dependency_wait();
+  const ExtendHead head = *p.head;
+  const int item = (int)blockIdx.y;
+  if (item >= head.tail) return;
+  const int lane = threadIdx.x & 31;
+  const int at = head.whole + item;
+  const int2 tile = __ldcg(p.order + at / p.num_kv_heads);
+  ExtendItem t;
+  t.kvh = at % p.num_kv_heads;
+  t.split = 0;
+  if (!extend_item(p, tile.x, tile.y, t)) return;
+  for (int row = (int)blockIdx.x * kExtTailRows + (threadIdx.x >> 5); row < t.rows;
+       row += kExtTailBlocks * kExtTailRows) {
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const size_t first = ((size_t)item * (2 * kExtRows) + row) * head.pieces;
+#pragma unroll 4
+    for (int i = 0; i < head.pieces; ++i) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.tail_ml) + (first + i));
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(p.tail_o + (first + i) * kHeadDim) + lane);
+      if (ml.x != -INFINITY) lse_fold(M, den, acc, ml.x, ml.y, o);
+    }
+    const int tok = row / p.gqa;
+    store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, t.row0 + tok,
+                 t.kvh * p.gqa + row - tok * p.gqa, lane, M != -INFINITY, M, den, acc);
   }
 }
 

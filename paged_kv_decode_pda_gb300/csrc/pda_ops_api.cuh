@@ -150,7 +150,10 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
   pl->nsplit = n < 1 ? 1 : (int)n;
   pl->sms = sms;
   pl->ordered = ctas > sms && pl->tiles <= pda::kExtMaxOrdered;   // then there is one split
-  pl->bytes = kQueueBytes + (pl->ordered ? (size_t)pl->tiles * sizeof(int2) : 0);
+  pl->bytes = kQueueBytes;
+  if (pl->ordered)  // what the order holds, the order, and the rows of up to one piece per CTA
+    pl->bytes += 256 + align256((size_t)pl->tiles * sizeof(int2)) +
+                 (size_t)sms * 2 * pda::kExtRows * (kHeadDim + 2) * sizeof(float);
   if (pl->nsplit > 1) pl->bytes += (size_t)num_tokens * num_heads * pl->nsplit * (kHeadDim + 2) * sizeof(float);
   return PDA_OK;
 }
@@ -470,16 +473,25 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     if (pl.ordered && ws) {
-      int* count = reinterpret_cast<int*>(p.queue + 2);
-      int2* order = reinterpret_cast<int2*>(static_cast<char*>(ws) + kQueueBytes);
-      pda::pda_extend_order_kernel<<<1, pda::kExtOrderThreads, 0, stream>>>(p, order, count);
+      char* at = static_cast<char*>(ws) + kQueueBytes;
+      pda::ExtendHead* head = reinterpret_cast<pda::ExtendHead*>(at);
+      int2* order = reinterpret_cast<int2*>(at + 256);
+      p.tail_o = reinterpret_cast<float*>(at + 256 + align256((size_t)pl.tiles * sizeof(int2)));
+      p.tail_ml = p.tail_o + (size_t)pl.sms * 2 * pda::kExtRows * kHeadDim;
+      pda::pda_extend_order_kernel<<<1, pda::kExtOrderThreads, 0, stream>>>(p, order, head, pl.sms);
       if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
       p.order = order;
-      p.order_count = count;
+      p.head = head;
       lc.attrs = attr;
       lc.numAttrs = 1;
     }
     if (cudaLaunchKernelEx(&lc, pda::pda_extend_kernel, p) != cudaSuccess) return PDA_ERR_CUDA;
+    if (p.order) {
+      lc.gridDim = dim3(pda::kExtTailBlocks, (unsigned)(pl.sms + 1) / 2);   // two pieces an item at least
+      lc.blockDim = dim3(pda::kExtTailRows * 32);
+      lc.dynamicSmemBytes = 0;
+      return cudaLaunchKernelEx(&lc, pda::pda_extend_tail_kernel, p) == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+    }
     if (pl.nsplit == 1) return PDA_OK;
     pda::ExtendMergeParams m = {};
     m.out = out;

@@ -125,6 +125,17 @@ def test_a_long_context_split_over_the_gpu():
     check(c, window=5000)
 
 
+@pytest.mark.parametrize("seqs,H,Hk,bs", [
+    ([(2, 700 + 150 * (i % 9)) for i in range(21)], 16, 8, 16),               # 168 items of few rows, the last 16 cut
+    ([(70, 1100 + 37 * i) for i in range(20)] + [(1, 9), (0, 5)], 24, 8, 32),  # full tiles, and spare slots
+    ([(9, 2000)] * 41, 32, 4, 64),
+])
+def test_more_items_than_sms(seqs, H, Hk, bs):
+    c = O.Chunk(seqs, H, Hk, bs, seed=25)
+    check(c)
+    check(c, sinks=torch.linspace(-2, 4, H), window=900)
+
+
 def test_a_cache_past_2_31_bytes():
     bs, Hk, NB = 16, 8, 140_000
     kc = torch.zeros(NB, Hk, 8, bs, 16, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
