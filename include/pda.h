@@ -509,8 +509,8 @@ pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int n
  * free sequences without the host.
  *
  *   ref_counts    int32 [num_blocks]: table entries that hold the page; a
- *                 page with count 0 is free. (A caller that pins a page
- *                 adds 1.)
+ *                 page with count 0 is free. A caller that holds a page
+ *                 itself (a prefix kept for later) adds 1
  *   block_tables  int32 [num_rows][max_num_blocks_per_seq]
  *   seq_lens      int32 [num_rows]: row r holds its first
  *                 ceil(seq_lens[r] / block_size) entries; others are unused
@@ -577,9 +577,11 @@ pda_status pda_free_pages(const pda_page_table* table, const int32_t* rows, int 
 
 /* pda_compact_pages -- moves pages so that the L held pages are ids 0..L-1:
  * the k-th free id below L takes the k-th held page at or above L, in every
- * array; counts move along, and every table entry in use follows. */
+ * array; counts move along, and every table entry in use follows. new_ids
+ * (int32 [num_blocks] on the device, or NULL) receives each page's id after
+ * the call, for holders outside the table. */
 pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* arrays, int num_arrays,
-                             cudaStream_t stream);
+                             int32_t* new_ids, cudaStream_t stream);
 
 /* pda_reserve_pages -- size the page calls' workspace of (current device,
  * stream) for pools and tables up to these sizes and calls of up to

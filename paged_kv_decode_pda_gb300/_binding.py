@@ -83,7 +83,7 @@ SIGNATURES = {
     "pda_grow_pages": (_I, [_P, _P, _P, _I, _P]),
     "pda_fork_pages": (_I, [_P, _P, _P, _I, _P, _I, _P]),
     "pda_free_pages": (_I, [_P, _P, _I, _P]),
-    "pda_compact_pages": (_I, [_P, _P, _I, _P]),
+    "pda_compact_pages": (_I, [_P, _P, _I, _P, _P]),
     "pda_reserve_pages": (_I, [ctypes.c_longlong, _I, _I, _P]),
 }
 
@@ -505,14 +505,14 @@ def _on_device(what: str, tensors) -> int:
     for t in tensors:
         if t.get_device() != dev:
             _refuse(what + ": tensors must be on one CUDA device")
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _device():
         _refuse(what + ": tensors must be on the current CUDA device")
     return dev
 
 
 def _stream_on(stream, dev: int) -> int:
     """The raw handle of ``stream``, or of the current stream of device ``dev``."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_ptr(stream)
+    return _raw_stream(dev) if stream is None else _stream_ptr(stream)
 
 
 # ---------------------------------------------------------------- rotary
@@ -551,8 +551,8 @@ def _rope_refuse(what, heads, positions, inv_freq):
 
 
 _BF16, _I64, _I32, _F64 = torch.bfloat16, torch.int64, torch.int32, torch.float64
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_device = torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # absent in builds without CUDA
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor, *,
@@ -579,7 +579,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_f
         n, h, d = x.shape
         s0, s1, s2 = x.stride()
         if out is None:
-            out = x.new_empty((n, h, d))
+            out = torch.empty((n, h, d), dtype=_BF16, device=x.device)
             o0, o1, o2 = h * d, d, 1
         elif out.shape != x.shape or out.dtype is not _BF16 or out.get_device() != dev:
             _refuse("rope: out must be bf16, shaped like its input, on its device")
@@ -639,7 +639,7 @@ def rope_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
             or v_cache.shape != ((NB, Hk, bs // 16, D, 16) if v_shuffled else (NB, Hk, D, bs)):
         _refuse(what + ": shapes")
     if q_out is None:
-        q_out = q.new_empty((T, H, D))
+        q_out = torch.empty((T, H, D), dtype=_BF16, device=q.device)
         o0, o1, o2 = H * D, D, 1
     else:
         o0, o1, o2 = q_out.stride() if q_out.dim() == 3 else (0, 0, 0)
@@ -695,7 +695,7 @@ def extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
     fp8 = output_scale is not None
     want = torch.float8_e4m3fn if fp8 else torch.bfloat16
     if out is None:
-        out = q.new_empty((T, H, D), dtype=want)
+        out = torch.empty((T, H, D), dtype=want, device=q.device)
     elif out.shape != q.shape or out.dtype not in ((want, torch.uint8) if fp8 else (want,)):
         _refuse("extend: out")
     ts = (q, k_cache, v_cache, block_tables, seq_lens, query_starts, out)
@@ -727,17 +727,14 @@ def reserve_extend(num_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks
 def _page_table(what, ref_counts, block_tables, seq_lens, block_size, *lists):
     """(ctypes pda_page_table, device index) of the checked state and request lists."""
     dev = ref_counts.get_device()
-    if block_tables.dim() != 2 or ref_counts.dim() != 1:
+    S, MB = block_tables.shape if block_tables.dim() == 2 else (-1, -1)
+    if ref_counts.dim() != 1 or seq_lens.shape != (S,):
         _refuse(what + ": shapes (ref_counts [NB], block_tables [S, MB], seq_lens [S])")
-    S, MB = block_tables.shape
-    if seq_lens.shape != (S,):
-        _refuse(what + ": shapes (ref_counts [NB], block_tables [S, MB], seq_lens [S])")
-    for t in (ref_counts, block_tables, seq_lens) + lists:
+    for t in (ref_counts, block_tables, seq_lens, *lists):
         if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
             _refuse(what + ": tables, counts, lengths and lists must be contiguous int32 on one CUDA device")
-    for t in lists:
-        if t.dim() != 1 or t.shape != lists[0].shape:
-            _refuse(what + ": request lists must be vectors of one length")
+    if lists and (lists[0].dim() != 1 or lists[-1].shape != lists[0].shape):
+        _refuse(what + ": request lists must be vectors of one length")
     if dev < 0 or dev != _device():
         _refuse(what + ": tensors must be on the current CUDA device")
     return _PageTable(ref_counts.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), ref_counts.shape[0], S, MB,
@@ -757,7 +754,7 @@ def _page_arrays(what, caches, num_blocks, dev):
         return kind(), 0
     flat = []
     for t in caches:
-        if t.dim() < 1 or t.shape[0] != num_blocks or not t.is_contiguous() or t.get_device() != dev:
+        if t.dim() == 0 or t.shape[0] != num_blocks or not t.is_contiguous() or t.get_device() != dev:
             _refuse(what + ": caches must be contiguous [num_blocks, ...] tensors on the current device")
         flat.append((t.data_ptr(), t.nbytes // num_blocks))
     return kind(*flat), n
@@ -779,10 +776,11 @@ def copy_pages(caches, src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> 
 def grow_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, rows: torch.Tensor,
                add: torch.Tensor, block_size: int, *, stream=None) -> None:
     """``pda_grow_pages``: row ``rows[i]`` takes ``add[i]`` more tokens, with fresh pages where it needs them."""
-    lib = _lib or load()
     tab, dev = _page_table("grow_pages", ref_counts, block_tables, seq_lens, block_size, rows, add)
-    _check(lib.pda_grow_pages(ctypes.addressof(tab), rows.data_ptr(), add.data_ptr(), rows.shape[0],
-                              _stream_on(stream, dev)), "pda_grow_pages")
+    st = (_lib or load()).pda_grow_pages(ctypes.addressof(tab), rows.data_ptr(), add.data_ptr(), rows.shape[0],
+                                         _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_grow_pages")
 
 
 def fork_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, parents: torch.Tensor,
@@ -792,29 +790,39 @@ def fork_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: t
     Full pages are shared; a partly filled last page is copied to a fresh one
     in every tensor of ``caches`` (``[num_blocks, ...]`` each).
     """
-    lib = _lib or load()
     tab, dev = _page_table("fork_pages", ref_counts, block_tables, seq_lens, block_size, parents, children)
-    arr, n = _page_arrays("fork_pages", caches, ref_counts.shape[0], dev)
-    _check(lib.pda_fork_pages(ctypes.addressof(tab), parents.data_ptr(), children.data_ptr(), parents.shape[0],
-                              ctypes.addressof(arr), n, _stream_on(stream, dev)), "pda_fork_pages")
+    arr, n = _page_arrays("fork_pages", caches, tab.num_blocks, dev)
+    st = (_lib or load()).pda_fork_pages(ctypes.addressof(tab), parents.data_ptr(), children.data_ptr(),
+                                         parents.shape[0], ctypes.addressof(arr), n,
+                                         _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_fork_pages")
 
 
 def free_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, rows: torch.Tensor,
                block_size: int, *, stream=None) -> None:
     """``pda_free_pages``: rows become empty and give their pages up."""
-    lib = _lib or load()
     tab, dev = _page_table("free_pages", ref_counts, block_tables, seq_lens, block_size, rows)
-    _check(lib.pda_free_pages(ctypes.addressof(tab), rows.data_ptr(), rows.shape[0], _stream_on(stream, dev)),
-           "pda_free_pages")
+    st = (_lib or load()).pda_free_pages(ctypes.addressof(tab), rows.data_ptr(), rows.shape[0],
+                                         _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_free_pages")
 
 
 def compact_pages(ref_counts: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, block_size: int,
-                  caches=(), *, stream=None) -> None:
-    """``pda_compact_pages``: move the held pages to the lowest ids, in every cache, count and table entry."""
+                  caches=(), *, new_ids: torch.Tensor | None = None, stream=None) -> None:
+    """``pda_compact_pages``: move the held pages to the lowest ids, in every cache, count and table entry.
+
+    ``new_ids`` (int32 ``[num_blocks]``) receives every page's id after the call.
+    """
     lib = _lib or load()
     tab, dev = _page_table("compact_pages", ref_counts, block_tables, seq_lens, block_size)
     arr, n = _page_arrays("compact_pages", caches, ref_counts.shape[0], dev)
-    _check(lib.pda_compact_pages(ctypes.addressof(tab), ctypes.addressof(arr), n, _stream_on(stream, dev)),
+    if new_ids is not None and (new_ids.shape != ref_counts.shape or new_ids.dtype is not _I32
+                                or not new_ids.is_contiguous() or new_ids.get_device() != dev):
+        _refuse("compact_pages: new_ids must be contiguous int32 [num_blocks] on the tables' device")
+    _check(lib.pda_compact_pages(ctypes.addressof(tab), ctypes.addressof(arr), n,
+                                 None if new_ids is None else new_ids.data_ptr(), _stream_on(stream, dev)),
            "pda_compact_pages")
 
 

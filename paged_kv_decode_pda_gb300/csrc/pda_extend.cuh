@@ -1074,10 +1074,24 @@ __global__ void __launch_bounds__(kExtOrderThreads) pda_extend_order_kernel(cons
     *head = ExtendHead{tiles, whole, items - whole, n};
   }
   __syncthreads();
-  for (int slot = tid; slot < p.tiles; slot += kExtOrderThreads) {
-    int2 at;
-    const int n = size_of(slot, at);
-    if (n >= 0) order[atomicAdd(&hist[kExtOrderThreads - 1 - n], 1)] = at;
+  // Scatter in slot order within a size (warp after warp, so that the same
+  // state always gives the same order, and with it the same pieces).
+  for (int slot0 = 0; slot0 < p.tiles; slot0 += kExtOrderThreads) {
+    int2 at = make_int2(0, 0);
+    const int n = slot0 + tid < p.tiles ? size_of(slot0 + tid, at) : -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, n);
+    const int leader = __ffs((int)peers) - 1;
+    int pos = 0;
+#pragma unroll 1
+    for (int w = 0; w < kExtOrderThreads / 32; ++w) {
+      if (w == warp && n >= 0 && lane == leader) {
+        pos = hist[kExtOrderThreads - 1 - n];
+        hist[kExtOrderThreads - 1 - n] = pos + __popc(peers);
+      }
+      __syncthreads();
+    }
+    pos = __shfl_sync(0xffffffffu, pos, leader) + __popc(peers & ((1u << lane) - 1u));
+    if (n >= 0) order[pos] = at;
   }
 }
 

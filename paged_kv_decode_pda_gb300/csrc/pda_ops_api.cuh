@@ -432,7 +432,7 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
     p.gqa = num_heads / num_kv_heads;
     p.block_size = block_size;
     p.max_blocks = max_num_blocks_per_seq;
-    p.window = window;
+    p.window = window < (1 << 30) ? window : 1 << 30;   // no position is that large
     p.logit_scale_log2 = (float)std::fabs(logit);
     p.negate = logit < 0.0 ? 1 : 0;
     p.v_scale = v_scale;
@@ -601,12 +601,14 @@ pda_status pda_free_pages(const pda_page_table* table, const int32_t* rows, int 
 }
 
 pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* arrays, int num_arrays,
-                             cudaStream_t stream) {
+                             int32_t* new_ids, cudaStream_t stream) {
   return guarded([&]() -> pda_status {
     pda::CompactParams p = {};
     pda_status st = page_state(table, &p.st);
     if (st == PDA_OK) st = check_arrays(arrays, num_arrays);
+    if (st == PDA_OK && misaligned(new_ids, 4)) st = PDA_ERR_INVALID_ARG;
     if (st != PDA_OK || table->num_blocks == 0) return st;
+    p.new_ids = new_ids;
     void* ws = nullptr;
     st = get_page_workspace(stream, page_ws_bytes(table->num_blocks, table->num_rows, 0), &ws);
     if (st != PDA_OK) return st;

@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(128) pda_page_free_kernel(const FreeParams p) 
 struct CompactParams {
   PageState st;
   PageWs ws;
+  int32_t* new_ids;    // [num_blocks], or nullptr
 };
 __global__ void __launch_bounds__(kPageThreads) pda_page_compact_kernel(const CompactParams p) {
   __shared__ int warp_sums[kPageWarps];
@@ -423,6 +424,9 @@ __global__ void __launch_bounds__(kPageThreads) pda_page_compact_kernel(const Co
   cluster_prefix(&movers, mover0, all);
   if (nh) each_ranked(first, end, hole0, warp_sums, is_hole, [&](int r, int id) { p.ws.fresh[r] = id; });
   if (nm) each_ranked(first, end, mover0, warp_sums, is_mover, [&](int r, int id) { p.ws.moved[r] = id; });
+  if (p.new_ids)
+    for (int i = first + tid; i < end; i += kPageThreads)
+      if (!is_mover(i)) p.new_ids[i] = i;
   if (me == 0 && tid == 0) {
     p.ws.head[0] = live;
     p.ws.head[1] = all;
@@ -432,6 +436,7 @@ __global__ void __launch_bounds__(kPageThreads) pda_page_compact_kernel(const Co
   for (int k = me * kPageThreads + tid; k < all; k += ctas * kPageThreads) {
     const int id = __ldcg(p.ws.moved + k), to = __ldcg(p.ws.fresh + k);
     p.ws.remap[id] = to;
+    if (p.new_ids) p.new_ids[id] = to;
     p.st.refs[to] = __ldcg(p.st.refs + id);
     p.st.refs[id] = 0;
   }

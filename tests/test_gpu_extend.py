@@ -171,6 +171,46 @@ def test_the_same_call_gives_the_same_bits():
         assert torch.equal(pda.extend(**d), a)
 
 
+def test_the_same_bits_where_items_are_cut():
+    # 40 x 8 items of one size: which of them the last round holds must not change
+    c = O.Chunk([(3, 1500)] * 40, 16, 8, seed=26)
+    d = c.to(DEV)
+    a = pda.extend(**d)
+    for _ in range(5):
+        assert torch.equal(pda.extend(**d), a)
+
+
+@pytest.mark.parametrize("scale,ks", [(-0.09, 0.05), (0.09, -0.05), (0.0, 0.05), (-0.09, -0.05)])
+def test_scales_of_any_sign(scale, ks):
+    c = O.Chunk([(40, 200), (1, 150)], 8, 2, seed=27)
+    c.scale, c.ks = scale, ks
+    check(c)
+    check(c, window=(1 << 31) - 1)
+
+
+def test_a_window_past_every_position_with_rows_in_front_of_the_cache():
+    c = O.Chunk([(9, 4), (150, 120)], 8, 2, seed=28)
+    check(c, window=(1 << 31) - 1)
+
+
+@pytest.mark.parametrize("seqs", [[(40, 300), (1, 30)], [(2, 9000)], [(3, 400)] * 30])
+def test_captured_without_a_workspace(seqs):
+    c = O.Chunk(seqs, 8, 2 if len(seqs) < 9 else 8, seed=29)
+    d = c.to(DEV)
+    ref, spread = c.exact()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.zeros_like(d["q"])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        pda.extend(**d, out=out)
+    for _ in range(2):
+        out.zero_()
+        gr.replay()
+    torch.cuda.synchronize()
+    O.check_rows(out, ref, spread)
+
+
 def test_two_batches_in_turn_on_one_stream():
     big, small = O.Chunk([(2, 9000), (2, 8000)], 8, 2, seed=20), O.Chunk([(3, 4000)], 8, 2, seed=21)
     outs = [(run(c), c) for c in (big, small, big)]

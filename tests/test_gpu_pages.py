@@ -125,6 +125,25 @@ def test_freeing_a_free_page_is_flagged():
     assert b.dev[0].tolist() == [0] * 8
 
 
+@pytest.mark.parametrize("NB", [40, 9000])
+def test_compact_tells_the_new_ids(NB):
+    b = Both(NB, 4, 6)
+    b.step("grow", [0, 1, 2], [90, 40, 60])
+    b.step("free", [0])
+    b.dev[0][NB - 1] = 1                      # held outside the table
+    b.ref.refs[NB - 1] = 1
+    want = list(range(NB))
+    b.ref.compact()
+    for src, dst in b.ref.moves:
+        want[src] = dst
+    for p in b.pages:
+        b.ref.apply_moves(p)
+    ids = torch.full((NB,), -9, dtype=torch.int32, device=DEV)
+    pda.compact_pages(*b.dev, 16, b.caches, new_ids=ids)
+    assert ids.tolist() == want and want[NB - 1] < NB - 1
+    b.same()
+
+
 def test_copy_pages():
     NB = 50
     rng = np.random.default_rng(0)

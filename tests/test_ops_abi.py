@@ -90,6 +90,14 @@ def test_extend_refuses(lib, kw, status):
     assert extend_call(lib, **kw) == status
 
 
+def test_reserve_extend_refuses(lib):
+    assert lib.pda_reserve_extend(-1, 1, 8, 2, 4, 16, None) == INVALID
+    assert lib.pda_reserve_extend(4, 1, 7, 2, 4, 16, None) == INVALID
+    assert lib.pda_reserve_extend(4, 1, 8, 2, 4, 24, None) == UNSUPPORTED
+    assert lib.pda_reserve_extend(1 << 30, 1, 16, 2, 4, 16, None) == UNSUPPORTED
+    assert lib.pda_reserve_extend(0, 0, 8, 2, 4, 16, None) == pda.PDA_OK
+
+
 def test_extend_of_nothing_is_a_noop(lib):
     assert extend_call(lib, T=0, out=None, q=None) == pda.PDA_OK
     assert extend_call(lib, S=0, tables=None, lens=None, starts=None) == pda.PDA_OK
@@ -117,7 +125,7 @@ def test_page_calls_refuse_tables(lib, kw, status):
     assert lib.pda_grow_pages(p, A, A, 1, None) == status
     assert lib.pda_fork_pages(p, A, A, 1, None, 0, None) == status
     assert lib.pda_free_pages(p, A, 1, None) == status
-    assert lib.pda_compact_pages(p, None, 0, None) == status
+    assert lib.pda_compact_pages(p, None, 0, None, None) == status
 
 
 def test_page_calls_refuse_arguments(lib):
@@ -130,13 +138,14 @@ def test_page_calls_refuse_arguments(lib):
     assert lib.pda_fork_pages(p, A, None, 1, None, 0, None) == INVALID
     assert lib.pda_fork_pages(p, A, A, 1, None, 1, None) == INVALID
     assert lib.pda_free_pages(p, None, 1, None) == INVALID
+    assert lib.pda_compact_pages(p, None, 0, A + 2, None) == INVALID
     assert lib.pda_reserve_pages(-1, 1, 1, None) == INVALID
     assert lib.pda_reserve_pages(1 << 31, 1, 1, None) == UNSUPPORTED
     for base, size in ((None, 64), (A + 8, 64), (A, 24), (A, 0)):
         arr = (B._PageArray * 1)(B._PageArray(base, size))
         for st in (lib.pda_copy_pages(ctypes.addressof(arr), 1, A, A, 1, 8, None),
                    lib.pda_fork_pages(p, A, A, 1, ctypes.addressof(arr), 1, None),
-                   lib.pda_compact_pages(p, ctypes.addressof(arr), 1, None)):
+                   lib.pda_compact_pages(p, ctypes.addressof(arr), 1, None, None)):
             assert st == INVALID
     arr = (B._PageArray * 1)(B._PageArray(A, 64))
     assert lib.pda_copy_pages(ctypes.addressof(arr), 1, None, A, 1, 8, None) == INVALID
