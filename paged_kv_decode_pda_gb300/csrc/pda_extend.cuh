@@ -59,6 +59,7 @@ struct ExtendParams {
   int num_heads;
   int num_kv_heads;
   int gqa;
+  int gqa_inverse;              // ceil(2^16 / gqa): see token_of
   int block_size;
   int max_blocks;
   int window;
@@ -139,6 +140,10 @@ __device__ __forceinline__ int sequence_of_row(const int32_t* starts, int num_se
   }
   return lo;
 }
+
+// Token of a tile's row: row / gqa, exact for rows below 256 and gqa <= 8
+// (the inverse is at most 8 / 2^16 too large, relative to 1 / gqa >= 1 / 8).
+__device__ __forceinline__ int token_of(const ExtendParams& p, int row) { return row * p.gqa_inverse >> 16; }
 
 // ------------------------------------------------- tensor core primitives
 
@@ -332,10 +337,10 @@ __device__ __forceinline__ int2 extend_slot(const ExtendParams& p, int slot) {
 
 // Describes the tile of sequence s from token `first` on (t.more, t.kvh and
 // t.split are set); false where it has no rows.
-__device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int first, ExtendItem& t) {
-  const int start = max(0, min(__ldg(p.query_starts + s), p.num_tokens));
-  const int end = max(start, min(__ldg(p.query_starts + s + 1), p.num_tokens));
-  const int len0 = __ldg(p.seq_lens + s);
+__device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int first, int start, int end, int len0,
+                                            ExtendItem& t) {
+  start = max(0, min(start, p.num_tokens));
+  end = max(start, min(end, p.num_tokens));
   const int n = end - start;
   if (first < 0 || first >= n) return false;
   const int tokens = min(p.tile_tokens, n - first);
@@ -366,6 +371,10 @@ __device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int fi
     t.j0b = max(t.j0b, t.jmin), t.j1b = max(t.j0b, min(t.j1b, t.jmax));
   }
   return true;
+}
+
+__device__ __forceinline__ bool extend_item(const ExtendParams& p, int s, int first, ExtendItem& t) {
+  return extend_item(p, s, first, __ldg(p.query_starts + s), __ldg(p.query_starts + s + 1), __ldg(p.seq_lens + s), t);
 }
 
 // The tiles block x takes: j0, j0 + step, ... below j1.
@@ -405,6 +414,16 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
     mbar_init(bar(kBarJoined), 8);
     mbar_init(bar(kBarAhead), 4);
     fence_barrier_init();
+  }
+  // Up to 32 sequences: the scheduling warp holds their starts and lengths,
+  // asked for while the CTA sets itself up.
+  const bool few = p.num_seqs <= 32;
+  int my_start = 0, my_end = 0, my_len = 0;
+  if (warp == 14 && few) {
+    const int s = min(lane, p.num_seqs - 1);
+    my_start = __ldg(p.query_starts + s);
+    my_end = __ldg(p.query_starts + s + 1);
+    my_len = __ldg(p.seq_lens + s);
   }
   if (warp == 12) tmem_alloc(sm + kExtMiscOff, 512);
   tc_fence_before();
@@ -462,7 +481,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
 #pragma unroll 1
     for (int it = 0; ok && next_item(it, t); ++it) {
       const int row = t.both ? (tid & 127) : tid;             // of the tile
-      const int tok = row / p.gqa;
+      const int tok = token_of(p, row);
       const bool live = row < t.rows;
       // The row's queries: shifted by a power of two into f16 (its largest |q|
       // in [2^14, 2^15)), stored as this row of the A operand. The products
@@ -477,7 +496,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         uint4 vv[4][4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int r = wrow + 8 * q + r8, rt = r / p.gqa;
+          const int r = wrow + 8 * q + r8, rt = token_of(p, r);
           const uint4* src = reinterpret_cast<const uint4*>(
               p.q + ((size_t)(t.row0 + rt) * p.num_heads + t.kvh * p.gqa + r - rt * p.gqa) * kHeadDim) + piece;
 #pragma unroll
@@ -521,8 +540,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       // tiles inside [in_lo, in_hi] need no mask for any live row of the block
       const int last_row = min(t.rows, t.both ? kExtRows : (x + 1) * kExtRows) - 1;
       const int first_row = t.both ? 0 : x * kExtRows;
-      const int in_hi = t.pos0 + first_row / p.gqa;
-      const int in_lo = p.window > 0 ? t.pos0 + last_row / p.gqa - p.window + 1 : 0;
+      const int in_hi = t.pos0 + token_of(p, first_row);
+      const int in_lo = p.window > 0 ? t.pos0 + token_of(p, last_row) - p.window + 1 : 0;
       int j, j1, step;
       block_tiles(t, x, j, j1, step);
       const bool any = j < j1;
@@ -619,7 +638,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       // read again rather than held in registers through the tiles
       read_item(it, t);
       release_item(it, t);
-      const int row2 = t.both ? (tid & 127) : tid, tok2 = row2 / p.gqa;
+      const int row2 = t.both ? (tid & 127) : tid, tok2 = token_of(p, row2);
       const bool live2 = row2 < t.rows;
       const int head2 = t.kvh * p.gqa + row2 - tok2 * p.gqa;
       const size_t orow2 = (size_t)(t.row0 + tok2) * p.num_heads + head2;
@@ -701,7 +720,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         const int c0 = t.both ? cols / 2 * x : 0, c1 = t.both ? c0 + cols / 2 : cols;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
-          const int rr = wrow + 8 * q + r8, rt = rr / p.gqa;
+          const int rr = wrow + 8 * q + r8, rt = token_of(p, rr);
           if (rr < t.rows) {
             uint8_t* dst = static_cast<uint8_t*>(p.out) +
                            ((size_t)(t.row0 + rt) * p.num_heads + t.kvh * p.gqa + rr - rt * p.gqa) * (size_t)(cols * 16);
@@ -958,18 +977,31 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
           } else if (t.more == 1) {
             t.split = 1 << 8;
           }
-          const int2 at = p.order ? __ldcg(p.order + tile) : extend_slot(p, p.tiles - 1 - (int)tile);
-          found = extend_item(p, at.x, at.y, t);
+          const int slot = p.tiles - 1 - (int)tile;
+          int2 at;
+          if (p.order) {
+            at = __ldcg(p.order + tile);
+          } else if (few) {
+            const int first_slot = (my_start - __shfl_sync(0xffffffffu, my_start, 0)) / p.tile_tokens + lane;
+            const unsigned hit = __ballot_sync(0xffffffffu, lane < p.num_seqs && first_slot <= slot);
+            at.x = hit ? 31 - __clz((int)hit) : 0;
+            at.y = (slot - __shfl_sync(0xffffffffu, first_slot, at.x)) * p.tile_tokens;
+          } else {
+            at = extend_slot(p, slot);
+          }
+          found = few ? extend_item(p, at.x, at.y, __shfl_sync(0xffffffffu, my_start, at.x),
+                                    __shfl_sync(0xffffffffu, my_end, at.x), __shfl_sync(0xffffffffu, my_len, at.x), t)
+                      : extend_item(p, at.x, at.y, t);
           if (found) break;
           take();
         }
         if (!found) t.more = 0;
-        const int slot = it % kExtSlots;
-        if (it >= kExtSlots) ok = warp_wait(kBarItemFree + slot, (uint32_t)(it / kExtSlots - 1) & 1u);
+        const int place = it % kExtSlots;
+        if (it >= kExtSlots) ok = warp_wait(kBarItemFree + place, (uint32_t)(it / kExtSlots - 1) & 1u);
         if (!ok) break;
         if (lane == 0) {
-          *reinterpret_cast<ExtendItem*>(smem + kExtItemOff + slot * 64) = t;
-          mbar_arrive(bar(kBarItemFull + slot));
+          *reinterpret_cast<ExtendItem*>(smem + kExtItemOff + place * 64) = t;
+          mbar_arrive(bar(kBarItemFull + place));
         }
         if (!t.more) break;
       }
@@ -1124,7 +1156,7 @@ __global__ void __launch_bounds__(kExtTailRows * 32) pda_extend_tail_kernel(cons
       const float4 o = __ldcg(reinterpret_cast<const float4*>(p.tail_o + (first + i) * kHeadDim) + lane);
       if (ml.x != -INFINITY) lse_fold(M, den, acc, ml.x, ml.y, o);
     }
-    const int tok = row / p.gqa;
+    const int tok = token_of(p, row);
     store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, t.row0 + tok,
                  t.kvh * p.gqa + row - tok * p.gqa, lane, M != -INFINITY, M, den, acc);
   }

@@ -430,6 +430,7 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
     p.num_heads = num_heads;
     p.num_kv_heads = num_kv_heads;
     p.gqa = num_heads / num_kv_heads;
+    p.gqa_inverse = (65536 + p.gqa - 1) / p.gqa;
     p.block_size = block_size;
     p.max_blocks = max_num_blocks_per_seq;
     p.window = window < (1 << 30) ? window : 1 << 30;   // no position is that large
