@@ -1033,9 +1033,9 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
 // that the items that come last are short; the last, partial round of them is
 // cut into pieces for the CTAs it would leave idle (pda_extend_tail_kernel joins
 // them). GB300, us without either / with the order / with both: 2 x 2048
-// tokens at 8192 (3.4 items a CTA) 355 / 361 / 337, 64 x 4 tokens over
-// 2000-4000 157 / 157 / 152, a mixed batch of 24 sequences (6.9 items) 159 / 153
-// / 157.
+// tokens at 8192 (3.4 items a CTA) 349 / 361 / 338, 64 x 4 tokens over
+// 2000-4000 152 / 157 / 152, a mixed batch of 24 sequences (6.9 items)
+// 159 / 153 / 156.
 constexpr int kExtOrderThreads = 1024;
 constexpr int kExtMaxOrdered = 16384;                 // tile slots
 constexpr int kExtMaxPieces = 4;

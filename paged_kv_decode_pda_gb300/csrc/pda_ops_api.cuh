@@ -75,24 +75,29 @@ pda_status rope_launch(pda::RopeParams& p, bool vec, cudaStream_t stream) {
     pda::pda_rope_any_kernel<kCache><<<(unsigned)blocks, pda::kRopeThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
   }
-  // Heads of a CTA: with the cache a kv head's; else as many as leave about a
-  // wave (every CTA makes its tokens' angles anew; 4096 tokens of 40/8 heads:
-  // 25.4 us against 27.1 with twice the CTAs).
+  // Heads of a CTA: with the cache a kv head's; else as many as leave about
+  // four CTAs an SM (every CTA makes its tokens' angles anew).
   const int heads = p.num_heads + p.num_kv_heads;
-  const long long tiles16 = (T + 15) / 16;
-  long long groups = kCache ? p.num_kv_heads : (608 + tiles16 - 1) / tiles16;
+  const long long tiles4 = (T + 3) / 4, tiles16 = (T + 15) / 16;
+  long long groups = kCache ? p.num_kv_heads : (608 + tiles4 - 1) / tiles4;
   if (!kCache && groups > (heads + 7) / 8) groups = (heads + 7) / 8;
   p.groups = (int)groups;
-  // Tokens per CTA: 16 store whole V rows; a step's fewer tokens go 4 or one to
-  // a CTA, which spreads them over the SMs (GB300, us with 4 / one a CTA: 256
-  // tokens of 40/8 heads 4.5 / 6.0, with the cache 32/8 heads 8.0 / 9.4; 64
-  // tokens with the cache 6.3 / 5.6).
-  const long long ctas16 = tiles16 * groups;
-  if (ctas16 >= 608) {
-    const dim3 grid((unsigned)tiles16, (unsigned)p.groups);
-    pda::pda_rope_kernel<16, kCache><<<grid, pda::kRopeThreads, 0, stream>>>(p);
-  } else if (ctas16 >= 64) {
-    const dim3 grid((unsigned)((T + 3) / 4), (unsigned)p.groups);
+  // Tokens per CTA. With the cache 16, which store whole V rows where the slots
+  // run on (1024 tokens of 64/8 heads: 12.3 us against 19.0 with 4; 2000
+  // scattered ones 29.1 / 26.8), from two CTAs an SM on.
+  if constexpr (kCache) {
+    if (tiles16 * groups >= 304) {
+      const dim3 grid((unsigned)tiles16, (unsigned)p.groups);
+      pda::pda_rope_kernel<16, kCache><<<grid, pda::kRopeThreads, 0, stream>>>(p);
+      return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+    }
+  }
+  // Else 4, or one for the steps of the fewest tokens, which it spreads over
+  // more SMs (us with 4 / one a CTA: 256 tokens of 40/8 heads 4.4 / 6.0, with
+  // the cache 32/8 heads 7.0 / 10.1, 64 tokens with it 5.8 / 6.2; 16 tokens of
+  // 40/8 heads 3.6 / 3.3).
+  if (tiles4 * groups >= 128) {
+    const dim3 grid((unsigned)tiles4, (unsigned)p.groups);
     pda::pda_rope_kernel<4, kCache><<<grid, pda::kRopeThreads, 0, stream>>>(p);
   } else {
     const dim3 grid((unsigned)T, (unsigned)p.groups);

@@ -15,11 +15,13 @@
 // Bound: bytes (6 flops per 4 bytes moved). One CTA holds kTok tokens and one
 // group of heads: it computes the (cos, sin) table of its tokens once and
 // rotates every head of the group with it, each thread keeping its token's
-// eight pairs in registers; the first loads are issued before the table is
-// made. What counts then is how many CTAs fit an SM: 64 and 72 registers a
-// thread (8 and 7 CTAs; two heads in flight per thread) measured 75 us for
-// 16,384 tokens of 40/8 heads (5.4 TB/s) and 71 us with the cache for 8192 of
-// 64/8 (4.5 TB/s), against 87 and 79 with 92 to 96 registers and four heads.
+// eight pairs in registers. What counts then is how many loads are in flight:
+// each thread runs a ring of four heads of asynchronous copies into shared
+// memory, private to it, so no barrier stands between them, and 8 (with the
+// cache 7) CTAs fit an SM. 16,384 tokens of 40/8 heads take 62.7 us (6.4 TB/s),
+// 8192 of 64/8 with the cache 55.7 us (5.7 TB/s), against 75 and 71 with two
+// heads in registers. Rings of 2, 3 and 6 heads: 67.1, 65.0 and 66.2 us with
+// the cache where 4 took 64.6 (half of its accesses then half-sectors).
 #pragma once
 
 #include "pda_kernels.cuh"
@@ -61,16 +63,14 @@ struct RopeItem {
 };
 
 // Dims of item j's two vectors. With R a multiple of 16 a head is 8 items:
-// item j < R/16 holds pairs 8j .. 8j+7 (half layout: dims 8j.. and 8j + R/2..;
-// interleaved: dims 16j .. 16j+15), the others dims that pass through.
-__device__ __forceinline__ void rope_item_dims(int j, int pairs, bool interleaved, int& da, int& db) {
-  if (j >= pairs / 8 || interleaved) {
-    da = 16 * j;
-    db = 16 * j + 8;
-  } else {
-    da = 8 * j;
-    db = 8 * j + pairs;
-  }
+// item j < R/16 holds dims 8j.. and 8j + R/2.. of the rotated part (the two
+// sides of pairs 8j .. 8j+7; interleaved, pairs 4j .. 4j+3 and R/4 + 4j ..),
+// the others dims of the rest, likewise in two halves: lanes next to each
+// other touch vectors next to each other, so an access fills its sectors.
+__device__ __forceinline__ void rope_item_dims(int j, int pairs, int& da, int& db) {
+  const bool turned = j < pairs / 8;
+  da = turned ? 8 * j : pairs + 8 * j;
+  db = da + (turned ? pairs : kHeadDim / 2 - pairs);
 }
 
 // Rotates item j in fp32: r[0..7] vector a's dims, r[8..15] vector b's. t:
@@ -124,18 +124,28 @@ __device__ __forceinline__ uint2 quantize8(const float* r, float scale) {
   return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
+// The thread's cp.async copies since the last call form a group; waits until
+// at most n groups are in flight.
+__device__ __forceinline__ void cp_async_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+}
+
 // kTok tokens x one head group per 128-thread CTA. 8 threads hold one head
 // of one token, so 16 / kTok heads go side by side.
+constexpr int kRopeDepth = 4;           // heads in flight per thread
 template <int kTok, bool kCache>
 __global__ void __launch_bounds__(kRopeThreads, kCache ? 7 : 8) pda_rope_kernel(const __grid_constant__ RopeParams p) {
   constexpr int kSide = 16 / kTok;     // heads side by side
-  constexpr int kBatch = 2;            // heads in flight per thread
-  // (cos, sin) of a token's pairs: pairs 8j + 2i, 8j + 2i + 1 are entry 8i + j,
-  // so that the 8 threads of a token read entry i of each without conflicts
+  // (cos, sin) of a token's pairs: the two pairs of an item's i-th float4 (see
+  // rope_item_dims) are entry 8i + j, so that the 8 threads of a token read
+  // entry i of each without conflicts
   __shared__ float4 cs[kTok][kRopeMaxPairs / 2];
   __shared__ __align__(16) uint8_t kt[kCache ? kTok : 1][kHeadDim];
   __shared__ __align__(16) uint8_t vt[kCache ? kTok : 1][kHeadDim];
   __shared__ long long slots[kTok];
+  __shared__ uint4 ring[kRopeDepth][2][kRopeThreads];   // each thread's own items
   const int tid = threadIdx.x;
   const int j = tid & 7;
   const int tl = (tid >> 3) % kTok;
@@ -146,27 +156,33 @@ __global__ void __launch_bounds__(kRopeThreads, kCache ? 7 : 8) pda_rope_kernel(
   const int q0 = (int)((long long)p.num_heads * y / p.groups), q1 = (int)((long long)p.num_heads * (y + 1) / p.groups);
   const int k0 = (int)((long long)p.num_kv_heads * y / p.groups);
   const int k1 = (int)((long long)p.num_kv_heads * (y + 1) / p.groups);
-  const int nq = q1 - q0, nh = nq + k1 - k0;
+  const int nq = q1 - q0, nk = nq + k1 - k0;
+  const int nh = kCache ? nk + 1 : nk;   // the cache build: its V head comes last
   const bool il = p.interleaved != 0;
   int da, db;
-  rope_item_dims(j, p.pairs, il, da, db);
+  rope_item_dims(j, p.pairs, da, db);
 
-  auto source = [&](int h) {
-    return h < nq ? p.q + t * p.q_tok + (q0 + h) * p.q_head : p.k + t * p.k_tok + (k0 + h - nq) * p.k_head;
-  };
-  RopeItem x[kBatch];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = h0 + u * kSide + side;
-      if (in && h < nh) {
-        const __nv_bfloat16* s = source(h);
-        x[u].a = *reinterpret_cast<const uint4*>(s + da);
-        x[u].b = *reinterpret_cast<const uint4*>(s + db);
+  const uint32_t mine_at = smem_u32(&ring[0][0][tid]);
+  // one copy group per step, empty past the last head
+  auto load = [&](int step) {
+    const int h = step * kSide + side;
+    if (in && h < nh) {
+      const uint32_t at = mine_at + (uint32_t)((unsigned)step % kRopeDepth) * (2 * kRopeThreads * 16);
+      if (kCache && h >= nk) {
+        const __nv_bfloat16* s = p.v + t * p.v_tok + (long long)y * p.v_head + 8 * j;
+        cp_async_16(at, s);
+        cp_async_16(at + kRopeThreads * 16, s + kHeadDim / 2);
+      } else {
+        const __nv_bfloat16* s =
+            h < nq ? p.q + t * p.q_tok + (q0 + h) * p.q_head : p.k + t * p.k_tok + (k0 + h - nq) * p.k_head;
+        cp_async_16(at, s + da);
+        cp_async_16(at + kRopeThreads * 16, s + db);
       }
     }
+    cp_async_close();
   };
-  load(0);
+#pragma unroll
+  for (int d = 0; d < kRopeDepth; ++d) load(d);
   if constexpr (kCache) {
     if (side == 0 && j == 0) {
       long long slot = in ? __ldg(p.slot_mapping + t) : -1;
@@ -187,7 +203,9 @@ __global__ void __launch_bounds__(kRopeThreads, kCache ? 7 : 8) pda_rope_kernel(
       const int frac = (int)(uint32_t)((turn + 0x80000000ull) >> 32);
       float sn, cn;
       sincospif((float)frac * 4.656612873077393e-10f, &sn, &cn);   // 2^-31 half turns
-      reinterpret_cast<float2*>(&cs[tt][8 * ((pr >> 1) & 3) + (pr >> 3)])[pr & 1] =
+      const int hi = pr >= p.pairs / 2, pp = hi ? pr - p.pairs / 2 : pr;
+      const int e = il ? 8 * (2 * hi + ((pp >> 1) & 1)) + (pp >> 2) : 8 * ((pr >> 1) & 3) + (pr >> 3);
+      reinterpret_cast<float2*>(&cs[tt][e])[pr & 1] =
           make_float2(cn * p.magnitude, sn * p.magnitude);
     }
   }
@@ -197,40 +215,36 @@ __global__ void __launch_bounds__(kRopeThreads, kCache ? 7 : 8) pda_rope_kernel(
 #pragma unroll
   for (int i = 0; i < 4; ++i) mine[i] = cs[tl][8 * i + j];
 
-  for (int h0 = 0; h0 < nh; h0 += kBatch * kSide) {
-    if (h0) load(h0);
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = h0 + u * kSide + side;
-      if (!in || h >= nh) continue;
+  const int steps = (nh + kSide - 1) / kSide;
+  for (int step = 0; step < steps; ++step) {
+    const int h = step * kSide + side;
+    cp_async_wait<kRopeDepth - 1>();
+    if (in && h < nh) {
+      RopeItem x;
+      x.a = ring[(unsigned)step % kRopeDepth][0][tid];
+      x.b = ring[(unsigned)step % kRopeDepth][1][tid];
       float r[16];
-      rope_rotate(x[u], j, p.pairs, il, mine, r);
-      if (kCache && h >= nq) {
-        *reinterpret_cast<uint2*>(&kt[kCache ? tl : 0][da]) = quantize8(r, p.k_scale);
-        *reinterpret_cast<uint2*>(&kt[kCache ? tl : 0][db]) = quantize8(r + 8, p.k_scale);
+      if (kCache && h >= nk) {
+        rope_rotate(x, kHeadDim, p.pairs, il, mine, r);
+        *reinterpret_cast<uint2*>(&vt[kCache ? tl : 0][8 * j]) = quantize8(r, p.v_scale);
+        *reinterpret_cast<uint2*>(&vt[kCache ? tl : 0][kHeadDim / 2 + 8 * j]) = quantize8(r + 8, p.v_scale);
       } else {
-        __nv_bfloat16* d = h < nq ? p.q_out + t * p.qo_tok + (q0 + h) * p.qo_head
-                                  : p.k_out + t * p.ko_tok + (k0 + h - nq) * p.ko_head;
-        *reinterpret_cast<uint4*>(d + da) = pack_bf16x8(r);
-        *reinterpret_cast<uint4*>(d + db) = pack_bf16x8(r + 8);
+        rope_rotate(x, j, p.pairs, il, mine, r);
+        if (kCache && h >= nq) {
+          *reinterpret_cast<uint2*>(&kt[kCache ? tl : 0][da]) = quantize8(r, p.k_scale);
+          *reinterpret_cast<uint2*>(&kt[kCache ? tl : 0][db]) = quantize8(r + 8, p.k_scale);
+        } else {
+          __nv_bfloat16* d = h < nq ? p.q_out + t * p.qo_tok + (q0 + h) * p.qo_head
+                                    : p.k_out + t * p.ko_tok + (k0 + h - nq) * p.ko_head;
+          *reinterpret_cast<uint4*>(d + da) = pack_bf16x8(r);
+          *reinterpret_cast<uint4*>(d + db) = pack_bf16x8(r + 8);
+        }
       }
     }
+    // the stores above waited for this slot's reads
+    load(step + kRopeDepth);
   }
   if constexpr (kCache) {
-    // V comes last: held through the heads, its registers cost a third of the CTAs
-    if (in && side == 0) {
-      const uint4* s = reinterpret_cast<const uint4*>(p.v + t * p.v_tok + (long long)y * p.v_head + 16 * j);
-      const uint4 va = s[0], vb = s[1];
-      const uint32_t w[8] = {va.x, va.y, va.z, va.w, vb.x, vb.y, vb.z, vb.w};
-      float r[16];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r[2 * i] = bf16lo_f32(w[i]);
-        r[2 * i + 1] = bf16hi_f32(w[i]);
-      }
-      *reinterpret_cast<uint2*>(&vt[tl][16 * j]) = quantize8(r, p.v_scale);
-      *reinterpret_cast<uint2*>(&vt[tl][16 * j + 8]) = quantize8(r + 8, p.v_scale);
-    }
     __syncthreads();
     const int bs = p.block_size;
     // K: one 16-byte row of a token per thread
