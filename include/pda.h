@@ -25,6 +25,11 @@
  * page's supports_block_size / customize_spec; GQA ratios up to 8 follow the
  * pull request's "Claims" and "Cut and precision" items.
  *
+ * Around that call: the cache write (pda_reshape_and_cache), rotary positions
+ * alone or with it (pda_rope, pda_rope_and_cache), attention of chunks of new
+ * tokens over the same cache (pda_extend), and the bookkeeping of its pages
+ * (pda_grow_pages and the calls beside it).
+ *
  * Threading and ordering. Every entry point is thread-safe. pda_decode is
  * stream-ordered: it validates on the host, enqueues its kernels on `stream`
  * and returns without synchronising the host, reading device memory from the

@@ -95,7 +95,7 @@ pda_status rope_launch(pda::RopeParams& p, bool vec, cudaStream_t stream) {
   // Else 4, or one for the steps of the fewest tokens, which it spreads over
   // more SMs (us with 4 / one a CTA: 256 tokens of 40/8 heads 4.4 / 6.0, with
   // the cache 32/8 heads 7.0 / 10.1, 64 tokens with it 5.8 / 6.2; 16 tokens of
-  // 40/8 heads 3.6 / 3.3).
+  // 32/8 heads 3.6 / 3.3).
   if (tiles4 * groups >= 128) {
     const dim3 grid((unsigned)tiles4, (unsigned)p.groups);
     pda::pda_rope_kernel<4, kCache><<<grid, pda::kRopeThreads, 0, stream>>>(p);
