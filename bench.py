@@ -128,14 +128,13 @@ def kernel_source_sha() -> str:
     """
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "paged_kv_decode_pda_gb300", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith(".cuh"):
-            with open(os.path.join(csrc, name), encoding="utf-8") as f:
-                text = f.read()
-            text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-            text = re.sub(r"//[^\n]*", "", text)
-            text = "\n".join(line.rstrip() for line in text.splitlines() if line.strip())
-            h.update(name.encode() + b"\0" + text.encode())
+    for name in ("pda_device.cuh", "pda_kernels.cuh"):
+        with open(os.path.join(csrc, name), encoding="utf-8") as f:
+            text = f.read()
+        text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+        text = re.sub(r"//[^\n]*", "", text)
+        text = "\n".join(line.rstrip() for line in text.splitlines() if line.strip())
+        h.update(name.encode() + b"\0" + text.encode())
     return h.hexdigest()[:16]
 
 

@@ -492,9 +492,9 @@ pda_status pda_rope_frequencies(double* inv_freq, double* magnitude, int rot_dim
  *
  * Limits: as pda_decode, and num_tokens * num_heads < 2^31. A call whose
  * tiles do not fill the GPU splits the KV range and needs a workspace per
- * (device, stream) for the partials, grown as pda_decode's is; captured
- * without one (pda_reserve_extend, or an earlier call of the sizes on that
- * stream) it runs unsplit. The result may differ in the last bits with the
+ * (device, stream) for the partials, grown, kept and shared as pda_decode's
+ * is; captured without one (pda_reserve_extend, or an earlier call of the
+ * sizes on that stream) it runs unsplit. The result may differ in the last bits with the
  * split; for one split count it is bitwise reproducible.
  */
 pda_status pda_extend(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,

@@ -17,6 +17,11 @@ pda_status guarded(F&& body) {
   }
 }
 
+// Held over the launches of a call that leaves something in the workspace from
+// one kernel to the next, so that calls of several threads on one stream follow
+// each other whole.
+std::mutex g_ops_mu;
+
 bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
 
 // ------------------------------------------------------------- rotary
@@ -452,6 +457,7 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
                                 max_num_blocks_per_seq, window, &pl);
     if (st != PDA_OK) return st;
     void* ws = nullptr;
+    std::lock_guard<std::mutex> lk(g_ops_mu);
     st = grow_workspace(g_ops_ws, dev, stream, pl.bytes, kQueueBytes, &ws);
     if (st == PDA_ERR_WORKSPACE) {
       // captured without pda_reserve_extend: one split, and the items dealt
@@ -566,6 +572,7 @@ pda_status pda_grow_pages(const pda_page_table* table, const int32_t* rows, cons
     if (n < 0) return PDA_ERR_INVALID_ARG;
     if (n == 0) return PDA_OK;
     if (!rows || !add || misaligned(rows, 4) || misaligned(add, 4)) return PDA_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(g_ops_mu);
     return page_alloc(table, rows, add, nullptr, n, &p, stream);
   });
 }
@@ -580,6 +587,7 @@ pda_status pda_fork_pages(const pda_page_table* table, const int32_t* parents, c
     if (n < 0) return PDA_ERR_INVALID_ARG;
     if (n == 0) return PDA_OK;
     if (!parents || !children || misaligned(parents, 4) || misaligned(children, 4)) return PDA_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> lk(g_ops_mu);
     st = page_alloc(table, parents, nullptr, children, n, &p, stream);
     if (st != PDA_OK) return st;
     pda::CopyParams c = {};
@@ -616,6 +624,7 @@ pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* 
     if (st != PDA_OK || table->num_blocks == 0) return st;
     p.new_ids = new_ids;
     void* ws = nullptr;
+    std::lock_guard<std::mutex> lk(g_ops_mu);
     st = get_page_workspace(stream, page_ws_bytes(table->num_blocks, table->num_rows, 0), &ws);
     if (st != PDA_OK) return st;
     p.ws = page_ws_layout(ws, table->num_blocks, table->num_rows, 0);

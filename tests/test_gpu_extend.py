@@ -1,5 +1,7 @@
 """Attention of new tokens over the paged cache (pda_extend) against the 64-bit reference."""
 
+import threading
+
 import pytest
 import torch
 
@@ -198,7 +200,7 @@ def test_captured_without_a_workspace(seqs):
     c = O.Chunk(seqs, 8, 2 if len(seqs) < 9 else 8, seed=29)
     d = c.to(DEV)
     ref, spread = c.exact()
-    s = torch.cuda.Stream()
+    s = torch.cuda.Stream(priority=-1)   # apart from the streams that other tests draw
     s.wait_stream(torch.cuda.current_stream())
     out = torch.zeros_like(d["q"])
     gr = torch.cuda.CUDAGraph()
@@ -224,7 +226,7 @@ def test_captured_and_on_another_stream(seqs):
     c = O.Chunk(seqs, 8, 2, seed=22)
     d = c.to(DEV)
     ref, spread = c.exact()
-    s = torch.cuda.Stream()
+    s = torch.cuda.Stream(priority=-1)   # apart from the streams that other tests draw
     s.wait_stream(torch.cuda.current_stream())
     out = torch.zeros_like(d["q"])
     with torch.cuda.stream(s):
@@ -251,6 +253,31 @@ def test_block_check_keeps_reads_in_the_pool():
         assert pda.query_device_status() == 64
     finally:
         pda.set_block_check(0)
+
+
+def test_more_tiles_than_are_ordered():
+    c = O.Chunk([(1, 1 + i % 5) for i in range(17000)], 1, 1, seed=31)
+    check(c)
+
+
+def test_threads_on_one_stream():
+    # both batches have an order and cut items, which the workspace hands from kernel to kernel
+    batches = [O.Chunk([(3, 1500 - 300 * i)] * 40, 16, 8, seed=32 + i).to(DEV) for i in range(2)]
+    want = [pda.extend(**d) for d in batches]
+    got = [[], []]
+
+    def work(i):
+        for _ in range(40):
+            got[i].append(pda.extend(**batches[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 40 and all(torch.equal(x, want[i]) for x in got[i])
 
 
 def test_nothing_to_do():

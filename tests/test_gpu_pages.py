@@ -183,7 +183,7 @@ def test_captured_with_a_reserved_workspace():
     b = Both(64, 6, 8)
     b.step("grow", [0, 1], [20, 35])
     parents, kids, rows, add = b.i32([0, 1]), b.i32([2, 3]), b.i32([0, 1, 2, 3]), b.i32([3, 14, 1, 30])
-    s = torch.cuda.Stream()
+    s = torch.cuda.Stream(priority=-1)   # apart from the streams that other tests draw
     s.wait_stream(torch.cuda.current_stream())
     pda.reserve_pages(64, 6, 4, stream=s)
     s.synchronize()
@@ -208,7 +208,7 @@ def test_captured_with_a_reserved_workspace():
 
 def test_a_capture_that_would_grow_the_workspace_is_refused():
     b = Both(64, 6, 8)
-    s = torch.cuda.Stream()
+    s = torch.cuda.Stream(priority=-1)   # apart from the streams that other tests draw
     rows = b.i32([0])
     gr = torch.cuda.CUDAGraph()
     with torch.cuda.graph(gr, stream=s):

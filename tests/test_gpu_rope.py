@@ -185,14 +185,14 @@ def test_captured_and_on_another_stream():
     f, _ = pda.rope_frequencies(128)
     pos = pos.to(DEV)
     want = pda.rope(q, k, pos, f)
-    s = torch.cuda.Stream()
+    s = torch.cuda.Stream(priority=-1)   # apart from the streams that other tests draw
     s.wait_stream(torch.cuda.current_stream())
     qo, ko = torch.empty_like(want[0]), torch.empty_like(want[1])
     pda.rope(q, k, pos, f, q_out=qo, k_out=ko, stream=s)
     s.synchronize()
     assert torch.equal(qo, want[0]) and torch.equal(ko, want[1])
     gr = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(gr):
+    with torch.cuda.graph(gr, stream=s):
         pda.rope(q, k, pos, f, q_out=qo, k_out=ko)
     pos.add_(1)
     gr.replay()
