@@ -41,7 +41,7 @@ def check_bf16(got, ref, x, n, mag, interleaved):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("T,H,Hk,rot", [
     (1, 1, 1, 128), (3, 8, 1, 64), (17, 40, 8, 128), (5, 7, 7, 96), (33, 4, 2, 32), (9, 3, 1, 20), (2, 2, 2, 2),
-    (4, 4, 2, 0), (130, 32, 8, 128), (700, 12, 4, 16)])
+    (4, 4, 2, 0), (130, 32, 8, 128), (700, 12, 4, 16), (2501, 3, 1, 128)])
 def test_rope(T, H, Hk, rot, interleaved):
     qkv, pos = inputs(T, H, Hk, seed=T + rot)
     q, k, _ = split(qkv, H, Hk)
