@@ -3,14 +3,16 @@
 //
 // One CTA holds up to 256 query rows of one (sequence, kv head): the g heads
 // of a group share K and V, so row r is token r / g, head r % g of the tile.
-// With S = Q K^T scaled to log2 units, each row keeps a reference m and
-//   P = 2^(S - m + 7),  l = sum P,  O += P V,   out = v_scale O / l.
-// The reference follows the running maximum lazily: while the maximum grows
-// by at most 2^8 over it, O stays as it is and P grows (P <= 2^15 fits f16;
-// the offset of 7 leaves f16 31 binades below the maximum for small weights);
-// only a larger step rescales O and l. S, l, O and the references are fp32;
-// P rounds once to f16 (2^-11 relative), Q is exact in f16 after a shift of
-// its row by a power of two, K and V are exact in f16.
+// With S = Q K^T and c the row's factor from S to logits in log2 units, each
+// row keeps a reference m, a value of S, and
+//   P = 2^(S c + b),  l = sum P,  O += P V,   out = v_scale O / l,
+// with b close to 7 - m c (extend_exponent). The reference follows the running
+// maximum lazily: while S c + b stays at or below 15, O stays as it is and P
+// grows (P <= 2^15 fits f16; the offset of 7 leaves f16 31 binades below the
+// maximum for small weights); only a larger step rescales O and l. S, l, O and
+// the references are fp32; P rounds once to f16 (2^-11 relative, while l sums
+// it unrounded), Q is exact in f16 after a shift of its row by a power of two,
+// K and V are exact in f16.
 //
 // Roles (16 warps):
 //   warps 0-3, 4-7    softmax of rows 0..127 (block A) and 128..255 (block B):
@@ -125,8 +127,8 @@ constexpr uint32_t kExtSumsOff = kExtItemOff + kExtSlots * 64u;
 constexpr uint32_t kExtMiscOff = kExtSumsOff + 2u * 128u * 8u;   // tensor memory base, abort flag
 constexpr uint32_t kExtSmem = kExtMiscOff + 16u;
 static_assert(kExtSmem <= 232448, "shared memory of one CTA");
-constexpr float kExtOffset = 7.f;                     // P = 2^(S - m + kExtOffset)
-constexpr float kExtSlack = 8.f;                      // growth of the maximum that leaves m as it is
+constexpr float kExtOffset = 7.f;                     // P = 2^(S c + b), b = kExtOffset - m c
+constexpr float kExtLimit = 15.f;                     // largest S c + b that leaves m as it is
 
 // First s with query_starts[s + 1] > row, or num_seqs.
 __device__ __forceinline__ int sequence_of_row(const int32_t* starts, int num_seqs, int row) {
@@ -144,6 +146,25 @@ __device__ __forceinline__ int sequence_of_row(const int32_t* starts, int num_se
 // Token of a tile's row: row / gqa, exact for rows below 256 and gqa <= 8
 // (the inverse is at most 8 / 2^16 too large, relative to 1 / gqa >= 1 / 8).
 __device__ __forceinline__ int token_of(const ExtendParams& p, int row) { return row * p.gqa_inverse >> 16; }
+
+// The exponent of the weights of a row with reference m (finite): S c + b, for
+// logits S c0. Logits may reach 2^126, and b rounds where m c0 is large; what
+// counts is that P at the reference, 2^(m c + b), is a small power of two, and
+// that it is known. Up to 2^28 it is: b is off by half its last place, 8 at
+// most, so m c + b is in [-1, 15]. From there on neighbouring values of S are
+// 16 or more apart in logits, which carry S's 24 bits and no more, so c may be
+// another factor as long as neighbours stay far apart: the power of two that
+// takes m c to [2^29, 2^30), and b = -m c is exact.
+// (Subtracting m from each S instead costs 346 us where this takes 336, for
+// chunks of 2 x 2048 at 8192.)
+__device__ __forceinline__ void extend_exponent(float m, float c0, float& c, float& b) {
+  c = c0;
+  b = fmaf(-m, c0, kExtOffset);
+  if (fabsf(m) * c0 >= 268435456.f) {
+    c = exp2_int(29 - (int)((__float_as_uint(m) >> 23 & 255u) - 127u));
+    b = -m * c;
+  }
+}
 
 // ------------------------------------------------- tensor core primitives
 
@@ -546,6 +567,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       block_tiles(t, x, j, j1, step);
       const bool any = j < j1;
       float m = -INFINITY, l = 0.f;
+      const float c0 = c;
+      float b = 3e38f;                                        // no reference yet: any logit is past the limit
       bool first = true;
       const bool idle = (row & ~31) >= t.rows;                // no row of the warp is live
 #pragma unroll 1
@@ -581,11 +604,16 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
           for (int k = 0; k < 4; ++k)
             mx[k] = i + k + 4 < 128 ? fmaxf(mx[k], fmaxf(__uint_as_float(s[i + k]), __uint_as_float(s[(i + k + 4) & 127])))
                                     : fmaxf(mx[k], __uint_as_float(s[i + k]));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        const bool grow = top > m + kExtSlack;     // m = -inf: the row's first visible token
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const bool grow = fmaf(top, c, b) > kExtLimit;     // no reference yet: at the row's first visible token
         if (__any_sync(0xffffffffu, grow)) {
-          const float mn = grow ? top : m;
-          const float f = (m == -INFINITY || !grow) ? 1.f : fast_exp2(m - mn);
+          float f = 1.f;
+          if (grow) {
+            const float was = m == -INFINITY ? 0.f : fmaf(m, c, b);   // log2 of P at the reference
+            extend_exponent(top, c0, c, b);
+            if (m != -INFINITY) f = fast_exp2((m - top) * c0 + (fmaf(top, c, b) - was));
+            m = top;
+          }
           // O holds earlier tiles' sums (their product is complete: S was issued after it)
           if (!first && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
@@ -599,10 +627,8 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
             }
           }
           l *= f;
-          m = mn;
         }
-        const float b = m == -INFINITY ? 0.f : m - kExtOffset;
-        const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(-b, -b);
+        const uint64_t cc = pack_f32x2(c, c), bb = pack_f32x2(b, b);
         uint64_t s0 = 0, s1 = 0;                         // two fp32 sums each
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -642,23 +668,29 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       const bool live2 = row2 < t.rows;
       const int head2 = t.kvh * p.gqa + row2 - tok2 * p.gqa;
       const size_t orow2 = (size_t)(t.row0 + tok2) * p.num_heads + head2;
-      const float mt = m == -INFINITY ? -INFINITY : m - kExtOffset;
-      float M = mt, den = l, fa = 1.f, fb = 0.f;                // factors of this block's O and the other's
+      // factors of this block's O and the other's, which take P at the reference to 1
+      float top = m, den = l, fa = m == -INFINITY ? 0.f : fast_exp2(-fmaf(m, c, b)), fb = 0.f;
       if (t.both) {
         // Both blocks hold the rows: they exchange (m, l), and each reads
         // half the columns of both O's.
-        sums[x * 128 + row2] = make_float2(mt, l);
+        sums[x * 128 + row2] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kBarSums));
         if (!warp_wait(kBarSums, join_phase)) break;
         const float2 o = sums[(1 - x) * 128 + row2];
-        M = fmaxf(mt, o.x);
-        fa = mt == -INFINITY ? 0.f : fast_exp2(mt - M);
-        fb = o.x == -INFINITY ? 0.f : fast_exp2(o.x - M);
+        top = fmaxf(m, o.x);
+        if (m != -INFINITY) fa *= fast_exp2((m - top) * c0);
+        if (o.x != -INFINITY) {
+          float co, bo;
+          extend_exponent(o.x, c0, co, bo);
+          fb = fast_exp2((o.x - top) * c0 - fmaf(o.x, co, bo));
+        }
         den = l * fa + o.y * fb;
         tc_fence_after();
+      } else {
+        den *= fa;
       }
-      if (mt == -INFINITY) fa = 0.f;
+      const float M = top * c0;                                 // the reference in logits
       // Splits leave (O, reference, l): of a row of the call, or of the tail item's
       const int split = t.split & 255, splits = t.split >> 8;
       const bool partial = splits > 1;

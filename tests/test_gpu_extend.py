@@ -285,3 +285,54 @@ def test_nothing_to_do():
     mark = torch.full((c.T, 4, 128), 7.0, dtype=torch.bfloat16, device=DEV)
     run(c, out=mark)
     assert (mark == 7).all()
+
+
+@pytest.mark.parametrize("lagging", [False, True])
+@pytest.mark.parametrize("power", [12, 20, 24, 25, 26, 30, 60, 125])
+@pytest.mark.parametrize("seqs,H,Hk", [
+    ([(1, 1), (1, 5), (40, 300), (140, 400), (3, 2)], 8, 2), ([(2, 9000)], 8, 1), ([(3, 1500)] * 40, 16, 8)])
+def test_logits_of_any_magnitude(seqs, H, Hk, power, lagging):
+    # All tokens hold one value, so that the output is that value whatever the weights are. Lagging: the tokens' logits
+    # go up by a small step (3.3 in log2 units at 2^25) from one tile of 128 tokens to the next.
+    c = O.Chunk(seqs, H, Hk, seed=40, garbage=False)
+    if lagging:
+        c.q.zero_()
+        c.q[..., 0] = 1 + torch.arange(c.T * H).view(c.T, H) % 128 / 128
+        c.q[..., 127] = 2.0 ** -12
+        kb = torch.zeros(c.NB, Hk, 8, 16, 16)
+        kb[:, :, 0, :, 0] = 448
+        for s, (_, n) in enumerate(seqs):
+            for t in range(0, n, 16):
+                kb[int(c.tables[s, t // 16]), :, 7, :, 15] = t // 128 % 16 * 0.25
+        c.k_cache = kb.to(O.FP8)
+        top = 448.0 * 2
+    else:
+        k = c.k_cache.double().permute(0, 3, 1, 2, 4).reshape(-1, Hk, 128)
+        top = max((c.q[t].double().view(Hk, -1, 128) @ k.permute(1, 2, 0)).abs().max().item() for t in range(0, c.T, 7))
+    c.scale = 2.0 ** power / (top * c.ks)
+    v = torch.linspace(0.5, 2, Hk * 128).view(Hk, 128).to(O.FP8)
+    c.v_cache = v[None, :, :, None].expand(c.NB, Hk, 128, 16).contiguous()
+    want = (v.double() * c.vs).repeat_interleave(H // Hk, 0).expand(c.T, H, 128).clone()
+    for s, (n, L) in enumerate(seqs):
+        want[c.starts[s]:c.starts[s] + max(0, n - L)] = 0
+    O.check_rows(run(c), want, want.abs())
+    O.check_rows(run(c, sinks=torch.full((H,), -2e38, device=DEV)), want, want.abs())
+
+
+@pytest.mark.parametrize("power", [4, 8, 12])
+@pytest.mark.parametrize("seqs", [[(40, 300), (140, 400), (1, 5)], [(2, 9000)]])
+def test_large_logits_against_64_bits(seqs, power):
+    # logits below 2^power. With A the largest sum |q k| * scale, the fp32 sum of 128 products is off by at most
+    # 128 * 2^-24 * A: relative, a weight's error and, once more, their sum's
+    c = O.Chunk(seqs, 8, 2, seed=41)
+    top = big = 0.0
+    for s, (n, _) in enumerate(seqs):
+        q = c.q[c.starts[s]:c.starts[s + 1]].double().view(n, 2, 4, 128).permute(1, 0, 2, 3).reshape(2, -1, 128)
+        k = c.keys_values(s)[0].permute(1, 2, 0)
+        top, big = max(top, (q @ k).abs().max().item()), max(big, (q.abs() @ k.abs()).max().item())
+    c.scale = 2.0 ** power / top
+    ref, spread = c.exact()
+    # a weight below 2^-31 of the largest is below f16's smallest step once 2^7 stands for the largest (its half is
+    # 2^-25, and the largest's place is off by less than one): it may vanish whole where all others meet zeros in V
+    floor = max(n for _, n in seqs) * 2.0 ** -31 * 448 * c.vs
+    O.check_rows(run(c), ref, spread * (1 + 2.0 ** -16 * big * c.scale / O.WEIGHT_ERR) + floor / O.WEIGHT_ERR)
