@@ -534,7 +534,9 @@ pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int n
  * The calls share one workspace per (device, stream), grown like
  * pda_decode's (PDA_ERR_WORKSPACE when it must grow during capture: size it
  * with pda_reserve_pages) and freed by pda_release; calls on one stream run
- * in its order. block_size a multiple of 16 up to 128.
+ * in its order, and those of several threads follow each other whole (no
+ * kernel of one call falls between two of another's). block_size a multiple
+ * of 16 up to 128.
  */
 typedef struct pda_page_table {
   int32_t* ref_counts;

@@ -17,9 +17,10 @@ pda_status guarded(F&& body) {
   }
 }
 
-// Held over the launches of a call that leaves something in the workspace from
-// one kernel to the next, so that calls of several threads on one stream follow
-// each other whole.
+// Held over the launches of a call that leaves something from one kernel to
+// the next, in the workspace or (the page calls) in the tables and counts, and
+// over those of every call that must not fall between: calls of several threads
+// on one stream follow each other whole.
 std::mutex g_ops_mu;
 
 bool misaligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0; }
@@ -548,19 +549,22 @@ pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int n
 
 pda_status pda_copy_pages(const pda_page_array* arrays, int num_arrays, const int32_t* src, const int32_t* dst,
                           int num_pairs, long long num_blocks, cudaStream_t stream) {
-  pda_status st = check_arrays(arrays, num_arrays);
-  if (st != PDA_OK) return st;
-  if (num_pairs < 0 || num_blocks < 0) return PDA_ERR_INVALID_ARG;
-  if (num_blocks > INT32_MAX) return PDA_ERR_UNSUPPORTED;
-  if (num_pairs == 0 || num_arrays == 0) return PDA_OK;
-  if (!src || !dst || misaligned(src, 4) || misaligned(dst, 4)) return PDA_ERR_INVALID_ARG;
-  pda::CopyParams p = {};
-  p.mode = pda::kCopyPairs;
-  p.src = src;
-  p.dst = dst;
-  p.n = num_pairs;
-  p.st.num_blocks = (int)num_blocks;
-  return launch_copies(p, arrays, num_arrays, num_pairs, false, false, stream);
+  return guarded([&]() -> pda_status {
+    const pda_status st = check_arrays(arrays, num_arrays);
+    if (st != PDA_OK) return st;
+    if (num_pairs < 0 || num_blocks < 0) return PDA_ERR_INVALID_ARG;
+    if (num_blocks > INT32_MAX) return PDA_ERR_UNSUPPORTED;
+    if (num_pairs == 0 || num_arrays == 0) return PDA_OK;
+    if (!src || !dst || misaligned(src, 4) || misaligned(dst, 4)) return PDA_ERR_INVALID_ARG;
+    pda::CopyParams p = {};
+    p.mode = pda::kCopyPairs;
+    p.src = src;
+    p.dst = dst;
+    p.n = num_pairs;
+    p.st.num_blocks = (int)num_blocks;
+    std::lock_guard<std::mutex> lk(g_ops_mu);
+    return launch_copies(p, arrays, num_arrays, num_pairs, false, false, stream);
+  });
 }
 
 pda_status pda_grow_pages(const pda_page_table* table, const int32_t* rows, const int32_t* add, int n,
@@ -602,16 +606,19 @@ pda_status pda_fork_pages(const pda_page_table* table, const int32_t* parents, c
 }
 
 pda_status pda_free_pages(const pda_page_table* table, const int32_t* rows, int n, cudaStream_t stream) {
-  pda::FreeParams p = {};
-  const pda_status st = page_state(table, &p.st);
-  if (st != PDA_OK) return st;
-  if (n < 0) return PDA_ERR_INVALID_ARG;
-  if (n == 0) return PDA_OK;
-  if (!rows || misaligned(rows, 4)) return PDA_ERR_INVALID_ARG;
-  p.rows = rows;
-  p.n = n;
-  pda::pda_page_free_kernel<<<(unsigned)n, 128, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  return guarded([&]() -> pda_status {
+    pda::FreeParams p = {};
+    const pda_status st = page_state(table, &p.st);
+    if (st != PDA_OK) return st;
+    if (n < 0) return PDA_ERR_INVALID_ARG;
+    if (n == 0) return PDA_OK;
+    if (!rows || misaligned(rows, 4)) return PDA_ERR_INVALID_ARG;
+    p.rows = rows;
+    p.n = n;
+    std::lock_guard<std::mutex> lk(g_ops_mu);
+    pda::pda_page_free_kernel<<<(unsigned)n, 128, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  });
 }
 
 pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* arrays, int num_arrays,

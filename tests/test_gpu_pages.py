@@ -1,12 +1,17 @@
 """Page bookkeeping on the device against a plain Python reference: every table, count, length and page byte."""
 
+import ctypes
+import os
 import random
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
 import paged_kv_decode_pda_gb300 as pda
+from paged_kv_decode_pda_gb300 import _binding, build
 from tests import ops_util as O
 
 pytestmark = pytest.mark.gpu
@@ -228,3 +233,41 @@ def test_empty_pools_and_lists():
     b.step("compact")
     pda.compact_pages(z, torch.zeros(0, 4, dtype=torch.int32, device=DEV), z, 16)
     b.step("grow", [0, 1], [0, 0])
+
+
+@pytest.fixture(scope="module")
+def threads(tmp_path_factory):
+    """tests/page_threads.c beside the loaded library."""
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not found")
+    pda.load()
+    out = str(tmp_path_factory.mktemp("threads") / "page_threads.so")
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([gcc, "-std=c11", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-pthread",
+                    "-I", os.path.join(build.ROOT, "include"), os.path.join(here, "page_threads.c"), "-o", out,
+                    _binding.LIB_PATH, "-Wl,-rpath," + os.path.dirname(os.path.abspath(_binding.LIB_PATH))], check=True)
+    return ctypes.CDLL(out)
+
+
+def counts_follow_the_table(refs, tables, lens, bs):
+    held = torch.zeros(refs.shape[0], dtype=torch.int32)
+    for row, n in zip(tables.cpu(), lens.tolist()):
+        held.index_add_(0, row[:-(-n // bs)].long(), torch.ones(-(-n // bs), dtype=torch.int32))
+    assert torch.equal(held, refs.cpu())
+
+
+def test_freeing_beside_a_compaction(threads):
+    # threads on one stream: a call of one never falls between two kernels of another's
+    b = Both(4000, 40, 60, arrays=((32,),))
+    pda.grow_pages(*b.dev, b.i32(list(range(40))), b.i32([500 + 7 * r for r in range(40)]), 16)
+    rows, add = b.i32(list(range(0, 40, 3)) + list(range(1, 40, 3)) + [-1]), b.i32([400] * 14)
+    table, _ = _binding._page_table("", *b.dev, 16)
+    array = _binding._PageArray(b.caches[0].data_ptr(), 32)
+    pda.reserve_pages(4000, 40, 14)
+    torch.cuda.synchronize()
+    assert threads.churn_beside_compaction(ctypes.byref(table), ctypes.byref(array), 1, ctypes.c_void_p(rows.data_ptr()),
+                                           ctypes.c_void_p(add.data_ptr()), 14, 5000,
+                                           ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    assert pda.query_device_status() == 0
+    counts_follow_the_table(*b.dev, 16)
