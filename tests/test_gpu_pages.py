@@ -244,7 +244,7 @@ def threads(tmp_path_factory):
     pda.load()
     out = str(tmp_path_factory.mktemp("threads") / "page_threads.so")
     here = os.path.dirname(os.path.abspath(__file__))
-    subprocess.run([gcc, "-std=c11", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-pthread",
+    subprocess.run([gcc, "-std=gnu11", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-pthread",
                     "-I", os.path.join(build.ROOT, "include"), os.path.join(here, "page_threads.c"), "-o", out,
                     _binding.LIB_PATH, "-Wl,-rpath," + os.path.dirname(os.path.abspath(_binding.LIB_PATH))], check=True)
     return ctypes.CDLL(out)
@@ -271,3 +271,56 @@ def test_freeing_beside_a_compaction(threads):
                                            ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
     assert pda.query_device_status() == 0
     counts_follow_the_table(*b.dev, 16)
+
+
+class Decoded:
+    """Rows of random pages whose K is the first and whose V the last of many arrays, so that their copies take many
+    launches; decoded by a thread of its own while a page call runs in another."""
+
+    H, K, NB, ROWS, COLS, ARRAYS = 4, 1, 80, 8, 12, 1300
+
+    def __init__(self, seed):
+        g = torch.Generator().manual_seed(seed)
+        self.k = O.e4m3(self.NB, self.K, 8, 16, 16, g=g).to(DEV)
+        self.v = O.e4m3(self.NB, self.K, 128, 16, g=g).to(DEV)
+        self.rest = torch.zeros(self.ARRAYS - 2, self.NB, 16, dtype=torch.uint8, device=DEV)
+        self.q = torch.randn(self.ROWS, self.H, 128, generator=g).to(torch.bfloat16).to(DEV)
+        i32 = torch.int32
+        self.state = (torch.zeros(self.NB, dtype=i32, device=DEV), torch.zeros(self.ROWS, self.COLS, dtype=i32, device=DEV),
+                      torch.zeros(self.ROWS, dtype=i32, device=DEV))
+
+    def grow(self, rows, add):
+        t = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+        pda.grow_pages(*self.state, t(rows), t(add), 16)
+
+    def free(self, rows):
+        pda.free_pages(*self.state, torch.tensor(rows, dtype=torch.int32, device=DEV), 16)
+
+    def beside(self, threads, parents=None, children=None, loops=60):
+        """The outputs [loops, ROWS, H, 128] of decodes beside the call, and of one behind it."""
+        table, _ = _binding._page_table("", *self.state, 16)
+        bases = [(self.k.data_ptr(), 2048)] + [(x.data_ptr(), 16) for x in self.rest] + [(self.v.data_ptr(), 2048)]
+        arrays = (_binding._PageArray * self.ARRAYS)(*bases)
+        out = torch.full((loops, self.ROWS, self.H, 128), 77.0, dtype=torch.bfloat16, device=DEV)
+        p, c = (None if x is None else torch.tensor(x, dtype=torch.int32, device=DEV) for x in (parents, children))
+        pda.reserve(self.ROWS, self.H, self.K, self.COLS, 16)
+        pda.reserve_pages(self.NB, self.ROWS, self.ROWS)
+        torch.cuda.synchronize()
+        ptr = lambda x: ctypes.c_void_p(None if x is None else x.data_ptr())  # noqa: E731
+        st = threads.decode_beside_pages(ctypes.byref(table), arrays, self.ARRAYS, ptr(p), ptr(c),
+                                         0 if p is None else len(parents), ptr(self.q), self.H, self.K, ptr(out),
+                                         ctypes.c_size_t(out[0].nbytes), loops,
+                                         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert st == 0 and pda.query_device_status() == 0
+        end = pda.decode(self.q, self.k, self.v, self.state[1], self.state[2], 0.1, 0.05, 0.05)
+        return out, end
+
+
+def test_decoding_beside_a_compaction_of_many_arrays(threads):
+    for seed in range(12):
+        d = Decoded(seed)
+        d.grow([0, 1, 2, 3, 4, 5], [160, 150, 170, 90, 150, 111])
+        d.free([0, 1])
+        out, end = d.beside(threads)
+        assert d.state[1][2:6, :6].max() < 36, "nothing was moved"
+        assert (out == end).all(), seed
