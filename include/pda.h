@@ -574,7 +574,8 @@ pda_status pda_grow_pages(const pda_page_table* table, const int32_t* rows, cons
  * a last page that is partly filled is copied, in every array, to a fresh
  * page of the child's own, so that both rows can grow. A row that is a child
  * of the call cannot be a parent in it. arrays (host memory) may be empty: the
- * bookkeeping alone. */
+ * bookkeeping alone. A child's row stays empty until its entries and its page
+ * are in place. */
 pda_status pda_fork_pages(const pda_page_table* table, const int32_t* parents, const int32_t* children, int n,
                           const pda_page_array* arrays, int num_arrays, cudaStream_t stream);
 

@@ -250,9 +250,10 @@ pda_status launch_cluster(void (*fn)(const P), const P& p, int num_blocks, cudaS
 }
 
 // The copies of p's mode over all arrays, kMaxPageArrays a launch. max_pairs:
-// the most pages a call can move. The table entries go with the last launch: a
-// decode of another thread that falls between two of them reads the old ids in
-// arrays that still hold the old pages (targets of copies were free).
+// the most pages a call can move. The table entries go with the last launch
+// (and a fork's lengths with them): a decode of another thread that falls
+// between two of them reads the old ids in arrays that still hold the old pages
+// (targets of copies were free).
 pda_status launch_copies(pda::CopyParams& p, const pda_page_array* arrays, int num_arrays, long long max_pairs,
                          bool table_work, bool after, cudaStream_t stream) {
   for (int a0 = 0; a0 < num_arrays || (a0 == 0 && table_work); a0 += pda::kMaxPageArrays) {

@@ -153,7 +153,9 @@ __device__ __forceinline__ int count_ids(int first, int end, int* warp_sums, Tes
 // past the table row, a page beyond the free ones) set a status bit, change
 // nothing and need no page. Request i is short of pages when the needs of
 // requests 0..i sum past the free pages.
-// Fork leaves the table rows to pda_page_copy_kernel, which has the whole GPU.
+// Fork leaves the table rows to pda_page_copy_kernel, which has the whole GPU,
+// and the children's lengths with them: until the entries and the copied page
+// are there, a child's row is empty to whoever reads it in between.
 struct AllocParams {
   PageState st;
   PageWs ws;
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(kPageThreads) pda_page_alloc_kernel(const Allo
       }
       __syncwarp();
     }
-    if (lane == 0) p.st.lens[r] = q.x;
+    if (lane == 0 && !fork) p.st.lens[r] = q.x;
   }
 }
 
@@ -306,6 +308,7 @@ __global__ void __launch_bounds__(kCopyThreads) pda_page_copy_kernel(const __gri
       const int2 q = __ldcg(p.ws.reqs + i);
       if (q.x < 0) continue;
       const int full = q.x / bs, np = pages_of(q.x, bs);
+      if (j0 == 0 && (tid & 31) == 0) p.st.lens[__ldg(p.children + i)] = q.x;
       const int32_t* from = p.st.tables + (size_t)__ldg(p.rows + i) * MB;
       int32_t* to = p.st.tables + (size_t)__ldg(p.children + i) * MB;
 #pragma unroll

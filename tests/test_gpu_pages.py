@@ -324,3 +324,17 @@ def test_decoding_beside_a_compaction_of_many_arrays(threads):
         out, end = d.beside(threads)
         assert d.state[1][2:6, :6].max() < 36, "nothing was moved"
         assert (out == end).all(), seed
+
+
+def test_decoding_beside_a_fork(threads):
+    # a child's row is empty or whole, never a length with another's pages
+    for seed in range(12):
+        d = Decoded(seed)
+        d.grow([0, 1, 2], [160, 150, 171])
+        d.state[1][4:] = torch.randint(40, 80, (4, 12), dtype=torch.int32, device=DEV)   # left from earlier owners
+        out, end = d.beside(threads, [0, 1, 2, 2], [4, 5, 6, 7])
+        assert torch.equal(d.state[2][4:], d.state[2][[0, 1, 2, 2]])
+        assert (out[:, :3] == end[:3]).all() and (out[:, 3] == 0).all(), seed
+        for r in range(4, 8):
+            for x in out[:, r]:
+                assert (x == 0).all() or torch.equal(x, end[r]), (seed, r)
