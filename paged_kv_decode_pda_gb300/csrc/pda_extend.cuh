@@ -108,8 +108,8 @@ constexpr int kExtSlots = 2;                          // work items known ahead
 enum : int {                                          // barriers (8 bytes each)
   kBarItemFull = 0,                                   // a work item described
   kBarItemFree = kBarItemFull + kExtSlots,            // read by the 14 warps that work on it
-  kBarQ = kBarItemFree + kExtSlots,                   // queries of block A, B stored (4 warps)
-  kBarKFull = kBarQ + 2,                              // f16 tiles (4 warps), up to 2 stages of K, 3 of V
+  kBarQ = kBarItemFree + kExtSlots,                   // queries of block A, B stored (4 warps), a pair per item slot
+  kBarKFull = kBarQ + 2 * kExtSlots,                              // f16 tiles (4 warps), up to 2 stages of K, 3 of V
   kBarKFree = kBarKFull + 2,                          // and let go of by both blocks
   kBarVFull = kBarKFree + 2,
   kBarVFree = kBarVFull + 3,
@@ -421,10 +421,10 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < kExtSlots; ++i) mbar_init(bar(kBarItemFull + i), 1), mbar_init(bar(kBarItemFree + i), 14);
+    for (int i = 0; i < 2 * kExtSlots; ++i) mbar_init(bar(kBarQ + i), 4);
     for (int i = 0; i < 2; ++i) mbar_init(bar(kBarKFull + i), 4), mbar_init(bar(kBarKFree + i), 2);
     for (int i = 0; i < 3; ++i) mbar_init(bar(kBarVFull + i), 4), mbar_init(bar(kBarVFree + i), 2);
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar(kBarQ + x), 4);
       mbar_init(bar(kBarS + x), 1);
       mbar_init(bar(kBarP + 2 * x), 4);
       mbar_init(bar(kBarP + 2 * x + 1), 4);
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarQ + x));
+        if (lane == 0) mbar_arrive(bar(kBarQ + 2 * (it % kExtSlots) + x));
       }
       const int hi = live ? t.pos0 + tok : -1;                // last token of the row
       const int lo = p.window > 0 ? max(0, hi - p.window + 1) : 0;
@@ -903,15 +903,21 @@ __global__ void __launch_bounds__(kExtThreads, 1) pda_extend_kernel(const Extend
       ExtendItem t;
 #pragma unroll 1
       for (int it = 0; ok && next_item(it, t); ++it) {
-        release_item(it, t);
         int j0, j1, step;
         block_tiles(t, x, j0, j1, step);
         const uint32_t qd = operand_desc_lo(sm + kExtQOff + (t.both ? 0u : (uint32_t)x * kExtOperand));
         int prev = -1;          // tile (from jmin) whose P V is due
         bool started = false;   // O holds something
         const int tiles = t.jmax - t.jmin;
-        ok = warp_wait(kBarQ + x, (uint32_t)it & 1u);
-        if (ok && t.both && x) ok = warp_wait(kBarQ, (uint32_t)it & 1u);
+        // The slot is let go of behind these waits: a softmax group whose block
+        // has no tiles goes on without the products, but it can store the
+        // queries of the slot's next item only once this one's have been seen.
+        const int q_bar = kBarQ + 2 * (it % kExtSlots);
+        const uint32_t q_phase = (uint32_t)(it / kExtSlots) & 1u;
+        ok = warp_wait(q_bar + x, q_phase);
+        if (ok && t.both && x) ok = warp_wait(q_bar, q_phase);
+        if (!ok) break;
+        release_item(it, t);
 #pragma unroll 1
         for (int i = 0; ok && i <= tiles; ++i) {             // the last round: what is left
           const int j = t.jmin + i;

@@ -336,3 +336,20 @@ def test_large_logits_against_64_bits(seqs, power):
     # 2^-25, and the largest's place is off by less than one): it may vanish whole where all others meet zeros in V
     floor = max(n for _, n in seqs) * 2.0 ** -31 * 448 * c.vs
     O.check_rows(run(c), ref, spread * (1 + 2.0 ** -16 * big * c.scale / O.WEIGHT_ERR) + floor / O.WEIGHT_ERR)
+
+
+@pytest.mark.parametrize("seqs,H,Hk", [
+    ([(1 + 7 * i % 60, 1 + 7 * i % 60 + i % 50) for i in range(300)], 8, 8),                # one KV tile an item
+    ([(1, 1 + i % 128) if i % 5 else (200 + i % 50, 120 + 40 * (i % 9)) for i in range(240)], 16, 2),
+    ([(150, 40), (1, 100), (3, 5000), (128, 128)] * 30, 8, 4),                              # blocks without tiles
+])
+def test_items_of_few_tiles_in_a_row(seqs, H, Hk):
+    # items that a block passes without a product, next to each other and next to long ones
+    c = O.Chunk(seqs, H, Hk, seed=42)
+    d = c.to(DEV)
+    ref, spread = c.exact()
+    a = pda.extend(**d, out=torch.zeros_like(d["q"]))
+    O.check_rows(a, ref, spread)
+    for _ in range(60):
+        assert torch.equal(pda.extend(**d, out=torch.zeros_like(a)), a)
+    assert pda.query_device_status() == 0
