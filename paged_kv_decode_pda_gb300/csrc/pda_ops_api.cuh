@@ -153,7 +153,8 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
   pl->tile_tokens = 2 * pda::kExtRows / g;
   pl->tiles = num_tokens / pl->tile_tokens + num_seqs;
   long long tokens = (long long)max_blocks * block_size;
-  if (window > 0 && window + pl->tile_tokens + pda::kExtTile < tokens) tokens = window + pl->tile_tokens + pda::kExtTile;
+  const long long seen = (long long)window + pl->tile_tokens + pda::kExtTile;   // of a tile's rows, whole KV tiles
+  if (window > 0 && seen < tokens) tokens = seen;
   const long long kv_tiles = (tokens + pda::kExtTile - 1) / pda::kExtTile;
   const long long ctas = (long long)pl->tiles * num_kv_heads;
   long long n = sms / ctas;

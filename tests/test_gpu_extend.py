@@ -353,3 +353,11 @@ def test_items_of_few_tiles_in_a_row(seqs, H, Hk):
     for _ in range(60):
         assert torch.equal(pda.extend(**d, out=torch.zeros_like(a)), a)
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 200, 1 << 30, 9001])
+def test_a_window_past_the_context_leaves_the_plan_as_it_is(window):
+    # a call that splits the KV range: the same splits, and with them the same bits, as without a window
+    c = O.Chunk([(2, 9000)], 8, 2, seed=43)
+    d = c.to(DEV)
+    assert torch.equal(pda.extend(**d, window=window), pda.extend(**d))
