@@ -493,7 +493,7 @@ pda_status pda_rope_frequencies(double* inv_freq, double* magnitude, int rot_dim
  * Limits: as pda_decode, and num_tokens * num_heads < 2^31. A call whose
  * tiles do not fill the GPU splits the KV range and needs a workspace per
  * (device, stream) for the partials, grown, kept and shared as pda_decode's
- * is; captured without one (pda_reserve_extend, or an earlier call of the
+ * is; captured without one (pda_reserve_extend, or an earlier call of the same
  * sizes on that stream) it runs unsplit. The result may differ in the last bits with the
  * split; for one split count it is bitwise reproducible.
  */
@@ -504,7 +504,8 @@ pda_status pda_extend(void* out, const void* q, const void* k_cache, const void*
                       int out_dtype, float output_scale, cudaStream_t stream);
 
 /* pda_reserve_extend -- size the workspace of (current device, stream) for
- * pda_extend calls of these sizes. It is the page calls' workspace too. */
+ * pda_extend calls of up to num_tokens, num_seqs and max_num_blocks_per_seq,
+ * with these heads and this block size. It is the page calls' workspace too. */
 pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int num_kv_heads,
                               int max_num_blocks_per_seq, int block_size, cudaStream_t stream);
 

@@ -717,7 +717,7 @@ def extend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_
 
 def reserve_extend(num_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq, block_size,
                    stream=None) -> None:
-    """``pda_reserve_extend``: size the workspace for ``extend`` calls of these sizes (before a stream capture)."""
+    """``pda_reserve_extend``: size the workspace for ``extend`` calls up to these sizes (before a stream capture)."""
     _check(load().pda_reserve_extend(num_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq,
                                      block_size, _stream_ptr(stream)), "pda_reserve_extend")
 

@@ -123,6 +123,36 @@ struct ExtendPlan {
   size_t bytes;      // of the work queue, and the order or the split partials
 };
 
+// What the order holds, the order, and the rows of up to one piece per CTA.
+size_t extend_order_bytes(int tiles, int sms) {
+  return 256 + align256((size_t)tiles * sizeof(int2)) +
+         (size_t)sms * 2 * pda::kExtRows * (kHeadDim + 2) * sizeof(float);
+}
+size_t extend_split_bytes(long long rows, long long nsplit) {
+  return (size_t)(rows * nsplit) * (kHeadDim + 2) * sizeof(float);
+}
+
+// The most workspace that a call of up to these sizes (the heads and the block
+// size as given) asks for. Fewer tiles get more splits, so each number of tiles
+// that is split is looked at, with the most tokens that make so many.
+size_t extend_most_bytes(int sms, int num_tokens, int num_seqs, int num_heads, int num_kv_heads, int block_size,
+                         int max_blocks) {
+  const int tile_tokens = 2 * pda::kExtRows / (num_heads / num_kv_heads);
+  const long long tiles = num_tokens / tile_tokens + (long long)num_seqs;
+  const int ordered = (int)(tiles < pda::kExtMaxOrdered ? tiles : pda::kExtMaxOrdered);
+  size_t most = (long long)ordered * num_kv_heads > sms ? extend_order_bytes(ordered, sms) : 0;
+  const long long kv_tiles = ((long long)max_blocks * block_size + pda::kExtTile - 1) / pda::kExtTile;
+  for (long long t = 1; t <= tiles; ++t) {
+    long long n = sms / (t * num_kv_heads);
+    n = n < kv_tiles / 2 ? n : kv_tiles / 2;
+    if (n < 2) break;
+    const long long tokens = t * tile_tokens - 1 < num_tokens ? t * tile_tokens - 1 : num_tokens;
+    const size_t b = extend_split_bytes(tokens * num_heads, n);
+    most = b > most ? b : most;
+  }
+  return kQueueBytes + most;
+}
+
 // The tiles, and how many splits of the KV range each gets: one, unless the
 // tiles of all kv heads leave SMs idle (one CTA per SM); then as many as fill
 // the SMs, of at least two 128-token tiles each at the longest context (GB300,
@@ -163,10 +193,8 @@ pda_status extend_plan(int dev, int num_tokens, int num_seqs, int num_heads, int
   pl->sms = sms;
   pl->ordered = ctas > sms && pl->tiles <= pda::kExtMaxOrdered;   // then there is one split
   pl->bytes = kQueueBytes;
-  if (pl->ordered)  // what the order holds, the order, and the rows of up to one piece per CTA
-    pl->bytes += 256 + align256((size_t)pl->tiles * sizeof(int2)) +
-                 (size_t)sms * 2 * pda::kExtRows * (kHeadDim + 2) * sizeof(float);
-  if (pl->nsplit > 1) pl->bytes += (size_t)num_tokens * num_heads * pl->nsplit * (kHeadDim + 2) * sizeof(float);
+  if (pl->ordered) pl->bytes += extend_order_bytes(pl->tiles, sms);
+  if (pl->nsplit > 1) pl->bytes += extend_split_bytes((long long)num_tokens * num_heads, pl->nsplit);
   return PDA_OK;
 }
 
@@ -547,8 +575,11 @@ pda_status pda_reserve_extend(int num_tokens, int num_seqs, int num_heads, int n
     if (cudaGetDevice(&dev) != cudaSuccess) return PDA_ERR_CUDA;
     ExtendPlan pl;
     st = extend_plan(dev, num_tokens, num_seqs, num_heads, num_kv_heads, block_size, max_num_blocks_per_seq, 0, &pl);
+    if (st != PDA_OK) return st;
+    const size_t bytes = extend_most_bytes(pl.sms, num_tokens, num_seqs, num_heads, num_kv_heads, block_size,
+                                           max_num_blocks_per_seq);
     void* ws = nullptr;
-    return st != PDA_OK ? st : grow_workspace(g_ops_ws, dev, stream, pl.bytes, kQueueBytes, &ws);
+    return grow_workspace(g_ops_ws, dev, stream, bytes, kQueueBytes, &ws);
   });
 }
 

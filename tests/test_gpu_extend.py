@@ -361,3 +361,30 @@ def test_a_window_past_the_context_leaves_the_plan_as_it_is(window):
     c = O.Chunk([(2, 9000)], 8, 2, seed=43)
     d = c.to(DEV)
     assert torch.equal(pda.extend(**d, window=window), pda.extend(**d))
+
+
+@pytest.mark.parametrize("reserved,seqs,H,Hk", [
+    ((24, 12, 600), [(2, 9000)], 8, 8),                  # one split, no order
+    ((4000, 500, 600), [(3, 4000), (1, 9)], 16, 2),      # an order
+    ((4096, 1, 600), [(700, 3000)], 8, 1),               # splits, and more rows than the call's
+    ((4000, 40, 100), [(3, 1500)] * 40, 16, 8),          # an order and pieces, fewer pages
+])
+def test_reserving_covers_smaller_calls(reserved, seqs, H, Hk):
+    # captured on a stream whose workspace was sized for more: the plan, and so the bits, of the call outside a capture
+    c = O.Chunk(seqs, H, Hk, seed=44)
+    d = c.to(DEV)
+    want = pda.extend(**d)
+    T, S, MB = reserved
+    assert T >= c.T and S >= len(seqs) and MB >= c.tables.shape[1]
+    pda.release()
+    s = torch.cuda.Stream(priority=-1)
+    s.wait_stream(torch.cuda.current_stream())
+    pda.reserve_extend(T, S, H, Hk, MB, c.bs, stream=s)
+    s.synchronize()
+    out = torch.zeros_like(d["q"])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        pda.extend(**d, out=out)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
