@@ -586,7 +586,8 @@ pda_status pda_free_pages(const pda_page_table* table, const int32_t* rows, int 
 
 /* pda_compact_pages -- moves pages so that the L held pages are ids 0..L-1:
  * the k-th free id below L takes the k-th held page at or above L, in every
- * array; counts move along, and every table entry in use follows. new_ids
+ * array; counts move along, and every table entry in use follows (one that
+ * names a free page stays as it is and sets bit 128). new_ids
  * (int32 [num_blocks] on the device, or NULL) receives each page's id after
  * the call, for holders outside the table. */
 pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* arrays, int num_arrays,

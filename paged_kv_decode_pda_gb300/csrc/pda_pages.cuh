@@ -40,12 +40,12 @@ struct PageState {
 
 // Workspace of one page call (ints, see page_ws_layout).
 struct PageWs {
-  int32_t* head;      // [0]: live pages, [1]: pages to move (compact)
+  int32_t* head;      // [0]: pages to move (compact)
   int32_t* claims;    // [num_rows]: lowest request that names the row
   int2* reqs;         // [n]: a request's length (-1: refused) and the rank of its first fresh page
   int32_t* fresh;     // [num_blocks]: free ids by rank; compact: target of each moved page
   int32_t* moved;     // [num_blocks]: compact: page to move, by rank
-  int32_t* remap;     // [num_blocks]: compact: new id of a moved page
+  int32_t* remap;     // [num_blocks]: compact: a page's id after it, -1 for a free page
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -265,7 +265,7 @@ struct CopyParams {
   const int32_t* dst;
   const int32_t* rows;       // kCopyFork: parents
   const int32_t* children;
-  int n;                     // pairs or forks (compact: the count is ws.head[1])
+  int n;                     // pairs or forks (compact: the count is ws.head[0])
   int mode;
   int tables;                // this launch does the table entries too
   int num_arrays;
@@ -329,19 +329,23 @@ __global__ void __launch_bounds__(kCopyThreads) pda_page_copy_kernel(const __gri
       }
     }
   } else if (p.tables && p.mode == kCopyCompact) {
-    const int live = __ldcg(p.ws.head);
     const long long items = (long long)p.st.num_rows * MB;
     for (long long it = (long long)blockIdx.x * kCopyThreads + tid; it < items; it += (long long)gridDim.x * kCopyThreads) {
       const int s = (int)(it / MB), j = (int)(it % MB);
       if (j >= pages_of(__ldg(p.st.lens + s), bs)) continue;
       const int id = p.st.tables[it];
-      if ((uint32_t)id >= (uint32_t)p.st.num_blocks)
+      if ((uint32_t)id >= (uint32_t)p.st.num_blocks) {
         atomicOr(&g_status, kStatusBadBlock);
-      else if (id >= live)
-        p.st.tables[it] = __ldcg(p.ws.remap + id);
+        continue;
+      }
+      const int to = __ldcg(p.ws.remap + id);
+      if (to < 0)
+        atomicOr(&g_status, kStatusPageRefused);   // the entry names a free page
+      else if (to != id)
+        p.st.tables[it] = to;
     }
   }
-  const int n = p.mode == kCopyCompact ? __ldcg(p.ws.head + 1) : p.n;
+  const int n = p.mode == kCopyCompact ? __ldcg(p.ws.head) : p.n;
   const long long items = (long long)n * p.num_arrays * p.chunks;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int c = (int)(it % p.chunks);
@@ -427,12 +431,13 @@ __global__ void __launch_bounds__(kPageThreads) pda_page_compact_kernel(const Co
   cluster_prefix(&movers, mover0, all);
   if (nh) each_ranked(first, end, hole0, warp_sums, is_hole, [&](int r, int id) { p.ws.fresh[r] = id; });
   if (nm) each_ranked(first, end, mover0, warp_sums, is_mover, [&](int r, int id) { p.ws.moved[r] = id; });
-  if (p.new_ids)
-    for (int i = first + tid; i < end; i += kPageThreads)
-      if (!is_mover(i)) p.new_ids[i] = i;
+  for (int i = first + tid; i < end; i += kPageThreads) {
+    if (is_mover(i)) continue;
+    p.ws.remap[i] = held(i) ? i : -1;
+    if (p.new_ids) p.new_ids[i] = i;
+  }
   if (me == 0 && tid == 0) {
-    p.ws.head[0] = live;
-    p.ws.head[1] = all;
+    p.ws.head[0] = all;
   }
   cluster_meet();
   grid_dependents_launch();

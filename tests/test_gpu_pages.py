@@ -338,3 +338,24 @@ def test_decoding_beside_a_fork(threads):
         for r in range(4, 8):
             for x in out[:, r]:
                 assert (x == 0).all() or torch.equal(x, end[r]), (seed, r)
+
+
+@pytest.mark.parametrize("NB", [60, 9000])
+@pytest.mark.parametrize("above", [False, True])
+def test_compacting_a_table_that_names_a_free_page(NB, above):
+    # the entry stays as it is and is flagged, whether its page lies below or above the held ones' number
+    b = Both(NB, 4, 8)
+    b.step("grow", [0, 1, 2], [90, 70, 100])
+    b.step("free", [0])
+    stale = NB - 3 if above else 2               # 0..5 are row 0's old pages; 12 are held
+    was = int(b.dev[1][2, 1])
+    b.dev[1][2, 1] = stale
+    b.dev[0][was] = 0
+    b.ref.tables[2][1] = stale
+    b.ref.refs[was] = 0
+    pda.compact_pages(*b.dev, 16, b.caches)
+    assert pda.query_device_status() == 128
+    tables = b.dev[1].tolist()
+    b.ref.compact()
+    b.ref.tables[2][1] = stale
+    assert tables == b.ref.tables and b.dev[0].tolist() == b.ref.refs
