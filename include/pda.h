@@ -483,9 +483,14 @@ pda_status pda_rope_frequencies(double* inv_freq, double* magnitude, int rot_dim
  * With n the rows of sequence s, its row i stands at position
  * p = seq_lens[s] - n + i and attends to tokens max(0, p - window + 1) .. p
  * (window > 0) or 0 .. p (window == 0: no limit); a row with p < 0 (fewer
- * tokens in the cache than rows) gets zeros. Everything else (cache, table,
- * scales, sinks, out_dtype, output_scale, kv_layout, supported set, value
- * range, pda_set_block_check) is as for pda_decode / pda_decode_ex; the
+ * tokens in the cache than rows) gets zeros. The probabilities enter the
+ * second product as one f16 each, half a step (2^-11) off relative to
+ * themselves, where pda_decode takes two f16 parts (2^-22): at most 2^-11 of
+ * the weighted mean of |v| in an output, and probabilities below about 2^-31 of
+ * the row's largest may vanish. The normaliser sums them in fp32, unrounded.
+ * Everything else (cache, table, scales, sinks, out_dtype, output_scale,
+ * kv_layout, supported set, value range, logits' precision,
+ * pda_set_block_check) is as for pda_decode / pda_decode_ex; the
  * first row's position and the window also bound which table entries are
  * read: those of pages that hold a token some row attends to. A NaN among the
  * tokens below seq_lens[s] gives undefined output in the sequence's rows.
@@ -494,8 +499,8 @@ pda_status pda_rope_frequencies(double* inv_freq, double* magnitude, int rot_dim
  * tiles do not fill the GPU splits the KV range and needs a workspace per
  * (device, stream) for the partials, grown, kept and shared as pda_decode's
  * is; captured without one (pda_reserve_extend, or an earlier call of the same
- * sizes on that stream) it runs unsplit. The result may differ in the last bits with the
- * split; for one split count it is bitwise reproducible.
+ * sizes on that stream) it runs unsplit. The result may differ in the last bits
+ * with the split; for one split count it is bitwise reproducible.
  */
 pda_status pda_extend(void* out, const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                       const int32_t* seq_lens, const int32_t* query_starts, int num_tokens, int num_seqs,
