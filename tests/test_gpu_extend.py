@@ -388,3 +388,22 @@ def test_reserving_covers_smaller_calls(reserved, seqs, H, Hk):
     gr.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("seqs,H,Hk", [
+    ([(300, 700), (130, 131)], 8, 2),                # full tiles of both blocks
+    ([(2, 9000), (1, 40)], 8, 2),                    # KV splits
+    ([(3, 1500)] * 40, 16, 8),                       # cut pieces
+    ([(70, 900 + 37 * i) for i in range(20)] + [(0, 5), (4, 2)], 24, 8)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_e4m3_output_on_every_path(seqs, H, Hk, sinks):
+    c = O.Chunk(seqs, H, Hk, seed=45)
+    s = torch.linspace(-2, 4, H) if sinks else None
+    ref, spread = c.exact(sinks=s)
+    scale = ref.abs().max().item() / 600                # some saturate
+    got = run(c, output_scale=scale, sinks=None if s is None else s.to(DEV)).cpu().double()
+    want = (ref / scale).clamp(-448, 448)
+    # as in test_e4m3_output: half an e4m3 step, and the kernel's own error
+    bound = torch.maximum(2.0 ** -4 * want.abs(), torch.tensor(2.0 ** -10, dtype=torch.float64)) \
+        + (1 + 2.0 ** -4) * O.WEIGHT_ERR * spread / scale
+    assert (want.abs() == 448).any() and ((got - want).abs() <= bound).all()

@@ -207,3 +207,26 @@ def test_empty_and_misplaced():
     assert qo.shape == e.shape
     with pytest.raises(pda.PdaError):
         pda.rope(torch.zeros(1, 1, 128, dtype=torch.bfloat16), None, torch.zeros(1, dtype=torch.int64), f)
+
+
+@pytest.mark.parametrize("shuffled", [False, True])
+@pytest.mark.parametrize("lengths,first,bs", [([700, 333, 470], 0, 16), ([900], 5, 64), ([611, 600], 40, 48)])
+def test_runs_that_start_off_the_slot_grid(lengths, first, bs, shuffled):
+    # packed prompts, and a chunk that goes on inside a block: the same bytes as token by token
+    H, Hk, T = 8, 8, sum(lengths)
+    qkv, pos = inputs(T, H, Hk, seed=T)
+    per = [-(-(first + n) // bs) for n in lengths]
+    NB = sum(per) + 2
+    blocks = torch.randperm(NB, generator=torch.Generator().manual_seed(1))
+    slots = torch.cat([blocks[sum(per[:i]):][(first + torch.arange(n)) // bs] * bs + (first + torch.arange(n)) % bs
+                       for i, n in enumerate(lengths)])
+    f = pda.rope_frequencies(128)[0]
+    q, k, v = split(qkv.to(DEV), H, Hk)
+    pos, slots = pos.to(DEV), slots.to(DEV)
+    shape = (NB, Hk, bs // 16, 128, 16) if shuffled else (NB, Hk, 128, bs)
+    caches = [[torch.full(s, 0x55, dtype=torch.uint8, device=DEV) for s in ((NB, Hk, 8, bs, 16), shape)] for _ in range(2)]
+    a = pda.rope_and_cache(q, k, v, pos, slots, f, *caches[0], 0.05, 0.03, v_shuffled=shuffled)
+    b = torch.cat([pda.rope_and_cache(q[t:t + 1], k[t:t + 1], v[t:t + 1], pos[t:t + 1], slots[t:t + 1], f, *caches[1],
+                                      0.05, 0.03, v_shuffled=shuffled) for t in range(T)])
+    assert pda.query_device_status() == 0
+    assert torch.equal(a, b) and torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])

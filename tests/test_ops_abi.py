@@ -255,3 +255,20 @@ def test_the_references_agree_with_worked_cases():
     assert p.refs == [1, 0, 1, 0]
     p.compact()
     assert p.refs == [1, 1, 0, 0] and p.tables[1][:2] == [0, 1] and p.moves == [(2, 1)]
+
+
+@pytest.mark.parametrize("rot,base,L,factor,low,high", [
+    (128, 10000.0, 4096.0, 16.0, 1.0, 32.0), (64, 500000.0, 8192.0, 8.0, 1.0, 32.0), (96, 10000.0, 2048.0, 4.0, 2.0, 20.0),
+    (32, 100.0, 4096.0, 4.0, 1.0, 32.0)])
+def test_ramp_between_the_bands(lib, rot, base, L, factor, low, high):
+    # over whole pair indices: from the last that makes `high` turns or more to the first that makes `low` or fewer
+    # (the indices go on past the last pair)
+    f, _ = pda.rope_frequencies(rot, base, scaling=pda.PDA_ROPE_RAMP, factor=factor, original_length=L, low=low, high=high)
+    turns = [L * base ** (-2 * i / rot) / (2 * math.pi) for i in range(rot)]
+    first = max([i for i in range(rot) if turns[i] >= high], default=0)
+    last = min([i for i in range(rot) if turns[i] <= low], default=rot - 1)
+    assert first < last
+    for i, got in enumerate(f.tolist()):
+        t = min(1.0, max(0.0, (i - first) / (last - first)))
+        plain = base ** (-2 * i / rot)
+        assert got == pytest.approx(plain * (1 - t) + plain / factor * t, rel=1e-12), i
