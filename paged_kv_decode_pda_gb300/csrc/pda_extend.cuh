@@ -130,19 +130,6 @@ static_assert(kExtSmem <= 232448, "shared memory of one CTA");
 constexpr float kExtOffset = 7.f;                     // P = 2^(S c + b), b = kExtOffset - m c
 constexpr float kExtLimit = 15.f;                     // largest S c + b that leaves m as it is
 
-// First s with query_starts[s + 1] > row, or num_seqs.
-__device__ __forceinline__ int sequence_of_row(const int32_t* starts, int num_seqs, int row) {
-  int lo = 0, hi = num_seqs;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(starts + mid + 1) > row)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return lo;
-}
-
 // Token of a tile's row: row / gqa, exact for rows below 256 and gqa <= 8
 // (the inverse is at most 8 / 2^16 too large, relative to 1 / gqa >= 1 / 8).
 __device__ __forceinline__ int token_of(const ExtendParams& p, int row) { return row * p.gqa_inverse >> 16; }
