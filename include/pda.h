@@ -426,7 +426,11 @@ pda_status pda_rope(const pda_rope_heads* q, const pda_rope_heads* k, const int6
  * one by an e4m3 step). v->in is not rotated; k->out and v->out are ignored.
  * slot_mapping, the caches, scales, kv_layout, padding (negative slots write
  * nothing to the cache; their q is rotated all the same) and slots past the
- * pool are as for pda_reshape_and_cache, rotary arguments as for pda_rope.
+ * pool are as for pda_reshape_and_cache, rotary arguments as for pda_rope. A
+ * slot that a call names twice ends with bytes of either token, not
+ * necessarily all of one. 16 consecutive tokens (counted from the call's
+ * first) whose slots are consecutive from a multiple of 16 on are written
+ * fastest.
  * q->out must not overlap k->in or v->in.
  */
 pda_status pda_rope_and_cache(const pda_rope_heads* q, const pda_rope_heads* k, const pda_rope_heads* v,
@@ -776,15 +780,16 @@ pda_status pda_reserve(int num_seqs, int num_heads, int num_kv_heads, int max_nu
  * the ones that growth retired included (synchronises each device used),
  * and forget the per-device set-up (SM counts, kernel attributes, the
  * pda_decode_noalloc array's address), which the next call takes again.
- * Graphs that captured a pda_decode* or pda_decode_host call refer to freed
- * memory afterwards and must not be replayed. A cudaDeviceReset destroys
+ * Graphs that captured a pda_decode*, pda_decode_host, pda_extend or page call
+ * refer to freed memory afterwards and must not be replayed. A cudaDeviceReset destroys
  * everything the library set up on that device: call pda_release before
  * resetting a device the library has used.
  */
 pda_status pda_release(void);
 
 /*
- * pda_workspace_info -- the workspace of (current device, stream): *bytes
+ * pda_workspace_info -- the decode workspace of (current device, stream; the
+ * one that pda_extend and the page calls share is apart): *bytes
  * receives its current size (0 when it has none) and *retired the number of
  * smaller buffers it replaced that are still allocated for graphs that
  * captured them. Diagnostic; host only, no synchronisation.

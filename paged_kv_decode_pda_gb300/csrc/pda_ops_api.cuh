@@ -88,9 +88,12 @@ pda_status rope_launch(pda::RopeParams& p, bool vec, cudaStream_t stream) {
   long long groups = kCache ? p.num_kv_heads : (608 + tiles4 - 1) / tiles4;
   if (!kCache && groups > (heads + 7) / 8) groups = (heads + 7) / 8;
   p.groups = (int)groups;
-  // Tokens per CTA. With the cache 16, which store whole V rows where the slots
-  // run on (1024 tokens of 64/8 heads: 12.3 us against 19.0 with 4; 2000
-  // scattered ones 29.1 / 26.8), from two CTAs an SM on.
+  // Tokens per CTA. With the cache 16, which store whole V rows where the CTA's
+  // slots are one run from a multiple of 16 on (us with 16 / 4, 64/8 heads and
+  // 64-token blocks: 1024 tokens 12.3 / 22.7, 8192 57.8 / 132.6), from two CTAs
+  // an SM on. Other slots take 1-byte stores of V either way: 8192 tokens of
+  // packed prompts that start between the CTAs' bounds 110.8 / 133.0, 8192
+  // scattered ones 116.2 / 120.6, 2000 37.4 / 35.3.
   if constexpr (kCache) {
     if (tiles16 * groups >= 304) {
       const dim3 grid((unsigned)tiles16, (unsigned)p.groups);

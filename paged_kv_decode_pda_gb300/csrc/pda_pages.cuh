@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(128) pda_page_free_kernel(const FreeParams p) 
 
 // pda_page_compact_kernel: with L live pages, the k-th free id below L takes
 // the k-th live page at or above L; the two are equally many. Writes the
-// moves (pda_page_copy_kernel makes them) and the counts' new places.
+// moves (pda_page_copy_kernel makes them), every page's id after them (-1 for a
+// free page, which no table entry in use may name) and the counts' new places.
 struct CompactParams {
   PageState st;
   PageWs ws;
