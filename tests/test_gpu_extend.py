@@ -407,3 +407,27 @@ def test_e4m3_output_on_every_path(seqs, H, Hk, sinks):
     bound = torch.maximum(2.0 ** -4 * want.abs(), torch.tensor(2.0 ** -10, dtype=torch.float64)) \
         + (1 + 2.0 ** -4) * O.WEIGHT_ERR * spread / scale
     assert (want.abs() == 448).any() and ((got - want).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("rows,lens", [([3] * 24, [140_000 - 611 * i for i in range(24)]), ([2], [140_000]),
+                                       ([40, 1], [135_000, 90])])
+def test_contexts_past_the_sorted_sizes(rows, lens):
+    # more than 1023 tiles of 128 tokens; against pda_decode, with each row as a sequence of its own
+    H, Hk, bs = 16, 8, 64
+    NB = -(-max(lens) // bs)
+    g = torch.Generator(device=DEV).manual_seed(46)
+    kc, vc = (torch.randint(0, 256, s, generator=g, dtype=torch.uint8, device=DEV).bitwise_and_(0xBF)   # below 2 in size
+              for s in ((NB, Hk, 8, bs, 16), (NB, Hk, 128, bs)))
+    tables = torch.stack([torch.randperm(NB, generator=g, device=DEV) for _ in rows]).to(torch.int32)
+    q = torch.randn(sum(rows), H, 128, generator=g, device=DEV).to(torch.bfloat16)
+    t32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    starts = t32([0] + torch.tensor(rows).cumsum(0).tolist())
+    args = (128 ** -0.5, 0.8, 1.0)
+    got = pda.extend(q, kc, vc, tables, t32(lens), starts, *args)
+    of = torch.repeat_interleave(torch.arange(len(rows)), torch.tensor(rows))
+    at = t32([n - m + 1 + i for n, m in zip(lens, rows) for i in range(m)])
+    want, spread = (pda.decode(q, kc, v, tables[of.to(DEV)].contiguous(), at, *args).double()
+                    for v in (vc, vc.bitwise_and(0x7F)))
+    assert pda.query_device_status() == 0
+    # half a bf16 step on either side, and the weights' error against a spread that is itself rounded to bf16
+    assert ((got.double() - want).abs() <= 2.0 ** -7 * want.abs() + 2 * O.WEIGHT_ERR * spread * (1 + 2.0 ** -8)).all()
