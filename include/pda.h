@@ -607,6 +607,145 @@ pda_status pda_compact_pages(const pda_page_table* table, const pda_page_array* 
  * max_requests requests. */
 pda_status pda_reserve_pages(long long num_blocks, int num_rows, int max_requests, cudaStream_t stream);
 
+/*
+ * Caches in fewer bits: writers that find the scales of what they write,
+ * readers that give a cache's values back, and attention over 4 bits.
+ *
+ * pda_token_rows -- keys or values of new tokens: bf16, the row of (token t, kv
+ * head h) at base + t * token_stride + h * head_stride (strides in elements, the
+ * row's 128 dims contiguous). Rows on the 16-byte grid are read in wide accesses,
+ * others in 2-byte ones.
+ */
+typedef struct pda_token_rows {
+  const void* base;
+  long long token_stride;
+  long long head_stride;
+} pda_token_rows;
+
+/*
+ * pda_reshape_and_cache_slot_scales -- cache write with a scale per slot: the
+ * writer of what pda_decode_slot_scales reads.
+ *
+ *   k_scales, v_scales  fp32 [num_blocks][num_kv_heads][block_size]  written at
+ *                       the slots of the call
+ *
+ * The row of 128 dims of one (token, kv head) gets the scale
+ * max(amax / 448, min_scale), amax over its finite values and the quotient
+ * rounded to binary32, and the codes E4M3(x / scale): the real quotient rounded
+ * to the nearest e4m3 value (ties to even), saturating at +-448 (infinities
+ * included), NaN kept. min_scale keeps rows of zeros from a scale of zero, and
+ * the scales of one context within pda_decode_slot_scales' ratio of 2^15; it
+ * must lie in [2^-100, 2^100].
+ * Layouts (the native one), slot_mapping, padding, slots past the pool and
+ * repeated slots as for pda_reshape_and_cache. Stream-ordered, no workspace,
+ * capturable.
+ */
+pda_status pda_reshape_and_cache_slot_scales(const pda_token_rows* key, const pda_token_rows* value, void* k_cache,
+                                             void* v_cache, float* k_scales, float* v_scales,
+                                             const int64_t* slot_mapping, int num_tokens, int num_kv_heads,
+                                             int head_size, int block_size, long long num_blocks, float min_scale,
+                                             cudaStream_t stream);
+
+/*
+ * The 4-bit cache: uint8 [num_blocks][num_kv_heads][144 * block_size], 16-byte
+ * aligned. The record of a block and kv head holds, one after the other,
+ *   K codes   [block_size][64]    byte j: dims 2j (low nibble) and 2j+1, e2m1
+ *   V codes   [block_size][64]    the same; in slots with bit 1 set the two
+ *                                 32-byte halves change places
+ *   K scales  [block_size][8]     e4m3, one per 16 dims
+ *   V scales  [block_size/16][8][16]  the scale of 16-dim group d of slot t (of
+ *                                 16) at [d][4 * ((t & 3) ^ (t >> 2 & 1)) + (t >> 2)]
+ * and a value is e2m1 * group scale * k_scale (v_scale). e2m1 is OCP FP4 E2M1:
+ * sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6. Pages of this cache are one array to
+ * the page calls (bytes_per_block = num_kv_heads * 144 * block_size).
+ */
+
+/*
+ * pda_reshape_and_cache_fp4 -- write new keys and values into the 4-bit cache.
+ *
+ * A group of 16 dims gets the scale s = E4M3(amax / (6 g)), g the tensor's scale
+ * (k_scale, v_scale) and amax over the group's finite values, and the codes
+ * E2M1(x / (s g)); both from the real quotients, to nearest (ties to even),
+ * saturating (at 448, and at 6: infinities too). A group with s == 0 holds
+ * zeros; a NaN makes its group's scale, and so its 16 values, NaN. g about
+ * max|x| / 2688 uses the scales' range best; it must lie in [2^-100, 2^100].
+ * slot_mapping, padding, slots past the pool as for pda_reshape_and_cache; a slot
+ * that the call names twice ends with bytes of either token, not necessarily all
+ * of one. Stream-ordered, no workspace, capturable.
+ */
+pda_status pda_reshape_and_cache_fp4(const pda_token_rows* key, const pda_token_rows* value, void* kv_cache,
+                                     const int64_t* slot_mapping, int num_tokens, int num_kv_heads, int head_size,
+                                     int block_size, long long num_blocks, float k_scale, float v_scale,
+                                     cudaStream_t stream);
+
+/*
+ * pda_gather_cache -- reads a cache back: the keys and values of sequences'
+ * tokens as bf16, packed.
+ *
+ *   k_out, v_out  bf16 [num_tokens][num_kv_heads][head_size]
+ *   token_starts  int32 [num_seqs + 1], nondecreasing: sequence s fills rows
+ *                 [token_starts[s], token_starts[s + 1]); rows of no sequence
+ *                 are left as they were
+ *   first         int32 [num_seqs], or NULL (zeros): row token_starts[s] + i
+ *                 is the token at position first[s] + i of table row s
+ *
+ * A row whose position lies outside its table row, or whose block id lies
+ * outside [0, num_blocks), gets zeros and sets bit 64 of the device status word.
+ * The value is code * scale in binary32, rounded to bf16. The slot-scale form
+ * reads scales [num_blocks][num_kv_heads][block_size] and the native layout; the
+ * 4-bit form reads records. Pointers 16-byte aligned (tables, starts, first,
+ * scales 4-byte), on the current device. Stream-ordered, no workspace,
+ * capturable.
+ */
+pda_status pda_gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                            const int32_t* block_tables, const int32_t* token_starts, const int32_t* first,
+                            int num_tokens, int num_seqs, int num_kv_heads, int head_size, int block_size,
+                            int max_num_blocks_per_seq, long long num_blocks, float k_scale, float v_scale,
+                            int kv_layout, cudaStream_t stream);
+pda_status pda_gather_cache_slot_scales(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
+                                        const float* k_scales, const float* v_scales, const int32_t* block_tables,
+                                        const int32_t* token_starts, const int32_t* first, int num_tokens,
+                                        int num_seqs, int num_kv_heads, int head_size, int block_size,
+                                        int max_num_blocks_per_seq, long long num_blocks, cudaStream_t stream);
+pda_status pda_gather_cache_fp4(void* k_out, void* v_out, const void* kv_cache, const int32_t* block_tables,
+                                const int32_t* token_starts, const int32_t* first, int num_tokens, int num_seqs,
+                                int num_kv_heads, int head_size, int block_size, int max_num_blocks_per_seq,
+                                long long num_blocks, float k_scale, float v_scale, cudaStream_t stream);
+
+/*
+ * pda_decode_fp4 -- decode attention over the 4-bit cache.
+ *
+ * As pda_decode_ex (queries, tables, lengths, sinks, out_dtype, output_scale,
+ * supported set, value range, logits' precision), with
+ *   kv_cache    the records above; dequantisation is exact up to k_scale and
+ *               v_scale, which enter in binary32
+ *   num_blocks  > 0: ids outside [0, num_blocks) set bit 64 of the device status
+ *               word and read block 0 (that sequence's output is undefined)
+ *   window      > 0: the last `window` tokens only; 0: all
+ * The probabilities enter the second product as one f16 each (at most 2^-11 of
+ * themselves off; those below 2^-24 of the running maximum may vanish); the
+ * normaliser sums them unrounded. A NaN among the tokens that count gives
+ * undefined output in the sequence's heads.
+ *
+ * Any mix of lengths loads the GPU evenly: the tokens of all sequences and kv
+ * heads are cut into equal runs. The cuts move with the batch, so a sequence's
+ * result may differ in the last bits from batch to batch; the same call gives the
+ * same bits. num_seqs * max_num_blocks_per_seq < 2^31.
+ *
+ * Needs a workspace per (device, stream), of one size (some 8 MB): made by the
+ * first call, or by pda_reserve_fp4, which a stream needs before its first
+ * capture (else PDA_ERR_WORKSPACE), and freed by pda_release. Graphs that
+ * captured calls of one stream share it and must not run at the same time.
+ */
+pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
+                          const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_size,
+                          int block_size, int max_num_blocks_per_seq, long long num_blocks, float scale, float k_scale,
+                          float v_scale, int window, const float* sinks, int out_dtype, float output_scale,
+                          cudaStream_t stream);
+
+/* pda_reserve_fp4 -- make pda_decode_fp4's workspace of (current device, stream). */
+pda_status pda_reserve_fp4(cudaStream_t stream);
+
 /* Static text for a status code; never NULL. */
 const char* pda_status_string(int status);
 

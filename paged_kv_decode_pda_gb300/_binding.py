@@ -34,6 +34,10 @@ class _RopeHeads(ctypes.Structure):
                 ("num_heads", ctypes.c_int)]
 
 
+class _TokenRows(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
 class _PageTable(ctypes.Structure):
     _fields_ = [("ref_counts", ctypes.c_void_p), ("block_tables", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
                 ("num_blocks", ctypes.c_longlong), ("num_rows", ctypes.c_int), ("max_blocks", ctypes.c_int),
@@ -84,6 +88,13 @@ SIGNATURES = {
     "pda_fork_pages": (_I, [_P, _P, _P, _I, _P, _I, _P]),
     "pda_free_pages": (_I, [_P, _P, _I, _P]),
     "pda_compact_pages": (_I, [_P, _P, _I, _P, _P]),
+    "pda_reshape_and_cache_slot_scales": (_I, [_P] * 7 + [_I, _I, _I, _I, ctypes.c_longlong, _F, _P]),
+    "pda_reshape_and_cache_fp4": (_I, [_P] * 4 + [_I, _I, _I, _I, ctypes.c_longlong, _F, _F, _P]),
+    "pda_gather_cache": (_I, [_P] * 7 + [_I] * 6 + [ctypes.c_longlong, _F, _F, _I, _P]),
+    "pda_gather_cache_slot_scales": (_I, [_P] * 9 + [_I] * 6 + [ctypes.c_longlong, _P]),
+    "pda_gather_cache_fp4": (_I, [_P] * 6 + [_I] * 6 + [ctypes.c_longlong, _F, _F, _P]),
+    "pda_decode_fp4": (_I, [_P] * 5 + [_I] * 6 + [ctypes.c_longlong, _F, _F, _F, _I, _P, _I, _F, _P]),
+    "pda_reserve_fp4": (_I, [_P]),
     "pda_reserve_pages": (_I, [ctypes.c_longlong, _I, _I, _P]),
 }
 
@@ -830,3 +841,243 @@ def reserve_pages(num_blocks: int, num_rows: int, max_requests: int, stream=None
     """``pda_reserve_pages``: size the page calls' workspace (before a stream capture)."""
     _check(load().pda_reserve_pages(int(num_blocks), int(num_rows), int(max_requests), _stream_ptr(stream)),
            "pda_reserve_pages")
+
+
+# ------------------------------------------------- caches in fewer bits
+
+FP4_TOKEN_BYTES = 144     # K and V of one (token, kv head): codes and group scales
+
+
+def fp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int) -> tuple[int, int, int]:
+    """Shape of the uint8 tensor of a 4-bit cache (layout: ``include/pda.h``)."""
+    return num_blocks, num_kv_heads, FP4_TOKEN_BYTES * block_size
+
+
+def _token_rows(what, key, value, slot_mapping):
+    """(key rows, value rows, T, Hk, D, device index) of checked new tokens ``[T, Hk, 128]`` (any token and head strides)."""
+    if key.dim() != 3 or value.shape != key.shape or key.dtype is not _BF16 or value.dtype is not _BF16:
+        _refuse(what + ": key and value must be bf16 [T, Hk, 128] of one shape")
+    T, Hk, D = key.shape
+    k0, k1, k2 = key.stride()
+    v0, v1, v2 = value.stride()
+    if (k2 != 1 or v2 != 1) and T * Hk:
+        _refuse(what + ": the 128 dims of a row must be contiguous")
+    if slot_mapping.dtype is not _I64 or slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
+        _refuse(what + ": slot_mapping must be contiguous int64 [T]")
+    dev = key.get_device()
+    if dev < 0 or dev != _device() or value.get_device() != dev or slot_mapping.get_device() != dev:
+        _refuse(what + ": tensors must be on the current CUDA device")
+    return _TokenRows(key.data_ptr(), k0, k1), _TokenRows(value.data_ptr(), v0, v1), T, Hk, D, dev
+
+
+def _e4m3_caches(what, k_cache, v_cache, dev, v_shuffled=False):
+    """(NB, Hk, bs) of checked e4m3 caches on device ``dev``."""
+    for t in (k_cache, v_cache):
+        if t.dtype not in _CACHE_TYPES or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(what + ": caches must be contiguous float8_e4m3fn on the current CUDA device")
+    if k_cache.dim() != 5:
+        _refuse(what + ": shapes")
+    NB, Hk, D16, bs, sixteen = k_cache.shape
+    if D16 != 8 or sixteen != 16 or v_cache.shape != ((NB, Hk, bs // 16, 128, 16) if v_shuffled else (NB, Hk, 128, bs)):
+        _refuse(what + ": shapes")
+    return NB, Hk, bs
+
+
+def _scale_tables(what, k_scales, v_scales, shape, dev):
+    for t in (k_scales, v_scales):
+        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(what + ": scale tables must be contiguous float32 [NB, Hk, bs] on the caches' device")
+
+
+def _fp4_cache(what, kv_cache, dev):
+    """(NB, Hk, bs) of a checked 4-bit cache on device ``dev``."""
+    if kv_cache.dim() != 3 or kv_cache.dtype is not torch.uint8 or not kv_cache.is_contiguous() \
+            or kv_cache.get_device() != dev:
+        _refuse(what + ": kv_cache must be contiguous uint8 [NB, Hk, 144 * bs] on the current CUDA device")
+    NB, Hk, n = kv_cache.shape
+    if n == 0 or n % FP4_TOKEN_BYTES:
+        _refuse(what + ": kv_cache must be [NB, Hk, 144 * bs]")
+    return NB, Hk, n // FP4_TOKEN_BYTES
+
+
+def reshape_and_cache_slot_scales(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  k_scales: torch.Tensor, v_scales: torch.Tensor, slot_mapping: torch.Tensor, *,
+                                  min_scale: float = 2.0 ** -20, stream=None) -> None:
+    """``pda_reshape_and_cache_slot_scales``: write new tokens as e4m3, each row with a scale of its own.
+
+    key / value ``[T, Hk, 128]`` bf16 with any token and head strides; the
+    caches (native layout) and ``slot_mapping`` as for ``reshape_and_cache``;
+    k_scales / v_scales float32 ``[NB, Hk, bs]``, as ``decode_slot_scales``
+    reads them. A scale is the row's amax / 448, at least ``min_scale``.
+    """
+    what = "reshape_and_cache_slot_scales"
+    lib = _lib or load()
+    k, v, T, Hk, D, dev = _token_rows(what, key, value, slot_mapping)
+    NB, Hk2, bs = _e4m3_caches(what, k_cache, v_cache, dev)
+    if Hk2 != Hk:
+        _refuse(what + ": shapes")
+    _scale_tables(what, k_scales, v_scales, (NB, Hk, bs), dev)
+    st = lib.pda_reshape_and_cache_slot_scales(ctypes.addressof(k), ctypes.addressof(v), k_cache.data_ptr(),
+                                               v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                                               slot_mapping.data_ptr(), T, Hk, D, bs, NB, min_scale,
+                                               _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_reshape_and_cache_slot_scales")
+
+
+def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, kv_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                          k_scale: float, v_scale: float, *, stream=None) -> None:
+    """``pda_reshape_and_cache_fp4``: write new tokens into a 4-bit cache ``[NB, Hk, 144 * bs]`` (``fp4_cache_shape``).
+
+    key / value and slot_mapping as for ``reshape_and_cache_slot_scales``. Each
+    16 dims get a scale of their own; ``k_scale`` / ``v_scale`` (about
+    max|x| / 2688) are the tensors'.
+    """
+    what = "reshape_and_cache_fp4"
+    lib = _lib or load()
+    k, v, T, Hk, D, dev = _token_rows(what, key, value, slot_mapping)
+    NB, Hk2, bs = _fp4_cache(what, kv_cache, dev)
+    if Hk2 != Hk:
+        _refuse(what + ": shapes")
+    st = lib.pda_reshape_and_cache_fp4(ctypes.addressof(k), ctypes.addressof(v), kv_cache.data_ptr(),
+                                       slot_mapping.data_ptr(), T, Hk, D, bs, NB, k_scale, v_scale,
+                                       _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_reshape_and_cache_fp4")
+
+
+def _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev):
+    """(k_out, v_out, S, MB, first's address) of the checked arguments that the readers share."""
+    if block_tables.dim() != 2:
+        _refuse(what + ": block_tables must be [S, MB]")
+    S, MB = block_tables.shape
+    if token_starts.shape != (S + 1,) or (first is not None and first.shape != (S,)):
+        _refuse(what + ": token_starts must be [S + 1], first [S]")
+    for t in (block_tables, token_starts) if first is None else (block_tables, token_starts, first):
+        if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(what + ": block_tables, token_starts and first must be contiguous int32 on the cache's device")
+    shape = (int(num_tokens), Hk, 128)
+    if shape[0] < 0:
+        _refuse(what + ": num_tokens")
+    outs = []
+    for out in (k_out, v_out):
+        if out is None:
+            out = torch.empty(shape, dtype=_BF16, device=block_tables.device)
+        elif out.shape != shape or out.dtype is not _BF16 or not out.is_contiguous() or out.get_device() != dev:
+            _refuse(what + ": k_out and v_out must be contiguous bf16 [num_tokens, Hk, 128] on the cache's device")
+        outs.append(out)
+    return outs[0], outs[1], S, MB, None if first is None else first.data_ptr()
+
+
+def gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, token_starts: torch.Tensor,
+                 num_tokens: int, k_scale: float, v_scale: float, *, first: torch.Tensor | None = None,
+                 v_shuffled: bool = False, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``pda_gather_cache``: the keys and values of sequences' tokens as bf16 ``[num_tokens, Hk, 128]``, packed.
+
+    Sequence s fills rows ``token_starts[s]`` up to ``token_starts[s + 1]``
+    (int32 ``[S + 1]``) with its tokens from position ``first[s]`` (int32
+    ``[S]``, default 0) on. Rows of no sequence are left as they are in
+    ``k_out`` / ``v_out`` (uninitialised when not given).
+    """
+    what = "gather_cache"
+    lib = _lib or load()
+    dev = _on_device(what, (k_cache, v_cache))
+    NB, Hk, bs = _e4m3_caches(what, k_cache, v_cache, dev, v_shuffled)
+    k, v, S, MB, at = _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev)
+    st = lib.pda_gather_cache(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                              token_starts.data_ptr(), at, k.shape[0], S, Hk, 128, bs, MB, NB, k_scale, v_scale,
+                              PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE,
+                              _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_gather_cache")
+    return k, v
+
+
+def gather_cache_slot_scales(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scales: torch.Tensor,
+                             v_scales: torch.Tensor, block_tables: torch.Tensor, token_starts: torch.Tensor,
+                             num_tokens: int, *, first: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                             v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``pda_gather_cache_slot_scales``: ``gather_cache`` with a scale per slot (float32 ``[NB, Hk, bs]``)."""
+    what = "gather_cache_slot_scales"
+    lib = _lib or load()
+    dev = _on_device(what, (k_cache, v_cache))
+    NB, Hk, bs = _e4m3_caches(what, k_cache, v_cache, dev)
+    _scale_tables(what, k_scales, v_scales, (NB, Hk, bs), dev)
+    k, v, S, MB, at = _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev)
+    st = lib.pda_gather_cache_slot_scales(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                          k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
+                                          token_starts.data_ptr(), at, k.shape[0], S, Hk, 128, bs, MB, NB,
+                                          _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_gather_cache_slot_scales")
+    return k, v
+
+
+def gather_cache_fp4(kv_cache: torch.Tensor, block_tables: torch.Tensor, token_starts: torch.Tensor, num_tokens: int,
+                     k_scale: float, v_scale: float, *, first: torch.Tensor | None = None,
+                     k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                     stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """``pda_gather_cache_fp4``: ``gather_cache`` out of a 4-bit cache ``[NB, Hk, 144 * bs]``."""
+    what = "gather_cache_fp4"
+    lib = _lib or load()
+    dev = _on_device(what, (kv_cache,))
+    NB, Hk, bs = _fp4_cache(what, kv_cache, dev)
+    k, v, S, MB, at = _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev)
+    st = lib.pda_gather_cache_fp4(k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
+                                  token_starts.data_ptr(), at, k.shape[0], S, Hk, 128, bs, MB, NB, k_scale, v_scale,
+                                  _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_gather_cache_fp4")
+    return k, v
+
+
+def decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+               k_scale: float, v_scale: float, *, window: int = 0, sinks: torch.Tensor | None = None,
+               output_scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """``pda_decode_fp4``: decode attention over a 4-bit cache ``[NB, Hk, 144 * bs]``.
+
+    q ``[S, H, 128]`` bf16, block_tables ``[S, MB]`` and seq_lens ``[S]``
+    int32, sinks and output_scale as for ``decode_ex``. ``window`` > 0 limits a
+    sequence to its last ``window`` tokens. The first call on a stream makes its
+    workspace; ``reserve_fp4`` does so ahead of a capture.
+    """
+    what = "decode_fp4"
+    lib = _lib or load()
+    if q.dim() != 3 or block_tables.dim() != 2 or q.dtype is not _BF16:
+        _refuse(what + ": q must be bf16 [S, H, 128], block_tables [S, MB]")
+    dev = q.get_device()
+    if dev < 0 or dev != _device():
+        _refuse(what + ": tensors must be on the current CUDA device")
+    NB, Hk, bs = _fp4_cache(what, kv_cache, dev)
+    S, H, D = q.shape
+    MB = block_tables.shape[1]
+    if block_tables.shape[0] != S or seq_lens.shape != (S,):
+        _refuse(what + ": shapes")
+    for t in (block_tables, seq_lens):
+        if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
+            _refuse(what + ": block_tables and seq_lens must be contiguous int32 on q's device")
+    if not q.is_contiguous():
+        _refuse(what + ": q must be contiguous")
+    fp8 = output_scale is not None
+    want = torch.float8_e4m3fn if fp8 else _BF16
+    if out is None:
+        out = torch.empty((S, H, D), dtype=want, device=q.device)
+    elif out.shape != q.shape or out.dtype not in ((want, torch.uint8) if fp8 else (want,)) or not out.is_contiguous() \
+            or out.get_device() != dev:
+        _refuse(what + ": out")
+    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.shape != (H,) or not sinks.is_contiguous()
+                              or sinks.get_device() != dev):
+        _refuse(what + ": sinks must be a contiguous float32 [num_heads] tensor on q's device")
+    st = lib.pda_decode_fp4(out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
+                            seq_lens.data_ptr(), S, H, Hk, D, bs, MB, NB, scale, k_scale, v_scale, window,
+                            None if sinks is None else sinks.data_ptr(), PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16,
+                            output_scale if fp8 else 1.0, _raw_stream(dev) if stream is None else _stream_ptr(stream))
+    if st:
+        raise PdaError(st, "pda_decode_fp4")
+    return out
+
+
+def reserve_fp4(stream=None) -> None:
+    """``pda_reserve_fp4``: make ``decode_fp4``'s workspace of the stream (before its first capture)."""
+    _check(load().pda_reserve_fp4(_stream_ptr(stream)), "pda_reserve_fp4")

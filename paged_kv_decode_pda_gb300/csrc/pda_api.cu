@@ -15,7 +15,9 @@
 
 #include "../../include/pda.h"
 #include "pda_extend.cuh"
+#include "pda_fp4.cuh"
 #include "pda_kernels.cuh"
+#include "pda_lowbits.cuh"
 #include "pda_pages.cuh"
 #include "pda_rope.cuh"
 
@@ -64,6 +66,7 @@ struct DeviceInfo {
   bool smem_attr_set = false;
   bool extend_set = false;                // pda_extend_kernel checked and opted in
   int extend_sms = 0;
+  int fp4_ctas = 0;                       // resident CTAs of pda_fp4_decode_kernel, all SMs (0: not asked yet)
   // co-resident clusters of n split CTAs: [instance][bs/16][n] (-1: not asked yet)
   int max_clusters[kNumKinds][9][17];
   DeviceInfo() {
@@ -90,6 +93,8 @@ std::map<std::pair<int, cudaStream_t>, Workspace> g_stage;
 // Workspaces of pda_extend's split partials and of the page calls, per
 // (device, stream); under g_ws_mu.
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ops_ws;
+// Workspaces of pda_decode_fp4 (one size), per (device, stream); under g_ws_mu.
+std::map<std::pair<int, cudaStream_t>, Workspace> g_fp4_ws;
 
 // Ring geometry for a block size: a stage holds max(16 * consumer warps, bs)
 // tokens of K and V (whole pages); about kRingBytes of stages per CTA.
@@ -1152,7 +1157,7 @@ pda_status pda_release(void) {
   int prev = 0;
   cudaGetDevice(&prev);
   pda_status st = PDA_OK;
-  for (auto* m : {&g_ws, &g_stage, &g_ops_ws}) {
+  for (auto* m : {&g_ws, &g_stage, &g_ops_ws, &g_fp4_ws}) {
     for (auto& kv : *m) {
       if (!kv.second.ptr) continue;
       if (cudaSetDevice(kv.first.first) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
@@ -1167,6 +1172,7 @@ pda_status pda_release(void) {
   g_ws.clear();
   g_stage.clear();
   g_ops_ws.clear();
+  g_fp4_ws.clear();
   cudaSetDevice(prev);
   // Per-device set-up (SM counts, occupancy, shared-memory opt-ins, the
   // no-allocation scratch address) is taken again on the next call, so a
@@ -1530,3 +1536,4 @@ extern "C" pda_status pda_decode_noalloc(void* out, const void* q, const void* k
 }
 
 #include "pda_ops_api.cuh"
+#include "pda_lowbits_api.cuh"
