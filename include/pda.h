@@ -732,10 +732,13 @@ pda_status pda_gather_cache_fp4(void* k_out, void* v_out, const void* kv_cache, 
  * result may differ in the last bits from batch to batch; the same call gives the
  * same bits. num_seqs * max_num_blocks_per_seq < 2^31.
  *
- * Needs a workspace per (device, stream), of one size (some 8 MB): made by the
+ * Needs a workspace per (device, stream), of one size (some 18 MB): made by the
  * first call, or by pda_reserve_fp4, which a stream needs before its first
  * capture (else PDA_ERR_WORKSPACE), and freed by pda_release. Graphs that
- * captured calls of one stream share it and must not run at the same time.
+ * captured calls of one stream share it and must not run at the same time. A call
+ * that gave up on a wait (bit 1 or 32 of the device status word) leaves its
+ * counters unfinished; pda_query_device_status, which reports the bit, puts them
+ * right.
  */
 pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
                           const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_size,

@@ -7,17 +7,28 @@
 // bandwidth brings 1.8 times the tokens, and converting and multiplying them is
 // what comes close to bounding the kernel.
 //
-// Work. A unit is a (sequence, kv head), its tokens in chunks of whole pages
-// (up to kF4ChunkTokens tokens). All units' chunks, one after the other, are cut
-// into equal runs, one per resident CTA, wherever the cuts fall: every batch (a
-// few long sequences, many ragged ones) loads all SMs alike, with no queue and
-// one launch. A unit cut by a run's end is joined from its pieces (O, m, l) in
-// the workspace by whichever CTA brings the last one, in the pieces' order, so
-// the result does not depend on which CTA that is.
+// Work. A unit is a (sequence, group of kv heads): four heads where the pages have
+// at most 64 tokens, whose records lie side by side, so that one copy brings a
+// page of all four and each consumer warp works on a head of its own, alone; two
+// or one where pages are larger or the heads do not divide, a head's tokens then
+// shared by two or four warps. A unit's tokens go in chunks of whole pages, 256 /
+// heads tokens at most. All units' chunks, one after the other, are cut into runs
+// wherever the cuts fall, one per resident CTA, so that every batch (a few long sequences, many ragged
+// ones) loads all SMs alike. (With smaller runs for the last quarter, taken from a
+// queue as CTAs come free, all CTAs end within 4 % of each other, not 20 %, and the
+// pieces this adds cost as much: 219 against 222 us at 256 x 4096 tokens of 32/8
+// heads, 120 against 119 at 256 x 1 to 4000 of 40/8, 83 against 67 at 2 x 131072 of
+// 64/8.) The pieces (O, m,
+// l) of a unit cut by a run's end go to the workspace, and a second kernel joins
+// them in their order, so the result does not depend on which CTA made which.
+// (Joined in this kernel, by the warp that brings a unit's last piece: 256 x 4096
+// tokens of 32/8 heads took 242 us against 212, as a warp that waits for counts and
+// other warps' rows holds up its CTA's ring.)
 //
-// A CTA. One producer warp copies a chunk's records (K, V and both scales of a
-// page are one contiguous piece: one bulk copy per page) into a ring; four
-// consumer warps take two of its 16-token tiles each:
+// A CTA. One producer warp copies chunks into a ring; four consumer warps take four
+// 16-token tiles of each (what a chunk costs beside its tiles, half a microsecond a
+// CTA, is spread over them: with two a warp 222 us against 200 at 256 x 4096 tokens
+// of 32/8 heads), or two in batches too short for even runs of so large chunks:
 //   S^T = K (16 tokens x 128) Q^T (128 x 8 heads), O^T += V^T (128 x 16) P^T
 // on warp MMAs whose A fragments are made in registers: e2m1 -> f16 by the
 // conversion instruction, times the block's scale, exact (6 significant bits).
@@ -40,27 +51,49 @@
 
 namespace pda {
 
-constexpr int kF4ChunkTokens = 128;
-constexpr int kF4Tiles = 2;                                    // 16-token tiles of a chunk per consumer warp
-static_assert(kF4ChunkTokens == 16 * kF4Tiles * kConsumerWarps, "a chunk's tiles go round the warps");
-constexpr int kF4MaxPages = kF4ChunkTokens / 16;
-constexpr int kF4Stages = 3;
-constexpr int kF4CtasPerSm = 3;
+#ifndef PDA_F4_STAGES
+#define PDA_F4_STAGES 2
+#endif
+#ifndef PDA_F4_CTAS
+#define PDA_F4_CTAS 3
+#endif
+constexpr int kF4Warps = 4;                                    // consumer warps
+constexpr int kF4Threads = kF4Warps * 32 + 32;
+constexpr int kF4CtasPerSm = PDA_F4_CTAS;
+constexpr int kF4Stages = PDA_F4_STAGES;
+constexpr int kF4Tiles = 4;                                    // 16-token tiles of a chunk per consumer warp at most
+constexpr int kF4ChunkTokens = 16 * kF4Tiles * kF4Warps;
 constexpr uint32_t kF4StageBytes = kF4ChunkTokens * kFp4TokenBytes;
-constexpr uint32_t kF4QBytes = kMaxGqa * kHeadDim * 2;
 constexpr int kF4MergeStride = kHeadDim + 4;
-static_assert(kConsumerWarps * kMaxGqa * (kF4MergeStride + 2) * 4 <= kF4StageBytes, "merge rows fit a stage");
-constexpr float kF4Lag = 8.f;                                  // the running maximum's lag, log2
-constexpr int kF4MaxCtas = 1024;
-constexpr int kF4FoldGroup = 16;                               // pieces folded at once where a unit has many
+static_assert(kF4Warps * kMaxGqa * (kF4MergeStride + 2) * 4 <= kF4StageBytes, "merge rows fit a stage");
+constexpr float kF4Lag = 8.f;                                  // the running reference's lag behind the maximum, log2
+constexpr int kF4MaxCtas = 512;
 constexpr int kF4RowFloats = kMaxGqa * (kHeadDim + 2);         // a piece: O rows, then (m, l) pairs
 
-// Workspace: a header that starts at zero, then 4 piece slots per CTA (two of
-// its own, two for folded groups).
+// Workspace: the join's CTAs that are done and the numbers of cut units, zero
+// between calls; the cut units {sequence, first kv head, first run, pieces} in no
+// order, those of few pieces from the front, those of many from the back; then the
+// pieces, two per run and warp.
+constexpr int kF4FewPieces = 8;
 struct Fp4Head {
-  unsigned epoch;                                              // calls finished
-  unsigned done;                                               // CTAs of this call that have left
-  unsigned long long arrived[3 * kF4MaxCtas];                  // epoch + 1 (high), pieces that have come (low)
+  unsigned joined, cuts[2];
+  unsigned pad[61];
+  int4 cut[kF4MaxCtas];
+};
+
+// The runs: C chunks over G CTAs, the first `more` of which take one more.
+struct Fp4Runs {
+  unsigned each, more;
+
+  __device__ __forceinline__ void plan(unsigned C, unsigned G) {
+    each = C / G;
+    more = C - each * G;
+  }
+  __device__ __forceinline__ unsigned first(unsigned r) const { return r * each + min(r, more); }
+  __device__ __forceinline__ unsigned owner(unsigned x) const {   // run of chunk x
+    const unsigned wide = more * (each + 1u);
+    return x < wide ? x / (each + 1u) : more + (x - wide) / each;
+  }
 };
 
 struct Fp4DecodeParams {
@@ -81,6 +114,9 @@ struct Fp4DecodeParams {
   int num_blocks;
   int window;
   int pages_per_chunk;
+  int group;                // kv heads of a unit: 4, 2 or 1
+  int tiles;                // of a chunk per consumer warp: 4 or 2
+  unsigned long long bs_inverse, chunk_inverse;   // ceil(2^40 / d) of block_size and pages_per_chunk
   float logit_scale_log2;   // |scale * k_scale| * log2(e)
   int negate;
   float v_scale;
@@ -88,39 +124,49 @@ struct Fp4DecodeParams {
   float out_scale;
 };
 
-// A chunk's header, written by the producer with its copies.
-struct Fp4Chunk {
-  int s, kvh;
-  int tok0, tokens;         // first token of the chunk's pages, tokens in them (0: an empty sequence)
-  int lo, hi;               // tokens of the sequence that count
-  int flags;
-  int piece, pieces;        // this CTA's piece of the unit
-  int pad;
+// Pages [first, first + n) and tokens [lo, hi) of a sequence.
+struct Fp4Span {
+  int first, n, lo, hi;
 };
-constexpr uint32_t kF4AuxBytes = kF4QBytes + ((sizeof(Fp4Chunk) + 15) / 16) * 16;
 
-// Ring, side entries, barriers (full, empty, consumers), scan sums and flags.
-constexpr uint32_t kF4Smem = 128 + kF4Stages * (kF4StageBytes + kF4AuxBytes) + (2 * kF4Stages + 1) * 8 + 128;
+// A chunk's note, written by the producer with its copies.
+struct __align__(16) Fp4Chunk {
+  int flags;                // kHdrFirst, kHdrLast: of this CTA's part of the unit; kF4Full
+  int t0;                   // the chunk's first token
+  int lo, hi;               // tokens that count (hi: also not past the chunk's pages)
+  int s, kvh;               // sequence, first kv head of the unit
+  int run0, piece, pieces;  // run of the unit's first piece; this one of how many
+  int pad[3];
+};
+constexpr int kF4Full = 8;  // a whole chunk, all of whose tokens count
+
+// Ring, notes, barriers (full, empty, consumers), scan sums and flag,
+// and the chunks before each thread's sequences.
+constexpr uint32_t kF4Smem = 128 + kF4Stages * (kF4StageBytes + (uint32_t)sizeof(Fp4Chunk)) + (2 * kF4Stages + 1) * 8 + 64 +
+                             kF4Threads * 4;
 
 __device__ __forceinline__ int fp4_row_token(int r) {
   const int t = (r >> 1) & 3;
   return ((r & 1) ? (t ^ 1) + 4 : t) + (r & 8);
 }
 
-// Pages [first, first + n) and tokens [lo, hi) of a sequence.
-struct Fp4Span {
-  int first, n, lo, hi;
-};
+// x / d for 0 <= x < 2^31 and d <= 128, with ceil(2^40 / d): off by less than 2^-9
+// before it is cut, and x / d lies at least 2^-7 below the next integer.
+__device__ __forceinline__ int fp4_divide(int x, unsigned long long inverse) {
+  return (int)(((unsigned long long)(unsigned)x * inverse) >> 40);
+}
 __device__ __forceinline__ Fp4Span fp4_span(const Fp4DecodeParams& p, int s) {
   Fp4Span a;
   a.hi = max(0, min(__ldg(p.seq_lens + s), p.max_blocks * p.block_size));
   a.lo = p.window > 0 ? max(0, a.hi - p.window) : 0;
-  a.first = a.lo / p.block_size;
-  a.n = (a.hi + p.block_size - 1) / p.block_size - a.first;
+  a.first = a.lo > 0 ? fp4_divide(a.lo, p.bs_inverse) : 0;
+  a.n = fp4_divide(a.hi + p.block_size - 1, p.bs_inverse) - a.first;
   return a;
 }
 // An empty sequence has one chunk too: somebody writes its zeros.
-__device__ __forceinline__ int fp4_chunks(int pages, int per) { return pages > 0 ? (pages + per - 1) / per : 1; }
+__device__ __forceinline__ int fp4_chunks(const Fp4DecodeParams& p, int pages) {
+  return pages > 0 ? fp4_divide(pages + p.pages_per_chunk - 1, p.chunk_inverse) : 1;
+}
 
 // A consumer warp's share of a unit.
 struct Fp4Worker {
@@ -128,7 +174,8 @@ struct Fp4Worker {
   uint32_t k_off, v_off, ks_off, vs_off;
   uint32_t qf[kChunks][2];
   float lsc0, lsc1;
-  float m0, m1, l0, l1;
+  float m0, m1, l0, l1;     // running reference (log2, at most the lag below the maximum), sums
+  float t0, t1;             // unscaled logits past which the reference moves
   float o[kChunks][4];      // dims 16 gid + 2 mt (0, 1) and 16 gid + 2 mt + 1 (2, 3); heads 2 tig, 2 tig + 1
 
   __device__ __forceinline__ void setup(int lane) {
@@ -140,24 +187,30 @@ struct Fp4Worker {
     v_off = (uint32_t)(tig * 64) + ((uint32_t)(8 * gid) ^ (uint32_t)((tig & 2) << 4));
     vs_off = (uint32_t)(gid * 16 + 4 * tig);
   }
+  // The state of a unit, when one has ended: nothing of it is held in registers
+  // through what ends it.
   __device__ __forceinline__ void reset() {
-    m0 = m1 = -INFINITY;
-    l0 = l1 = 0.f;
+    m0 = m1 = t0 = t1 = -INFINITY;
+    l0 = l1 = lsc0 = lsc1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) qf[i][0] = qf[i][1] = 0u;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
 
-  // Q^T fragments of the row at qrow (shared): k step c's slots (2 tig, 2 tig
-  // + 1), (2 tig + 8, 2 tig + 9) are dims 32 tig + 4c .. + 3. Each row is shifted
-  // by a power of two that puts its largest |q| into [2^14, 2^15).
-  __device__ __forceinline__ void load_q(uint32_t qrow, bool live, float lsc, bool negate) {
+  // Q^T fragments of the row at qrow: k step c's slots (2 tig, 2 tig + 1),
+  // (2 tig + 8, 2 tig + 9) are dims 32 tig + 4c .. + 3. Each row is shifted by a
+  // power of two that puts its largest |q| into [2^14, 2^15).
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* qrow, bool live, float lsc, bool negate) {
     uint2 v[kChunks];
     uint32_t mx = 0u;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-      v[c] = live ? ld_shared_v2(qrow + (uint32_t)(64 * tig + 8 * c)) : make_uint2(0u, 0u);
-      mx = __vmaxu2(mx, v[c].x & 0x7FFF7FFFu);
-      mx = __vmaxu2(mx, v[c].y & 0x7FFF7FFFu);
+    for (int c = 0; c < kChunks; c += 2) {
+      const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(qrow + 32 * tig + 4 * c)) : make_uint4(0u, 0u, 0u, 0u);
+      v[c] = make_uint2(x.x, x.y);
+      v[c + 1] = make_uint2(x.z, x.w);
+      mx = __vmaxu2(__vmaxu2(mx, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+      mx = __vmaxu2(__vmaxu2(mx, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
     }
     mx = max(mx & 0xFFFFu, mx >> 16);
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -173,7 +226,7 @@ struct Fp4Worker {
     lsc1 = lsc * exp2_int(__shfl_sync(0xffffffffu, e, 8 * tig + 4));
   }
 
-  // Logits (log2) of a tile: z[0], z[1] token row gid, z[2], z[3] row gid + 8.
+  // Unscaled logits of a tile: z[0], z[1] token row gid, z[2], z[3] row gid + 8.
   __device__ __forceinline__ void scores(uint32_t k, uint32_t ks, float (&z)[4]) const {
     uint32_t wa[4], wb[4];
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(wa[0]), "=r"(wa[1]), "=r"(wa[2]), "=r"(wa[3]) : "r"(k + k_off));
@@ -182,7 +235,6 @@ struct Fp4Worker {
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(ua) : "r"(ks + ks_off));
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(ub) : "r"(ks + ks_off + 64u));
     const uint32_t sa = e4m3x2_lo_to_f16x2(ua), sb = e4m3x2_lo_to_f16x2(ub);
-    float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // words 0, 1 lie in the row's block 2 tig, words 2, 3 in 2 tig + 1
@@ -195,17 +247,15 @@ struct Fp4Worker {
         a[i] = mul_f16x2(a[i], fa);
         b[i] = mul_f16x2(b[i], fb);
       }
-      mma_f16(sc, a[0], b[0], a[1], b[1], qf[2 * j][0], qf[2 * j][1]);
-      mma_f16(sd, a[2], b[2], a[3], b[3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
+      if (j == 0) mma_f16_first(z, a[0], b[0], a[1], b[1], qf[0][0], qf[0][1]);
+      else mma_f16(z, a[0], b[0], a[1], b[1], qf[2 * j][0], qf[2 * j][1]);
+      mma_f16(z, a[2], b[2], a[3], b[3], qf[2 * j + 1][0], qf[2 * j + 1][1]);
     }
-    z[0] = (sc[0] + sd[0]) * lsc0;
-    z[1] = (sc[1] + sd[1]) * lsc1;
-    z[2] = (sc[2] + sd[2]) * lsc0;
-    z[3] = (sc[3] + sd[3]) * lsc1;
   }
 
   // O^T += V^T P^T of a tile; p in scores' order. [lo, hi): the tile's tokens
   // that count (the others' scales may hold anything, also NaN).
+  template <bool kMasked>
   __device__ __forceinline__ void values(uint32_t v, uint32_t vs, const float (&p)[4], int lo, int hi) {
     const uint32_t pb0 = movmatrix_trans(pack_f16x2(p[0], p[1]));
     const uint32_t pb1 = movmatrix_trans(pack_f16x2(p[2], p[3]));
@@ -215,7 +265,7 @@ struct Fp4Worker {
     const uint2 w3 = ld_shared_v2(v + v_off + 512u + ((tig & 1) ? 192u : 320u));          // (tig ^ 1) + 12
     uint32_t s;
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s) : "r"(vs + vs_off));
-    if (lo > 0 || hi < 16) {
+    if (kMasked && (lo > 0 || hi < 16)) {
       const int t1 = (tig ^ 1) + 4;
       if (tig < lo || tig >= hi) s &= 0xFFFFFF00u;
       if (t1 < lo || t1 >= hi) s &= 0xFFFF00FFu;
@@ -239,30 +289,39 @@ struct Fp4Worker {
     }
   }
 
-  // kN tiles at once; tile i's records at k[i], v[i], ks[i], vs[i], the tokens
-  // [lo[i], hi[i]) of its 16 counting (at least one).
-  template <int kN>
-  __device__ __forceinline__ void tiles(const uint32_t (&k)[kF4Tiles], const uint32_t (&v)[kF4Tiles],
-                                        const uint32_t (&ks)[kF4Tiles], const uint32_t (&vs)[kF4Tiles],
-                                        const int (&lo)[kF4Tiles], const int (&hi)[kF4Tiles]) {
+  // kN tiles at once: tile i's K codes at code[i] (V's v_step further), its K scales
+  // at scale[i] (V's vs_step further); kMasked: only the tokens [lo[i], hi[i]) of
+  // its 16 count (at least one).
+  template <int kN, bool kMasked>
+  __device__ __forceinline__ void tiles(const uint32_t (&code)[kN], const uint32_t (&scale)[kN], uint32_t v_step,
+                                        uint32_t vs_step, const int (&lo)[kN], const int (&hi)[kN]) {
     float z[kN][4];
-    float x0 = -INFINITY, x1 = -INFINITY;
+    bool far = false;   // a logit more than the lag past the running maximum
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      scores(k[i], ks[i], z[i]);
-      if (lo[i] > 0 || hi[i] < 16) {
+      scores(code[i], scale[i], z[i]);
+      if (kMasked && (lo[i] > 0 || hi[i] < 16)) {
         const int ta = fp4_row_token(gid), tb = ta + 8;
         if (ta < lo[i] || ta >= hi[i]) z[i][0] = z[i][1] = -INFINITY;
         if (tb < lo[i] || tb >= hi[i]) z[i][2] = z[i][3] = -INFINITY;
       }
-      x0 = fmaxf(x0, fmaxf(z[i][0], z[i][2]));
-      x1 = fmaxf(x1, fmaxf(z[i][1], z[i][3]));
+      far = far || z[i][0] > t0 || z[i][1] > t1 || z[i][2] > t0 || z[i][3] > t1;
     }
-    if (__any_sync(0xffffffffu, x0 > m0 + kF4Lag || x1 > m1 + kF4Lag)) {
-      const float n0 = fmaxf(m0, warp_max_over_gid(x0)), n1 = fmaxf(m1, warp_max_over_gid(x1));
+    if (__any_sync(0xffffffffu, far)) {
+      float x0 = fmaxf(z[0][0], z[0][2]), x1 = fmaxf(z[0][1], z[0][3]);
+#pragma unroll
+      for (int i = 1; i < kN; ++i) {
+        x0 = fmaxf(x0, fmaxf(z[i][0], z[i][2]));
+        x1 = fmaxf(x1, fmaxf(z[i][1], z[i][3]));
+      }
+      x0 = warp_max_over_gid(x0);
+      x1 = warp_max_over_gid(x1);
+      const float n0 = fmaxf(m0, x0 * lsc0), n1 = fmaxf(m1, x1 * lsc1);
       const float c0 = fast_exp2(m0 - n0), c1 = fast_exp2(m1 - n1);   // 0 while m is -inf
       m0 = n0;
       m1 = n1;
+      t0 = (m0 + kF4Lag) / lsc0;   // lsc 0 (all logits 0): infinite
+      t1 = (m1 + kF4Lag) / lsc1;
       l0 *= c0;
       l1 *= c1;
 #pragma unroll
@@ -275,11 +334,16 @@ struct Fp4Worker {
     }
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      const float p[4] = {fast_exp2(z[i][0] - m0), fast_exp2(z[i][1] - m1), fast_exp2(z[i][2] - m0),
-                          fast_exp2(z[i][3] - m1)};
+      // (one rounding; a masked -inf stays -inf unless lsc is 0, so it is asked for again)
+      float p[4] = {fast_exp2(fmaf(z[i][0], lsc0, -m0)), fast_exp2(fmaf(z[i][1], lsc1, -m1)),
+                    fast_exp2(fmaf(z[i][2], lsc0, -m0)), fast_exp2(fmaf(z[i][3], lsc1, -m1))};
+      if (kMasked) {
+        if (z[i][0] == -INFINITY) p[0] = p[1] = 0.f;
+        if (z[i][2] == -INFINITY) p[2] = p[3] = 0.f;
+      }
       l0 += p[0] + p[2];
       l1 += p[1] + p[3];
-      values(v[i], vs[i], p, lo[i], hi[i]);
+      values<kMasked>(code[i] + v_step, scale[i] + vs_step, p, lo[i], hi[i]);
     }
   }
 
@@ -301,211 +365,228 @@ struct Fp4Worker {
       ml[3] = l1;
     }
   }
+
+  // (m, l, O) straight to a piece's rows.
+  __device__ __forceinline__ void store_piece(float* rows, int g) {
+    l0 = warp_sum_over_gid(l0);
+    l1 = warp_sum_over_gid(l1);
+    const int h = 2 * tig;
+    float* r0 = rows + h * kHeadDim + 16 * gid;
+#pragma unroll
+    for (int mt = 0; mt < kChunks; mt += 2) {
+      if (h < g) __stcg(reinterpret_cast<float4*>(r0 + 2 * mt), make_float4(o[mt][0], o[mt][2], o[mt + 1][0], o[mt + 1][2]));
+      if (h + 1 < g)
+        __stcg(reinterpret_cast<float4*>(r0 + kHeadDim + 2 * mt), make_float4(o[mt][1], o[mt][3], o[mt + 1][1], o[mt + 1][3]));
+    }
+    if (gid == 0) __stcg(reinterpret_cast<float4*>(rows + kMaxGqa * kHeadDim + 4 * tig), make_float4(m0, l0, m1, l1));
+  }
+
+  // The unit's output rows; h0: its first query head.
+  __device__ __forceinline__ void store_out_rows(const Fp4DecodeParams& p, int s, int h0, bool any) {
+    l0 = warp_sum_over_gid(l0);
+    l1 = warp_sum_over_gid(l1);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int hh = 2 * tig + e;
+      if (hh >= p.gqa) continue;
+      const float zs = p.sinks ? __ldg(p.sinks + h0 + hh) * 1.4426950408889634f : -INFINITY;
+      const float M = e ? m1 : m0, den = e ? l1 : l0;
+      const size_t at = ((size_t)s * p.num_heads + h0 + hh) * kHeadDim + 16 * gid;
+      float r[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        r[i] = any ? finish(o[i >> 1][e + 2 * (i & 1)], den, M, zs, p.v_scale) : 0.f;
+      if (p.out_fp8) {
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          c[i] = f32x2_to_e4m3x2(__fdiv_rn(r[4 * i], p.out_scale), __fdiv_rn(r[4 * i + 1], p.out_scale)) |
+                 f32x2_to_e4m3x2(__fdiv_rn(r[4 * i + 2], p.out_scale), __fdiv_rn(r[4 * i + 3], p.out_scale)) << 16;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + at) = make_uint4(c[0], c[1], c[2], c[3]);
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
+        dst[0] = make_uint4(bf16x2_of(r[0], r[1]), bf16x2_of(r[2], r[3]), bf16x2_of(r[4], r[5]), bf16x2_of(r[6], r[7]));
+        dst[1] = make_uint4(bf16x2_of(r[8], r[9]), bf16x2_of(r[10], r[11]), bf16x2_of(r[12], r[13]), bf16x2_of(r[14], r[15]));
+      }
+    }
+  }
 };
 
-// One thread: piece counter i gains one piece; true for the last of `pieces`,
-// which leaves it at zero. A word of another call counts as zero, so a call that
-// gave up leaves nothing to the next.
-__device__ __forceinline__ bool fp4_arrive(Fp4Head* head, int i, unsigned epoch, unsigned pieces) {
-  const unsigned long long mine = (unsigned long long)(epoch + 1u) << 32;
-  unsigned long long old = __ldcg(head->arrived + i);
-  for (;;) {
-    const unsigned come = (old >> 32) == (mine >> 32) ? (unsigned)old + 1u : 1u;
-    const unsigned long long now = come == pieces ? 0ull : mine | come;
-    const unsigned long long seen = atomicCAS(head->arrived + i, old, now);
-    if (seen == old) return come == pieces;
-    old = seen;
-  }
-}
-
-// Slot of piece i of a unit whose first piece is CTA c0's: a CTA's slot 0 holds
-// a piece that an earlier CTA began, slot 1 one that begins with it.
+// A unit's pieces: piece i of one that begins in run c0 is run (c0 + i)'s; a run's
+// slot 0 holds a piece that an earlier run began, slot 1 one that begins with it.
+// Each has room for four kv heads' rows.
 __device__ __forceinline__ int fp4_slot(int c0, int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); }
+constexpr size_t kF4PieceFloats = (size_t)kF4Warps * kF4RowFloats;
+constexpr int kF4Slots = 2 * kF4MaxCtas;
 
-// Head row hh of `n` pieces folded in order (one warp, lane 4 dims).
-template <class Slot>
-__device__ __forceinline__ void fp4_fold(const float* pieces, const Slot& slot, int n, int hh, int lane, float& M,
-                                         float& den, float4& acc) {
-  M = -INFINITY;
-  den = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* r = pieces + (size_t)slot(i) * kF4RowFloats;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + kMaxGqa * kHeadDim) + hh);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(r + hh * kHeadDim) + lane);
-    lse_fold(M, den, acc, ml.x, ml.y, x);
-  }
-}
-__device__ __forceinline__ void fp4_store_piece(float* pieces, int slot, int hh, int lane, float M, float den,
-                                                const float4& acc) {
-  float* r = pieces + (size_t)slot * kF4RowFloats;
-  __stcg(reinterpret_cast<float4*>(r + hh * kHeadDim) + lane, acc);
-  if (lane == 0) __stcg(reinterpret_cast<float2*>(r + kMaxGqa * kHeadDim) + hh, make_float2(M, den));
-}
-
-__global__ void __launch_bounds__(kThreads, kF4CtasPerSm) pda_fp4_decode_kernel(const Fp4DecodeParams p) {
+__global__ void __launch_bounds__(kF4Threads, kF4CtasPerSm) pda_fp4_decode_kernel(const Fp4DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
+  grid_dependents_launch();   // the join kernel may start its launch: it waits for this grid's results
   uint8_t* ring = smem + ((128u - (smem_u32(smem) & 127u)) & 127u);
-  uint8_t* aux = ring + kF4Stages * kF4StageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(aux + kF4Stages * kF4AuxBytes);
-  long long* where = reinterpret_cast<long long*>(bars + 2 * kF4Stages + 1);   // first chunk of the first sequence
-  int* sums = reinterpret_cast<int*>(where + 1);                               // scan [5], first sequence, vote
+  Fp4Chunk* notes = reinterpret_cast<Fp4Chunk*>(ring + kF4Stages * kF4StageBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(notes + kF4Stages);
+  int* sums = reinterpret_cast<int*>(bars + 2 * kF4Stages + 1);   // scan [5]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sums + 8);
-  const uint32_t ring_u32 = smem_u32(ring), aux_u32 = smem_u32(aux);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kF4Stages, cons_bar = full0 + 16u * kF4Stages;
+  unsigned* pre = reinterpret_cast<unsigned*>(sums + 16);
+  const uint32_t ring_u32 = smem_u32(ring);
+  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8u * kF4Stages, cons_bar = empty0 + 8u * kF4Stages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bs = p.block_size, PPC = p.pages_per_chunk, Hk = p.num_kv_heads, g = p.gqa;
+  const int bs = p.block_size, PPC = p.pages_per_chunk, Hk = p.num_kv_heads, g = p.gqa, hw = p.group, tiles = p.tiles;
+  const int HG = Hk / hw;     // units of a sequence
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kF4Stages; ++i) {
       mbar_init(full0 + 8u * i, 1);
-      mbar_init(empty0 + 8u * i, kConsumerWarps);
+      mbar_init(empty0 + 8u * i, kF4Warps);
     }
-    mbar_init(cons_bar, kConsumerWarps);
+    mbar_init(cons_bar, kF4Warps);
     *abort_flag = 0;
-    *where = 0;
-    sums[5] = 0;
     fence_barrier_init();
   }
 
-  // ---- this CTA's run of chunks, and the sequence that it begins in
-  const int per = (p.num_seqs + kThreads - 1) / kThreads;
-  const int s_a = min(p.num_seqs, (int)threadIdx.x * per), s_b = min(p.num_seqs, s_a + per);
-  int mine = 0;
-  for (int s = s_a; s < s_b; ++s) mine += fp4_chunks(fp4_span(p, s).n, PPC);
-  int scan = mine;
+  // ---- the chunks of all sequences: thread i counts sequences [i * each, ...)
+  const int each = (p.num_seqs + kF4Threads - 1) / kF4Threads;
+  const int s_a = min(p.num_seqs, (int)threadIdx.x * each), s_b = min(p.num_seqs, s_a + each);
+  unsigned mine = 0u;
+  for (int s = s_a; s < s_b; ++s) mine += (unsigned)fp4_chunks(p, fp4_span(p, s).n);
+  unsigned scan = mine;
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) {
-    const int x = __shfl_up_sync(0xffffffffu, scan, d);
-    if (lane >= d) scan += x;
+    const unsigned y = __shfl_up_sync(0xffffffffu, scan, d);
+    if (lane >= d) scan += y;
   }
-  if (lane == 31) sums[warp] = scan;
-  const unsigned epoch = __ldcg(&p.head->epoch);
+  if (lane == 31) sums[warp] = (int)scan;
   __syncthreads();
-  int before = scan - mine, all = 0;
+  unsigned before = scan - mine, all = 0u;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
+  for (int w = 0; w < kF4Threads / 32; ++w) {
+    if (w < warp) before += (unsigned)sums[w];
+    all += (unsigned)sums[w];
   }
-  const long long C = (long long)all * Hk;
-  const long long G = (long long)gridDim.x < C ? (long long)gridDim.x : C;
-  const long long cta = blockIdx.x;
-  const long long begin = cta < G ? cta * C / G : 0, end = cta < G ? (cta + 1) * C / G : 0;
-  if (begin < end && begin >= (long long)before * Hk && begin < (long long)(before + mine) * Hk) {
-    long long at = before;
-    for (int s = s_a; s < s_b; ++s) {
-      const int n = fp4_chunks(fp4_span(p, s).n, PPC);
-      if (begin < (at + n) * Hk) {
-        *where = at * Hk;
-        sums[5] = s;
-        break;
-      }
-      at += n;
-    }
-  }
+  pre[threadIdx.x] = before * (unsigned)HG;
+  const unsigned C = all * (unsigned)HG, G = min(gridDim.x, C), run = blockIdx.x;
+  if (run >= G) return;   // (whole CTA)
   __syncthreads();
 
-  if (warp == kConsumerWarps) {
+  if (warp == kF4Warps) {
     // ---------------------------------------------------------- producer
-    int fill = 0;
-    bool ok = true;
-    if (begin < end) {
-      int s = sums[5];
-      Fp4Span a = fp4_span(p, s);
-      int n = fp4_chunks(a.n, PPC);
-      long long unit0 = *where;   // the unit's first chunk
-      int kvh = min((int)((begin - unit0) / n), Hk - 1);
-      unit0 += (long long)kvh * n;
-      int ci = (int)(begin - unit0);
-      bool fresh = true;          // first chunk of a unit (or of the run)
-      int piece = 0, pieces = 1;
-      auto entry = [&](const Fp4Span& b, int seq, int c) {
-        const int pg = c * PPC + lane;
-        return lane < PPC && pg < b.n ? __ldg(p.block_tables + (size_t)seq * p.max_blocks + b.first + pg) : 0;
-      };
-      int block = entry(a, s, ci);
-      for (long long x = begin; x < end; ++x, ++fill) {
-        if (fresh) {
-          const long long c0 = ((unit0 + 1) * G - 1) / C, c1 = ((unit0 + n) * G - 1) / C;
-          piece = (int)(cta - c0);
-          pieces = (int)(c1 - c0) + 1;
+    Fp4Runs runs;
+    runs.plan(C, G);
+    unsigned x = runs.first(run);
+    const unsigned end = runs.first(run + 1u);
+    int s, n, hg, ci;
+    unsigned unit0;                            // the unit's first chunk
+    Fp4Span a;
+    {
+      // the thread whose sequences hold chunk x, then the sequence, 32 at a time
+      int i = 0;
+      for (int j = lane; j - lane < kF4Threads; j += 32) i += __popc(__ballot_sync(0xffffffffu, pre[j] <= x));
+      unsigned at = pre[i - 1];
+      s = (i - 1) * each;
+      for (;;) {
+        const int sl = s + lane;
+        const unsigned m = sl < p.num_seqs ? (unsigned)fp4_chunks(p, fp4_span(p, sl).n) * (unsigned)HG : 0u;
+        unsigned sum = m;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const unsigned y = __shfl_up_sync(0xffffffffu, sum, d);
+          if (lane >= d) sum += y;
         }
-        // the next chunk, its table entries under way while this one's slot is awaited
-        const bool last = ci + 1 == n || x + 1 == end;
-        int s2 = s, kvh2 = kvh, ci2 = ci + 1, n2 = n;
-        long long unit2 = unit0;
-        Fp4Span a2 = a;
-        if (ci2 == n) {
-          ci2 = 0;
-          unit2 += n;
-          if (++kvh2 == Hk) {
-            kvh2 = 0;
-            s2 = min(s + 1, p.num_seqs - 1);
-            if (x + 1 < end) {
-              a2 = fp4_span(p, s2);
-              n2 = fp4_chunks(a2.n, PPC);
-            }
-          }
-        }
-        const int block2 = x + 1 < end ? entry(a2, s2, ci2) : 0;
-
-        const int np = min(PPC, a.n - ci * PPC);
-        const int stage = fill % kF4Stages;
-        const bool got = mbar_wait_bounded(empty0 + 8u * stage, ((uint32_t)(fill / kF4Stages) & 1u) ^ 1u, abort_flag,
-                                           kWaitLimitNs);
-        if (!__all_sync(0xffffffffu, got)) {
-          if (lane == 0) {
-            atomicOr(&g_status, kStatusEmptyWaitTimeout);
-            *abort_flag = 1;
-          }
-          ok = false;
+        const unsigned past = __ballot_sync(0xffffffffu, at + sum > x);
+        if (past != 0u || s + 32 >= p.num_seqs) {
+          const int l = past != 0u ? __ffs((int)past) - 1 : 31;
+          unit0 = at + __shfl_sync(0xffffffffu, sum - m, l);
+          s = min(s + l, p.num_seqs - 1);
           break;
         }
-        const uint32_t bar = full0 + 8u * stage;
-        const uint32_t page_bytes = (uint32_t)(kFp4TokenBytes * bs);
-        if (lane == 0) {
-          Fp4Chunk* hd = reinterpret_cast<Fp4Chunk*>(aux + (size_t)stage * kF4AuxBytes + kF4QBytes);
-          hd->s = s;
-          hd->kvh = kvh;
-          hd->tok0 = (a.first + ci * PPC) * bs;
-          hd->tokens = np * bs;
-          hd->lo = a.lo;
-          hd->hi = a.hi;
-          hd->flags = (fresh ? kHdrFirst : 0) | (last ? kHdrLast : 0);
-          hd->piece = piece;
-          hd->pieces = pieces;
-          if (np > 0) {
-            const uint32_t q_bytes = fresh ? (uint32_t)(g * kHeadDim * 2) : 0u;
-            mbar_arrive_expect_tx(bar, (uint32_t)np * page_bytes + q_bytes);
-            if (fresh)
-              bulk_g2s(aux_u32 + (uint32_t)stage * kF4AuxBytes, p.q + ((size_t)s * p.num_heads + (size_t)kvh * g) * kHeadDim,
-                       q_bytes, bar);
-          } else {
-            mbar_arrive(bar);
-          }
-        }
-        __syncwarp();
-        if (lane < np) {
-          const int b = checked_block(block, (uint32_t)p.num_blocks);
-          bulk_g2s(ring_u32 + (uint32_t)stage * kF4StageBytes + (uint32_t)lane * page_bytes,
-                   p.cache + ((size_t)b * Hk + kvh) * page_bytes, page_bytes, bar);
-        }
-        __syncwarp();
-        fresh = last;
-        s = s2, kvh = kvh2, ci = ci2, n = n2, unit0 = unit2, a = a2, block = block2;
+        at += __shfl_sync(0xffffffffu, sum, 31);
+        s += 32;
       }
+      a = fp4_span(p, s);
+      n = fp4_chunks(p, a.n);
+      hg = min((int)((x - unit0) / (unsigned)n), HG - 1);
+      unit0 += (unsigned)hg * (unsigned)n;
+      ci = (int)(x - unit0);
+    }
+    bool fresh = true, ok = true;              // fresh: first chunk of a unit (or of the run)
+    int run0 = 0, pieces = 1, fill = 0;
+    const uint64_t once = evict_first_policy();   // pages are read once: the pieces stay in L2 instead
+    const uint32_t page_bytes = (uint32_t)(kFp4TokenBytes * bs * hw);   // of the unit's heads, side by side
+    auto entry = [&]() {
+      const int pg = ci * PPC + lane;
+      return lane < PPC && pg < a.n ? __ldg(p.block_tables + (size_t)s * p.max_blocks + a.first + pg) : 0;
+    };
+    int block = entry();
+    uint32_t stage = 0, parity = 1;
+    for (; x < end; ++x, ++fill) {
+      const bool done = x + 1u == end, last = ci + 1 == n || done;
+      if (fresh) {
+        run0 = (int)runs.owner(unit0);
+        pieces = (int)runs.owner(unit0 + (unsigned)n - 1u) - run0 + 1;
+      }
+      // a unit that this run begins and another ends
+      if (done && lane == 0 && pieces > 1 && (int)run == run0) {
+        const int many = pieces > kF4FewPieces ? 1 : 0;
+        const unsigned at = atomicAdd(&p.head->cuts[many], 1u);
+        p.head->cut[many ? kF4MaxCtas - 1u - at : at] = make_int4(s, hg * hw, run0, pieces);
+      }
+      const int np = min(PPC, a.n - ci * PPC), t0 = (a.first + ci * PPC) * bs;
+      const bool got = mbar_wait_bounded(empty0 + 8u * stage, parity, abort_flag, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) {
+          atomicOr(&g_status, kStatusEmptyWaitTimeout);
+          *abort_flag = 1;
+        }
+        ok = false;
+        break;
+      }
+      const uint32_t bar = full0 + 8u * stage;
+      if (fresh) {
+        // the queries that the consumers read when the chunk is there
+        const __nv_bfloat16* q = p.q + ((size_t)s * p.num_heads + (size_t)(hg * hw) * g) * kHeadDim;
+        for (int i = lane; i < hw * g * 2; i += 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + i * 64));
+      }
+      if (lane == 0) {
+        Fp4Chunk* c = notes + stage;
+        const int hi = min(a.hi, t0 + np * bs);
+        c->flags = (fresh ? kHdrFirst : 0) | (last ? kHdrLast : 0) |
+                   (t0 >= a.lo && t0 + 16 * kF4Warps * tiles / hw <= hi ? kF4Full : 0);
+        c->t0 = t0;
+        c->lo = a.lo, c->hi = hi;
+        c->s = s, c->kvh = hg * hw;
+        c->run0 = run0, c->piece = (int)run - run0, c->pieces = pieces;
+        if (np > 0) mbar_arrive_expect_tx(bar, (uint32_t)np * page_bytes);
+        else mbar_arrive(bar);
+      }
+      __syncwarp();
+      if (lane < np) {
+        const int b = checked_block(block, (uint32_t)p.num_blocks);
+        bulk_g2s_hint(ring_u32 + stage * kF4StageBytes + (uint32_t)lane * page_bytes,
+                      p.cache + ((size_t)b * HG + hg) * page_bytes, page_bytes, bar, once);
+      }
+      // the next chunk; its table entries are under way while its stage is awaited
+      fresh = last;
+      if (++ci == n) {
+        ci = 0;
+        unit0 += (unsigned)n;
+        if (++hg == HG) {
+          hg = 0;
+          s = min(s + 1, p.num_seqs - 1);
+          a = fp4_span(p, s);
+          n = fp4_chunks(p, a.n);
+        }
+      }
+      if (!done) block = entry();
+      if (++stage == kF4Stages) stage = 0, parity ^= 1u;
+      __syncwarp();
     }
     if (ok) {
-      // end marker: a header without copies
-      const int stage = fill % kF4Stages;
-      const bool got = mbar_wait_bounded(empty0 + 8u * stage, ((uint32_t)(fill / kF4Stages) & 1u) ^ 1u, abort_flag,
-                                         kWaitLimitNs);
+      // end mark: a note without copies
+      const bool got = mbar_wait_bounded(empty0 + 8u * stage, parity, abort_flag, kWaitLimitNs);
       if (__all_sync(0xffffffffu, got)) {
         if (lane == 0) {
-          reinterpret_cast<Fp4Chunk*>(aux + (size_t)stage * kF4AuxBytes + kF4QBytes)->flags = kHdrEnd;
-          mbar_arrive(full0 + 8u * stage);
+          notes[stage].flags = kHdrEnd;
+            mbar_arrive(full0 + 8u * stage);
         }
         ++fill;
       } else if (lane == 0) {
@@ -521,152 +602,223 @@ __global__ void __launch_bounds__(kThreads, kF4CtasPerSm) pda_fp4_decode_kernel(
         break;
       }
     }
-  } else {
-    // --------------------------------------------------------- consumers
-    Fp4Worker w;
-    w.setup(lane);
-    w.reset();
-    uint32_t cons_phase = 0;
-    const int tpp = bs / 16;
-    // this warp's tiles of a chunk: warp, warp + 4
-    uint32_t code_off[kF4Tiles], scale_off[kF4Tiles];
-#pragma unroll
-    for (int i = 0; i < kF4Tiles; ++i) {
-      const int tile = warp + i * kConsumerWarps;
-      const uint32_t page = (uint32_t)(tile / tpp * (kFp4TokenBytes * bs));
-      code_off[i] = page + (uint32_t)(tile % tpp) * 1024u;
-      scale_off[i] = page + (uint32_t)(128 * bs) + (uint32_t)(tile % tpp) * 128u;
-    }
-    for (int fill = 0;; ++fill) {
-      const int stage = fill % kF4Stages;
-      const bool got = mbar_wait_bounded(full0 + 8u * stage, (uint32_t)(fill / kF4Stages) & 1u, abort_flag, kWaitLimitNs);
-      if (!__all_sync(0xffffffffu, got)) {
-        if (lane == 0) {
-          atomicOr(&g_status, kStatusFullWaitTimeout);
-          *abort_flag = 1;
-        }
-        break;
-      }
-      const uint32_t sbase = ring_u32 + (uint32_t)stage * kF4StageBytes;
-      const Fp4Chunk hd = *reinterpret_cast<const Fp4Chunk*>(aux + (size_t)stage * kF4AuxBytes + kF4QBytes);
-      if (hd.flags & kHdrEnd) break;
-      if (hd.flags & kHdrFirst) {
-        w.reset();
-        if (hd.tokens > 0)
-          w.load_q(aux_u32 + (uint32_t)stage * kF4AuxBytes + (uint32_t)(w.gid < g ? w.gid : 0) * (kHeadDim * 2), w.gid < g,
-                   p.logit_scale_log2, p.negate != 0);
-      }
-      // tiles of the chunk that hold tokens that count, the first ones of k, v, ...
-      uint32_t k[kF4Tiles], v[kF4Tiles], ks[kF4Tiles], vs[kF4Tiles];
-      int lo[kF4Tiles], hi[kF4Tiles], n = 0;
-#pragma unroll
-      for (int i = 0; i < kF4Tiles; ++i) {
-        const int t0 = 16 * (warp + i * kConsumerWarps);
-        const int a = hd.lo - hd.tok0 - t0, b = min(hd.hi - hd.tok0, hd.tokens) - t0;
-        if (a < 16 && b > 0) {
-          // (kept at constant indexes: registers)
-          if (n == 0) {
-            k[0] = sbase + code_off[i], ks[0] = sbase + scale_off[i], lo[0] = max(a, 0), hi[0] = min(b, 16);
-          } else {
-            k[1] = sbase + code_off[i], ks[1] = sbase + scale_off[i], lo[1] = max(a, 0), hi[1] = min(b, 16);
-          }
-          ++n;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kF4Tiles; ++i) {
-        if (i >= n) k[i] = ks[i] = 0u, lo[i] = 0, hi[i] = 16;
-        v[i] = k[i] + (uint32_t)(64 * bs);
-        vs[i] = ks[i] + (uint32_t)(8 * bs);
-      }
-      if (n == 2) w.tiles<2>(k, v, ks, vs, lo, hi);
-      else if (n == 1) w.tiles<1>(k, v, ks, vs, lo, hi);
+    return;
+  }
 
-      if (hd.flags & kHdrLast) {
-        // All warps are done with the stage: its memory takes the merge rows.
-        if (!consumer_sync(cons_bar, cons_phase, lane, abort_flag)) break;
-        float* mo = reinterpret_cast<float*>(ring + (size_t)stage * kF4StageBytes);
-        float* mml = mo + kConsumerWarps * kMaxGqa * kF4MergeStride;
-        w.store_merge(mo, mml, warp);
-        if (!consumer_sync(cons_bar, cons_phase, lane, abort_flag)) break;
-        const int c0 = blockIdx.x - hd.piece;
-        for (int hh = warp; hh < g; hh += kConsumerWarps) {
-          float M = -INFINITY, den = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // ------------------------------------------------------------- consumers
+  Fp4Worker w;
+  w.setup(lane);
+  w.reset();
+  // this warp's head of the unit, and its first token of a chunk (two tiles)
+  const int head = warp % hw, tok = 16 * tiles * (warp / hw);
+  const uint32_t rec = (uint32_t)(kFp4TokenBytes * bs);
+  uint32_t code_off[kF4Tiles], scale_off[kF4Tiles];
 #pragma unroll
-          for (int i = 0; i < kConsumerWarps; ++i) {
-            const float2 ml = *reinterpret_cast<const float2*>(mml + (i * kMaxGqa + hh) * 2);
-            const float4 x = *reinterpret_cast<const float4*>(mo + (i * kMaxGqa + hh) * kF4MergeStride + 4 * lane);
-            if (ml.x != -INFINITY) lse_fold(M, den, acc, ml.x, ml.y, x);   // a warp without a tile: nothing
-          }
-          if (hd.pieces == 1)
-            store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, hd.s, hd.kvh * g + hh, lane,
-                         hd.tokens > 0, M, den, acc);
-          else
-            fp4_store_piece(p.pieces, fp4_slot(c0, hd.piece), hh, lane, M, den, acc);
-        }
-        if (hd.pieces > 1) {
-          // Join: the pieces as they are, or where there are many in groups first.
-          const bool grouped = hd.pieces > 2 * kF4FoldGroup;
-          const int group = hd.piece / kF4FoldGroup, g0 = group * kF4FoldGroup;
-          const int gn = min(kF4FoldGroup, hd.pieces - g0), groups = (hd.pieces + kF4FoldGroup - 1) / kF4FoldGroup;
-          const int fold_base = 2 * gridDim.x;   // slots of folded groups
-          bool live = true;
-#pragma unroll 1
-          for (int level = grouped ? 0 : 1; level < 2 && live; ++level) {
-            __threadfence();   // this thread's part of the piece, before the arrival
-            if (!consumer_sync(cons_bar, cons_phase, lane, abort_flag)) {
-              live = false;
-              break;
-            }
-            if (threadIdx.x == 0) {
-              const bool all_here =
-                  level == 0 ? fp4_arrive(p.head, fp4_slot(c0, g0), epoch, (unsigned)gn)
-                             : fp4_arrive(p.head, 2 * kF4MaxCtas + c0, epoch, (unsigned)(grouped ? groups : hd.pieces));
-              __threadfence();
-              sums[6] = all_here ? 1 : 0;
-            }
-            if (!consumer_sync(cons_bar, cons_phase, lane, abort_flag)) {
-              live = false;
-              break;
-            }
-            if (*reinterpret_cast<volatile int*>(sums + 6) == 0) break;
-            for (int hh = warp; hh < g; hh += kConsumerWarps) {
-              float M, den;
-              float4 acc;
-              if (level == 0) {
-                fp4_fold(p.pieces, [&](int i) { return fp4_slot(c0, g0 + i); }, gn, hh, lane, M, den, acc);
-                fp4_store_piece(p.pieces, fold_base + fp4_slot(c0, g0), hh, lane, M, den, acc);
-              } else {
-                if (grouped)
-                  fp4_fold(p.pieces, [&](int i) { return fold_base + fp4_slot(c0, i * kF4FoldGroup); }, groups, hh, lane, M,
-                           den, acc);
-                else
-                  fp4_fold(p.pieces, [&](int i) { return fp4_slot(c0, i); }, hd.pieces, hh, lane, M, den, acc);
-                store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, hd.s, hd.kvh * g + hh, lane,
-                             true, M, den, acc);
-              }
-            }
-          }
-          if (!live) break;
-        }
-        // the merge rows were written through the generic proxy; copies come next
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  for (int i = 0; i < kF4Tiles; ++i) {
+    const int t = tok + 16 * i;
+    const uint32_t at = ((uint32_t)(t / bs) * hw + head) * rec;
+    code_off[i] = at + (uint32_t)(t % bs) * 64u;
+    scale_off[i] = at + (uint32_t)(128 * bs) + (uint32_t)(t % bs) * 8u;
+  }
+  uint32_t cons_phase = 0, parity = 0;
+  for (uint32_t stage = 0;; stage = stage + 1 < kF4Stages ? stage + 1 : 0u, parity ^= stage == 0u ? 1u : 0u) {
+    const bool got = mbar_wait_bounded(full0 + 8u * stage, parity, abort_flag, kWaitLimitNs);
+    if (!__all_sync(0xffffffffu, got)) {
+      if (lane == 0) {
+        atomicOr(&g_status, kStatusFullWaitTimeout);
+        *abort_flag = 1;
       }
+      return;
+    }
+    const uint32_t base = ring_u32 + stage * kF4StageBytes;
+    const Fp4Chunk* c = notes + stage;
+    const int flags = c->flags;
+    if (flags & kHdrEnd) return;
+    if (flags & kHdrFirst) {
+      const __nv_bfloat16* q = p.q + ((size_t)c->s * p.num_heads + (size_t)(c->kvh + head) * g) * kHeadDim;
+      w.load_q(q + (w.gid < g ? w.gid : 0) * kHeadDim, w.gid < g, p.logit_scale_log2, p.negate != 0);
+    }
+    if (flags & kF4Full) {
+#pragma unroll
+      for (int i = 0; i < kF4Tiles; i += 2) {
+        if (i >= tiles) break;
+        const uint32_t code[2] = {base + code_off[i], base + code_off[i + 1]};
+        const uint32_t scale[2] = {base + scale_off[i], base + scale_off[i + 1]};
+        const int none[2] = {0, 0}, all16[2] = {16, 16};
+        w.tiles<2, false>(code, scale, 64u * bs, 8u * bs, none, all16);
+      }
+    } else {
+      // the tiles that hold tokens that count, one at a time
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i) {
+        const int t0 = c->t0 + tok + 16 * i;
+        const int lo[1] = {max(c->lo - t0, 0)}, hi[1] = {min(c->hi - t0, 16)};
+        if (lo[0] >= hi[0]) continue;
+        const int tt = tok + 16 * i;
+        const uint32_t at = base + ((uint32_t)(tt / bs) * hw + head) * rec;
+        const uint32_t code[1] = {at + (uint32_t)(tt % bs) * 64u}, scale[1] = {at + (uint32_t)(128 * bs + tt % bs * 8)};
+        w.tiles<1, true>(code, scale, 64u * bs, 8u * bs, lo, hi);
+      }
+    }
+    if (!(flags & kHdrLast)) {
       __syncwarp();
       if (lane == 0) mbar_arrive(empty0 + 8u * stage);
+      continue;
+    }
+    const Fp4Chunk hd = *c;
+    float* rows = p.pieces + (size_t)fp4_slot(hd.run0, hd.piece) * kF4PieceFloats;
+    if (hw == kF4Warps) {
+      // the head was this warp's alone
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty0 + 8u * stage);
+      if (hd.pieces == 1) {
+        w.store_out_rows(p, hd.s, (hd.kvh + head) * g, hd.hi > hd.lo);
+      } else {
+        w.store_piece(rows + head * kF4RowFloats, g);
+      }
+      w.reset();
+      continue;
+    }
+    // All warps are done with the stage: its memory takes the merge rows.
+    if (!consumer_sync(cons_bar, cons_phase, lane, abort_flag)) return;
+    float* mo = reinterpret_cast<float*>(ring + stage * kF4StageBytes);
+    float* mml = mo + kF4Warps * kMaxGqa * kF4MergeStride;
+    w.store_merge(mo, mml, warp);
+    w.reset();
+    if (!consumer_sync(cons_bar, cons_phase, lane, abort_flag)) return;
+    for (int r = warp; r < hw * g; r += kF4Warps) {
+      const int hh = r / hw, kh = r % hw;   // query head of the group, kv head of the unit
+      float M = -INFINITY, den = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = kh; i < kF4Warps; i += hw) {
+        const float2 ml = *reinterpret_cast<const float2*>(mml + (i * kMaxGqa + hh) * 2);
+        const float4 y = *reinterpret_cast<const float4*>(mo + (i * kMaxGqa + hh) * kF4MergeStride + 4 * lane);
+        if (ml.x != -INFINITY) lse_fold(M, den, acc, ml.x, ml.y, y);   // a warp without a tile: nothing
+      }
+      if (hd.pieces == 1) {
+        store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, hd.s, (hd.kvh + kh) * g + hh, lane,
+                     hd.hi > hd.lo, M, den, acc);
+      } else {
+        float* to = rows + kh * kF4RowFloats;
+        __stcg(reinterpret_cast<float4*>(to + hh * kHeadDim) + lane, acc);
+        if (lane == 0) __stcg(reinterpret_cast<float2*>(to + kMaxGqa * kHeadDim) + hh, make_float2(M, den));
+      }
+    }
+    // the merge rows were written through the generic proxy; copies come next
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty0 + 8u * stage);
+  }
+}
+
+// The join, a programmatic dependent of the decode kernel. Rows of few pieces: a
+// warp each. Rows of many (long sequences): a CTA
+// each, its warps taking every eighth piece. The order of the additions is the
+// pieces' alone.
+constexpr int kF4JoinThreads = 256;
+constexpr int kF4JoinWarps = kF4JoinThreads / 32;
+constexpr int kF4JoinCtas = 760;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// One row's pieces first, first + step, ... (k <= 32 of them), added up by a warp:
+// lane i weighs piece i while the rows are on their way, four at a time.
+__device__ __forceinline__ void fp4_add_pieces(const float* pieces, int run0, int first, int step, int k, int kh, int hh,
+                                               int lane, float& M, float& den, float4& acc) {
+  auto piece = [&](int i) {
+    return pieces + (size_t)fp4_slot(run0, first + i * step) * kF4PieceFloats + kh * kF4RowFloats;
+  };
+  constexpr int kAhead = 4;
+  float4 y[kAhead];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      y[j] = j0 + j < k ? __ldcg(reinterpret_cast<const float4*>(piece(j0 + j) + hh * kHeadDim) + lane)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < k) ml = __ldcg(reinterpret_cast<const float2*>(piece(lane) + kMaxGqa * kHeadDim) + hh);
+  load(0);
+  M = warp_max(ml.x);
+  const float f = lane < k ? fast_exp2(ml.x - M) : 0.f;   // 0 past the last piece
+  den = warp_sum(f * ml.y);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int j0 = 0; j0 < k; j0 += kAhead) {
+    if (j0 > 0) load(j0);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const float v = __shfl_sync(0xffffffffu, f, (j0 + j) & 31);
+      acc.x = fmaf(v, y[j].x, acc.x);
+      acc.y = fmaf(v, y[j].y, acc.y);
+      acc.z = fmaf(v, y[j].z, acc.z);
+      acc.w = fmaf(v, y[j].w, acc.w);
     }
   }
-  // Every CTA counts itself out, also one that gave up; the last one starts the
-  // next call's epoch, to which counters that a call left unfinished mean nothing.
+}
+
+__global__ void __launch_bounds__(kF4JoinThreads, 5) pda_fp4_join_kernel(const Fp4DecodeParams p) {
+  __shared__ int cuts[2];
+  __shared__ float part_ml[kF4JoinWarps][2];
+  __shared__ float4 part_o[kF4JoinWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = p.gqa, per = p.group * g;   // rows of a unit
+  grid_dependency_wait();
+  if (threadIdx.x < 2) cuts[threadIdx.x] = min((int)__ldcg(&p.head->cuts[threadIdx.x]), kF4MaxCtas);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(&p.head->done, 1u) == gridDim.x - 1u) {
-      atomicExch(&p.head->done, 0u);
-      atomicAdd(&p.head->epoch, 1u);
-    }
+  // Entry i of the list (a call that gave up on a wait may have left any).
+  auto cut_of = [&](int i) {
+    int4 c = __ldcg(p.head->cut + i);
+    if (c.x < 0 || c.x >= p.num_seqs || c.y < 0 || c.y + p.group > p.num_kv_heads || c.z < 0 || c.z + c.w > kF4MaxCtas) c.w = 0;
+    return c;
+  };
+  for (int r = blockIdx.x * kF4JoinWarps + warp; r < cuts[0] * per; r += gridDim.x * kF4JoinWarps) {
+    const int4 c = cut_of(r / per);
+    const int kh = r % per / g, hh = r % per % g;
+    if (c.w < 1) continue;
+    float M, den;
+    float4 acc;
+    fp4_add_pieces(p.pieces, c.z, 0, 1, min(c.w, kF4FewPieces), kh, hh, lane, M, den, acc);
+    store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, c.x, (c.y + kh) * g + hh, lane, true, M, den,
+                 acc);
   }
+#pragma unroll 1
+  for (int r = blockIdx.x; r < cuts[1] * per; r += gridDim.x) {
+    const int4 c = cut_of(kF4MaxCtas - 1 - r / per);   // the same for the whole CTA
+    const int kh = r % per / g, hh = r % per % g;
+    if (c.w <= kF4FewPieces) continue;
+    float M = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = warp; b < c.w; b += 32 * kF4JoinWarps) {   // more than 8 pieces: every warp has one
+      float m1, d1;
+      float4 a1;
+      fp4_add_pieces(p.pieces, c.z, b, kF4JoinWarps, min(32, (c.w - b + kF4JoinWarps - 1) / kF4JoinWarps), kh, hh, lane, m1, d1,
+                     a1);
+      lse_fold(M, den, acc, m1, d1, a1);
+    }
+    if (lane == 0) part_ml[warp][0] = M, part_ml[warp][1] = den;
+    part_o[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0) {
+      M = -INFINITY, den = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int v = 0; v < kF4JoinWarps; ++v) lse_fold(M, den, acc, part_ml[v][0], part_ml[v][1], part_o[v][lane]);
+      store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, c.x, (c.y + kh) * g + hh, lane, true, M,
+                   den, acc);
+    }
+    __syncthreads();
+  }
+  // The last CTA leaves the lists empty (each has read their lengths).
+  if (threadIdx.x == 0 && atomicInc(&p.head->joined, gridDim.x - 1u) == gridDim.x - 1u) p.head->cuts[0] = p.head->cuts[1] = 0u;
 }
 
 }  // namespace pda

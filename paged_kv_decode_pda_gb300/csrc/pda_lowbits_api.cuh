@@ -94,7 +94,7 @@ pda_status fp4_resident(int dev, int* ctas) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         cudaFuncSetAttribute(pda::pda_fp4_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)pda::kF4Smem) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, pda::pda_fp4_decode_kernel, pda::kThreads, pda::kF4Smem) !=
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, pda::pda_fp4_decode_kernel, pda::kF4Threads, pda::kF4Smem) !=
             cudaSuccess ||
         occ < 1)
       return PDA_ERR_CUDA;
@@ -107,10 +107,20 @@ pda_status fp4_resident(int dev, int* ctas) {
 
 constexpr size_t kFp4HeadBytes = (sizeof(pda::Fp4Head) + 255) / 256 * 256;
 
-// One size for every call: four piece slots per resident CTA.
-pda_status fp4_workspace(int dev, cudaStream_t stream, int ctas, void** ws) {
-  const size_t bytes = kFp4HeadBytes + (size_t)ctas * 4 * pda::kF4RowFloats * sizeof(float);
+// One size for every call.
+pda_status fp4_workspace(int dev, cudaStream_t stream, void** ws) {
+  const size_t bytes = kFp4HeadBytes + (size_t)pda::kF4Slots * pda::kF4PieceFloats * sizeof(float);
   return grow_workspace(g_fp4_ws, dev, stream, bytes, kFp4HeadBytes, ws);
+}
+
+pda_status fp4_zero_counters() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return PDA_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_ws_mu);
+  for (auto& kv : g_fp4_ws)
+    if (kv.first.first == dev && kv.second.ptr && cudaMemset(kv.second.ptr, 0, kFp4HeadBytes) != cudaSuccess)
+      return PDA_ERR_CUDA;
+  return cudaDeviceSynchronize() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
 }  // namespace
@@ -253,6 +263,20 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
   if (misaligned(sinks, 4)) return PDA_ERR_INVALID_ARG;
   if (num_blocks > INT32_MAX || (long long)num_seqs * max_num_blocks_per_seq > INT32_MAX) return PDA_ERR_UNSUPPORTED;
   if (num_seqs == 0) return PDA_OK;
+  // Heads of a unit, as many as share a chunk of whole pages (see pda_fp4.cuh), and
+  // the chunks at the longest lengths, for `tiles` tiles a warp.
+  int tiles = pda::kF4Tiles, group = 0, per = 0;
+  long long most = 0;
+  auto cut = [&] {
+    const int tokens = 16 * pda::kF4Warps * tiles;
+    group = 4;
+    while (group > 1 && (num_kv_heads % group != 0 || block_size * group > tokens)) group /= 2;
+    per = tokens / group / block_size;
+    most = (long long)num_seqs * (num_kv_heads / group) *
+           (max_num_blocks_per_seq > per ? (max_num_blocks_per_seq + per - 1) / per : 1);
+  };
+  cut();
+  if (most > INT32_MAX) return PDA_ERR_UNSUPPORTED;
   if (num_blocks == 0 || !out || !q || !kv_cache || !seq_lens || (max_num_blocks_per_seq > 0 && !block_tables))
     return PDA_ERR_INVALID_ARG;
   if (!aligned16(out) || !aligned16(q) || !aligned16(kv_cache) || misaligned(block_tables, 4) || misaligned(seq_lens, 4))
@@ -263,8 +287,15 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     pda_status st = fp4_resident(dev, &ctas);
     if (st != PDA_OK) return st;
     void* ws = nullptr;
-    st = fp4_workspace(dev, stream, ctas, &ws);
+    st = fp4_workspace(dev, stream, &ws);
     if (st != PDA_OK) return st;
+    // Half as large chunks where large ones are too few for even runs: below four a CTA
+    // (us with 4 / 2 tiles a warp, 32/8 heads: 16 x 1024 tokens 16.3 / 15.0, 32 x 1024
+    // 20.9 / 19.1, 64 x 1024 25.2 / 25.3, 128 x 1 to 2048 43.7 / 48.8).
+    if (most < 4ll * ctas) {
+      tiles = 2;
+      cut();
+    }
     const double logit = (double)scale * (double)k_scale * 1.4426950408889634;
     pda::Fp4DecodeParams p = {};
     p.out = out;
@@ -283,19 +314,30 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     p.max_blocks = max_num_blocks_per_seq;
     p.num_blocks = (int)num_blocks;
     p.window = window;
-    p.pages_per_chunk = pda::kF4ChunkTokens / block_size;
+    p.pages_per_chunk = per;
+    p.group = group;
+    p.tiles = tiles;
+    p.bs_inverse = ((1ull << 40) + block_size - 1) / block_size;
+    p.chunk_inverse = ((1ull << 40) + per - 1) / per;
     p.logit_scale_log2 = (float)std::fabs(logit);
     p.negate = logit < 0.0 ? 1 : 0;
     p.v_scale = v_scale;
     p.out_fp8 = out_dtype == PDA_OUT_E4M3;
     p.out_scale = output_scale;
-    // No more CTAs than the longest lengths make chunks.
-    const int per = p.pages_per_chunk;
-    const long long most = (long long)num_seqs * num_kv_heads *
-                           (max_num_blocks_per_seq > per ? (max_num_blocks_per_seq + per - 1) / per : 1);
     const unsigned grid = (unsigned)(most < ctas ? most : ctas);
-    pda::pda_fp4_decode_kernel<<<grid, pda::kThreads, pda::kF4Smem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+    std::lock_guard<std::mutex> lk(g_ops_mu);   // the two kernels follow each other
+    pda::pda_fp4_decode_kernel<<<grid, pda::kF4Threads, pda::kF4Smem, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(pda::kF4JoinCtas);
+    lc.blockDim = dim3(pda::kF4JoinThreads);
+    lc.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelEx(&lc, pda::pda_fp4_join_kernel, p) == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
   });
 }
 
@@ -306,7 +348,7 @@ pda_status pda_reserve_fp4(cudaStream_t stream) {
     const pda_status st = fp4_resident(dev, &ctas);
     if (st != PDA_OK) return st;
     void* ws = nullptr;
-    return fp4_workspace(dev, stream, ctas, &ws);
+    return fp4_workspace(dev, stream, &ws);
   });
 }
 
