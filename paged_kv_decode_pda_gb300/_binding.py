@@ -853,51 +853,49 @@ def fp4_cache_shape(num_blocks: int, num_kv_heads: int, block_size: int) -> tupl
     return num_blocks, num_kv_heads, FP4_TOKEN_BYTES * block_size
 
 
-def _token_rows(what, key, value, slot_mapping):
-    """(key rows, value rows, T, Hk, D, device index) of checked new tokens ``[T, Hk, 128]`` (any token and head strides)."""
-    if key.dim() != 3 or value.shape != key.shape or key.dtype is not _BF16 or value.dtype is not _BF16:
-        _refuse(what + ": key and value must be bf16 [T, Hk, 128] of one shape")
-    T, Hk, D = key.shape
-    k0, k1, k2 = key.stride()
-    v0, v1, v2 = value.stride()
-    if (k2 != 1 or v2 != 1) and T * Hk:
-        _refuse(what + ": the 128 dims of a row must be contiguous")
-    if slot_mapping.dtype is not _I64 or slot_mapping.shape != (T,) or not slot_mapping.is_contiguous():
-        _refuse(what + ": slot_mapping must be contiguous int64 [T]")
-    dev = key.get_device()
-    if dev < 0 or dev != _device() or value.get_device() != dev or slot_mapping.get_device() != dev:
-        _refuse(what + ": tensors must be on the current CUDA device")
-    return _TokenRows(key.data_ptr(), k0, k1), _TokenRows(value.data_ptr(), v0, v1), T, Hk, D, dev
+_U8, _F32 = torch.uint8, torch.float32
 
 
-def _e4m3_caches(what, k_cache, v_cache, dev, v_shuffled=False):
-    """(NB, Hk, bs) of checked e4m3 caches on device ``dev``."""
-    for t in (k_cache, v_cache):
-        if t.dtype not in _CACHE_TYPES or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(what + ": caches must be contiguous float8_e4m3fn on the current CUDA device")
-    if k_cache.dim() != 5:
-        _refuse(what + ": shapes")
-    NB, Hk, D16, bs, sixteen = k_cache.shape
-    if D16 != 8 or sixteen != 16 or v_cache.shape != ((NB, Hk, bs // 16, 128, 16) if v_shuffled else (NB, Hk, 128, bs)):
-        _refuse(what + ": shapes")
-    return NB, Hk, bs
+def _say_why(what, checks):
+    """Raises with the first of the (holds, message) checks that fails: the quick checks of a call did."""
+    for holds, message in checks:
+        if not holds():
+            _refuse(what + ": " + message)
+    _refuse(what + ": tensors must be on the current CUDA device")
 
 
-def _scale_tables(what, k_scales, v_scales, shape, dev):
-    for t in (k_scales, v_scales):
-        if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(what + ": scale tables must be contiguous float32 [NB, Hk, bs] on the caches' device")
+def _write_refuse(what, key, value, slot_mapping, cache_checks):
+    _say_why(what, [
+        (lambda: key.dim() == 3 and value.shape == key.shape and key.dtype is _BF16 and value.dtype is _BF16,
+         "key and value must be bf16 [T, Hk, 128] of one shape"),
+        (lambda: key.numel() == 0 or (key.stride(2) == 1 and value.stride(2) == 1),
+         "the 128 dims of a row must be contiguous"),
+        (lambda: slot_mapping.dtype is _I64 and slot_mapping.shape == key.shape[:1] and slot_mapping.is_contiguous(),
+         "slot_mapping must be contiguous int64 [T]")] + cache_checks)
 
 
-def _fp4_cache(what, kv_cache, dev):
-    """(NB, Hk, bs) of a checked 4-bit cache on device ``dev``."""
-    if kv_cache.dim() != 3 or kv_cache.dtype is not torch.uint8 or not kv_cache.is_contiguous() \
-            or kv_cache.get_device() != dev:
-        _refuse(what + ": kv_cache must be contiguous uint8 [NB, Hk, 144 * bs] on the current CUDA device")
-    NB, Hk, n = kv_cache.shape
-    if n == 0 or n % FP4_TOKEN_BYTES:
-        _refuse(what + ": kv_cache must be [NB, Hk, 144 * bs]")
-    return NB, Hk, n // FP4_TOKEN_BYTES
+def _e4m3_checks(k_cache, v_cache, v_shuffled=False, heads=None):
+    def shapes():
+        if k_cache.dim() != 5:
+            return False
+        NB, Hk, D16, bs, sixteen = k_cache.shape
+        want = (NB, Hk, bs // 16, 128, 16) if v_shuffled else (NB, Hk, 128, bs)
+        return D16 == 8 and sixteen == 16 and v_cache.shape == want and heads in (None, Hk)
+
+    return [(lambda: k_cache.dtype in _CACHE_TYPES and v_cache.dtype in _CACHE_TYPES and k_cache.is_contiguous()
+             and v_cache.is_contiguous(), "caches must be contiguous float8_e4m3fn"), (shapes, "shapes of the caches")]
+
+
+def _scale_checks(k_scales, v_scales, k_cache):
+    return [(lambda: all(t.dtype is _F32 and t.is_contiguous() and t.shape == (k_cache.shape[0], k_cache.shape[1],
+                                                                               k_cache.shape[3])
+                         for t in (k_scales, v_scales)), "scale tables must be contiguous float32 [NB, Hk, bs]")]
+
+
+def _fp4_checks(kv_cache, heads=None):
+    return [(lambda: kv_cache.dim() == 3 and kv_cache.dtype is _U8 and kv_cache.is_contiguous() and kv_cache.shape[2] > 0
+             and kv_cache.shape[2] % FP4_TOKEN_BYTES == 0 and heads in (None, kv_cache.shape[1]),
+             "kv_cache must be contiguous uint8 [NB, Hk, 144 * bs]")]
 
 
 def reshape_and_cache_slot_scales(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -912,14 +910,29 @@ def reshape_and_cache_slot_scales(key: torch.Tensor, value: torch.Tensor, k_cach
     """
     what = "reshape_and_cache_slot_scales"
     lib = _lib or load()
-    k, v, T, Hk, D, dev = _token_rows(what, key, value, slot_mapping)
-    NB, Hk2, bs = _e4m3_caches(what, k_cache, v_cache, dev)
-    if Hk2 != Hk:
-        _refuse(what + ": shapes")
-    _scale_tables(what, k_scales, v_scales, (NB, Hk, bs), dev)
+    # One condition, as in rope: a decode step spends more time in these checks than on the GPU.
+    dev = key.get_device()
+    ks, cs = key.shape, k_cache.shape
+    if not (len(ks) == 3 and len(cs) == 5 and value.shape == ks and key.dtype is _BF16 and value.dtype is _BF16
+            and slot_mapping.dtype is _I64 and slot_mapping.shape == ks[:1] and slot_mapping.is_contiguous()
+            and k_cache.dtype in _CACHE_TYPES and v_cache.dtype in _CACHE_TYPES and k_cache.is_contiguous()
+            and v_cache.is_contiguous() and cs[1] == ks[1] and cs[2] == 8 and cs[4] == 16
+            and v_cache.shape == (cs[0], cs[1], 128, cs[3]) and k_scales.dtype is _F32 and v_scales.dtype is _F32
+            and k_scales.shape == (cs[0], cs[1], cs[3]) and v_scales.shape == k_scales.shape
+            and k_scales.is_contiguous() and v_scales.is_contiguous()
+            and 0 <= dev == value.get_device() == slot_mapping.get_device() == k_cache.get_device() == v_cache.get_device()
+            == k_scales.get_device() == v_scales.get_device() == _device()):
+        _write_refuse(what, key, value, slot_mapping, _e4m3_checks(k_cache, v_cache, heads=ks[1] if len(ks) == 3 else -1)
+                      + _scale_checks(k_scales, v_scales, k_cache))
+    T, Hk, D = ks
+    k0, k1, k2 = key.stride()
+    v0, v1, v2 = value.stride()
+    if (k2 != 1 or v2 != 1) and T * Hk:
+        _refuse(what + ": the 128 dims of a row must be contiguous")
+    k, v = _TokenRows(key.data_ptr(), k0, k1), _TokenRows(value.data_ptr(), v0, v1)
     st = lib.pda_reshape_and_cache_slot_scales(ctypes.addressof(k), ctypes.addressof(v), k_cache.data_ptr(),
                                                v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-                                               slot_mapping.data_ptr(), T, Hk, D, bs, NB, min_scale,
+                                               slot_mapping.data_ptr(), T, Hk, D, cs[3], cs[0], min_scale,
                                                _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         raise PdaError(st, "pda_reshape_and_cache_slot_scales")
@@ -935,38 +948,58 @@ def reshape_and_cache_fp4(key: torch.Tensor, value: torch.Tensor, kv_cache: torc
     """
     what = "reshape_and_cache_fp4"
     lib = _lib or load()
-    k, v, T, Hk, D, dev = _token_rows(what, key, value, slot_mapping)
-    NB, Hk2, bs = _fp4_cache(what, kv_cache, dev)
-    if Hk2 != Hk:
-        _refuse(what + ": shapes")
+    dev = key.get_device()
+    ks, cs = key.shape, kv_cache.shape
+    if not (len(ks) == 3 and len(cs) == 3 and value.shape == ks and key.dtype is _BF16 and value.dtype is _BF16
+            and slot_mapping.dtype is _I64 and slot_mapping.shape == ks[:1] and slot_mapping.is_contiguous()
+            and kv_cache.dtype is _U8 and kv_cache.is_contiguous() and cs[1] == ks[1] and cs[2] and cs[2] % 144 == 0
+            and 0 <= dev == value.get_device() == slot_mapping.get_device() == kv_cache.get_device() == _device()):
+        _write_refuse(what, key, value, slot_mapping, _fp4_checks(kv_cache, heads=ks[1] if len(ks) == 3 else -1))
+    T, Hk, D = ks
+    k0, k1, k2 = key.stride()
+    v0, v1, v2 = value.stride()
+    if (k2 != 1 or v2 != 1) and T * Hk:
+        _refuse(what + ": the 128 dims of a row must be contiguous")
+    k, v = _TokenRows(key.data_ptr(), k0, k1), _TokenRows(value.data_ptr(), v0, v1)
     st = lib.pda_reshape_and_cache_fp4(ctypes.addressof(k), ctypes.addressof(v), kv_cache.data_ptr(),
-                                       slot_mapping.data_ptr(), T, Hk, D, bs, NB, k_scale, v_scale,
+                                       slot_mapping.data_ptr(), T, Hk, D, cs[2] // 144, cs[0], k_scale, v_scale,
                                        _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         raise PdaError(st, "pda_reshape_and_cache_fp4")
 
 
-def _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev):
+def _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev, cache_ok, cache_checks):
     """(k_out, v_out, S, MB, first's address) of the checked arguments that the readers share."""
-    if block_tables.dim() != 2:
-        _refuse(what + ": block_tables must be [S, MB]")
-    S, MB = block_tables.shape
-    if token_starts.shape != (S + 1,) or (first is not None and first.shape != (S,)):
-        _refuse(what + ": token_starts must be [S + 1], first [S]")
-    for t in (block_tables, token_starts) if first is None else (block_tables, token_starts, first):
-        if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(what + ": block_tables, token_starts and first must be contiguous int32 on the cache's device")
-    shape = (int(num_tokens), Hk, 128)
-    if shape[0] < 0:
-        _refuse(what + ": num_tokens")
-    outs = []
-    for out in (k_out, v_out):
-        if out is None:
-            out = torch.empty(shape, dtype=_BF16, device=block_tables.device)
-        elif out.shape != shape or out.dtype is not _BF16 or not out.is_contiguous() or out.get_device() != dev:
-            _refuse(what + ": k_out and v_out must be contiguous bf16 [num_tokens, Hk, 128] on the cache's device")
-        outs.append(out)
-    return outs[0], outs[1], S, MB, None if first is None else first.data_ptr()
+    bt = block_tables.shape
+    shape = (num_tokens, Hk, 128)
+    if not (cache_ok and len(bt) == 2 and token_starts.shape == (bt[0] + 1,) and block_tables.dtype is _I32
+            and token_starts.dtype is _I32 and block_tables.is_contiguous() and token_starts.is_contiguous()
+            and num_tokens >= 0 and 0 <= dev == block_tables.get_device() == token_starts.get_device() == _device()
+            and (first is None or (first.shape == bt[:1] and first.dtype is _I32 and first.is_contiguous()
+                                   and first.get_device() == dev))):
+        _say_why(what, cache_checks() + [
+            (lambda: len(bt) == 2 and token_starts.shape == (bt[0] + 1,) and (first is None or first.shape == bt[:1]),
+             "shapes (block_tables [S, MB], token_starts [S + 1], first [S])"),
+            (lambda: all(t is None or (t.dtype is _I32 and t.is_contiguous()) for t in (block_tables, token_starts, first)),
+             "block_tables, token_starts and first must be contiguous int32"),
+            (lambda: num_tokens >= 0, "num_tokens")])
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=_BF16, device=block_tables.device)
+    elif not (k_out.shape == shape and k_out.dtype is _BF16 and k_out.is_contiguous() and k_out.get_device() == dev):
+        _refuse(what + ": k_out must be contiguous bf16 [num_tokens, Hk, 128] on the cache's device")
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
+    elif not (v_out.shape == shape and v_out.dtype is _BF16 and v_out.is_contiguous() and v_out.get_device() == dev):
+        _refuse(what + ": v_out must be contiguous bf16 [num_tokens, Hk, 128] on the cache's device")
+    return k_out, v_out, bt[0], bt[1], None if first is None else first.data_ptr()
+
+
+def _e4m3_ok(k_cache, v_cache, dev, v_shuffled=False):
+    cs = k_cache.shape
+    return (len(cs) == 5 and cs[2] == 8 and cs[4] == 16 and k_cache.dtype in _CACHE_TYPES
+            and v_cache.dtype in _CACHE_TYPES and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and v_cache.get_device() == dev
+            and v_cache.shape == ((cs[0], cs[1], cs[3] // 16, 128, 16) if v_shuffled else (cs[0], cs[1], 128, cs[3])))
 
 
 def gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor, token_starts: torch.Tensor,
@@ -980,13 +1013,14 @@ def gather_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: tor
     ``[S]``, default 0) on. Rows of no sequence are left as they are in
     ``k_out`` / ``v_out`` (uninitialised when not given).
     """
-    what = "gather_cache"
     lib = _lib or load()
-    dev = _on_device(what, (k_cache, v_cache))
-    NB, Hk, bs = _e4m3_caches(what, k_cache, v_cache, dev, v_shuffled)
-    k, v, S, MB, at = _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev)
+    dev = k_cache.get_device()
+    cs = k_cache.shape
+    ok = _e4m3_ok(k_cache, v_cache, dev, v_shuffled)
+    k, v, S, MB, at = _gather_rows("gather_cache", block_tables, token_starts, first, num_tokens, cs[1] if ok else 0, k_out,
+                                   v_out, dev, ok, lambda: _e4m3_checks(k_cache, v_cache, v_shuffled))
     st = lib.pda_gather_cache(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                              token_starts.data_ptr(), at, k.shape[0], S, Hk, 128, bs, MB, NB, k_scale, v_scale,
+                              token_starts.data_ptr(), at, num_tokens, S, cs[1], 128, cs[3], MB, cs[0], k_scale, v_scale,
                               PDA_KV_SHUFFLED_V if v_shuffled else PDA_KV_NATIVE,
                               _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if st:
@@ -999,15 +1033,18 @@ def gather_cache_slot_scales(k_cache: torch.Tensor, v_cache: torch.Tensor, k_sca
                              num_tokens: int, *, first: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
                              v_out: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """``pda_gather_cache_slot_scales``: ``gather_cache`` with a scale per slot (float32 ``[NB, Hk, bs]``)."""
-    what = "gather_cache_slot_scales"
     lib = _lib or load()
-    dev = _on_device(what, (k_cache, v_cache))
-    NB, Hk, bs = _e4m3_caches(what, k_cache, v_cache, dev)
-    _scale_tables(what, k_scales, v_scales, (NB, Hk, bs), dev)
-    k, v, S, MB, at = _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev)
+    dev = k_cache.get_device()
+    cs = k_cache.shape
+    ok = (_e4m3_ok(k_cache, v_cache, dev) and k_scales.shape == (cs[0], cs[1], cs[3]) and v_scales.shape == k_scales.shape
+          and k_scales.dtype is _F32 and v_scales.dtype is _F32 and k_scales.is_contiguous() and v_scales.is_contiguous()
+          and dev == k_scales.get_device() == v_scales.get_device())
+    k, v, S, MB, at = _gather_rows("gather_cache_slot_scales", block_tables, token_starts, first, num_tokens,
+                                   cs[1] if ok else 0, k_out, v_out, dev, ok,
+                                   lambda: _e4m3_checks(k_cache, v_cache) + _scale_checks(k_scales, v_scales, k_cache))
     st = lib.pda_gather_cache_slot_scales(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                           k_scales.data_ptr(), v_scales.data_ptr(), block_tables.data_ptr(),
-                                          token_starts.data_ptr(), at, k.shape[0], S, Hk, 128, bs, MB, NB,
+                                          token_starts.data_ptr(), at, num_tokens, S, cs[1], 128, cs[3], MB, cs[0],
                                           _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         raise PdaError(st, "pda_gather_cache_slot_scales")
@@ -1019,14 +1056,15 @@ def gather_cache_fp4(kv_cache: torch.Tensor, block_tables: torch.Tensor, token_s
                      k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
                      stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """``pda_gather_cache_fp4``: ``gather_cache`` out of a 4-bit cache ``[NB, Hk, 144 * bs]``."""
-    what = "gather_cache_fp4"
     lib = _lib or load()
-    dev = _on_device(what, (kv_cache,))
-    NB, Hk, bs = _fp4_cache(what, kv_cache, dev)
-    k, v, S, MB, at = _gather_rows(what, block_tables, token_starts, first, num_tokens, Hk, k_out, v_out, dev)
+    dev = kv_cache.get_device()
+    cs = kv_cache.shape
+    ok = len(cs) == 3 and kv_cache.dtype is _U8 and kv_cache.is_contiguous() and cs[2] > 0 and cs[2] % 144 == 0
+    k, v, S, MB, at = _gather_rows("gather_cache_fp4", block_tables, token_starts, first, num_tokens, cs[1] if ok else 0,
+                                   k_out, v_out, dev, ok, lambda: _fp4_checks(kv_cache))
     st = lib.pda_gather_cache_fp4(k.data_ptr(), v.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
-                                  token_starts.data_ptr(), at, k.shape[0], S, Hk, 128, bs, MB, NB, k_scale, v_scale,
-                                  _raw_stream(dev) if stream is None else _stream_ptr(stream))
+                                  token_starts.data_ptr(), at, num_tokens, S, cs[1], 128, cs[2] // 144, MB, cs[0],
+                                  k_scale, v_scale, _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         raise PdaError(st, "pda_gather_cache_fp4")
     return k, v
@@ -1042,37 +1080,34 @@ def decode_fp4(q: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tens
     sequence to its last ``window`` tokens. The first call on a stream makes its
     workspace; ``reserve_fp4`` does so ahead of a capture.
     """
-    what = "decode_fp4"
     lib = _lib or load()
-    if q.dim() != 3 or block_tables.dim() != 2 or q.dtype is not _BF16:
-        _refuse(what + ": q must be bf16 [S, H, 128], block_tables [S, MB]")
     dev = q.get_device()
-    if dev < 0 or dev != _device():
-        _refuse(what + ": tensors must be on the current CUDA device")
-    NB, Hk, bs = _fp4_cache(what, kv_cache, dev)
-    S, H, D = q.shape
-    MB = block_tables.shape[1]
-    if block_tables.shape[0] != S or seq_lens.shape != (S,):
-        _refuse(what + ": shapes")
-    for t in (block_tables, seq_lens):
-        if t.dtype is not _I32 or not t.is_contiguous() or t.get_device() != dev:
-            _refuse(what + ": block_tables and seq_lens must be contiguous int32 on q's device")
-    if not q.is_contiguous():
-        _refuse(what + ": q must be contiguous")
+    qs, cs, bt = q.shape, kv_cache.shape, block_tables.shape
+    if not (len(qs) == 3 and len(cs) == 3 and len(bt) == 2 and bt[0] == qs[0] and seq_lens.shape == qs[:1]
+            and q.dtype is _BF16 and kv_cache.dtype is _U8 and block_tables.dtype is _I32 and seq_lens.dtype is _I32
+            and q.is_contiguous() and kv_cache.is_contiguous() and block_tables.is_contiguous()
+            and seq_lens.is_contiguous() and cs[2] and cs[2] % 144 == 0
+            and 0 <= dev == kv_cache.get_device() == block_tables.get_device() == seq_lens.get_device() == _device()):
+        _say_why("decode_fp4", [
+            (lambda: len(qs) == 3 and q.dtype is _BF16 and q.is_contiguous(), "q must be contiguous bf16 [S, H, 128]")]
+            + _fp4_checks(kv_cache) + [
+            (lambda: len(bt) == 2 and bt[0] == qs[0] and seq_lens.shape == qs[:1], "block_tables [S, MB] and seq_lens [S]"),
+            (lambda: all(t.dtype is _I32 and t.is_contiguous() for t in (block_tables, seq_lens)),
+             "block_tables and seq_lens must be contiguous int32")])
     fp8 = output_scale is not None
-    want = torch.float8_e4m3fn if fp8 else _BF16
     if out is None:
-        out = torch.empty((S, H, D), dtype=want, device=q.device)
-    elif out.shape != q.shape or out.dtype not in ((want, torch.uint8) if fp8 else (want,)) or not out.is_contiguous() \
-            or out.get_device() != dev:
-        _refuse(what + ": out")
-    if sinks is not None and (sinks.dtype is not torch.float32 or sinks.shape != (H,) or not sinks.is_contiguous()
-                              or sinks.get_device() != dev):
-        _refuse(what + ": sinks must be a contiguous float32 [num_heads] tensor on q's device")
+        out = torch.empty_like(q, dtype=torch.float8_e4m3fn) if fp8 else torch.empty_like(q)
+    elif not (out.shape == qs and out.dtype in (_CACHE_TYPES if fp8 else (_BF16,)) and out.is_contiguous()
+              and out.get_device() == dev):
+        _refuse("decode_fp4: out")
+    if sinks is not None and not (sinks.dtype is _F32 and sinks.shape == qs[1:2] and sinks.is_contiguous()
+                                  and sinks.get_device() == dev):
+        _refuse("decode_fp4: sinks must be a contiguous float32 [num_heads] tensor on q's device")
     st = lib.pda_decode_fp4(out.data_ptr(), q.data_ptr(), kv_cache.data_ptr(), block_tables.data_ptr(),
-                            seq_lens.data_ptr(), S, H, Hk, D, bs, MB, NB, scale, k_scale, v_scale, window,
-                            None if sinks is None else sinks.data_ptr(), PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16,
-                            output_scale if fp8 else 1.0, _raw_stream(dev) if stream is None else _stream_ptr(stream))
+                            seq_lens.data_ptr(), qs[0], qs[1], cs[1], qs[2], cs[2] // 144, bt[1], cs[0], scale, k_scale,
+                            v_scale, window, None if sinks is None else sinks.data_ptr(),
+                            PDA_OUT_E4M3 if fp8 else PDA_OUT_BF16, output_scale if fp8 else 1.0,
+                            _raw_stream(dev) if stream is None else _stream_ptr(stream))
     if st:
         raise PdaError(st, "pda_decode_fp4")
     return out

@@ -13,14 +13,13 @@
 // or one where pages are larger or the heads do not divide, a head's tokens then
 // shared by two or four warps. A unit's tokens go in chunks of whole pages, 256 /
 // heads tokens at most. All units' chunks, one after the other, are cut into runs
-// wherever the cuts fall, one per resident CTA, so that every batch (a few long sequences, many ragged
-// ones) loads all SMs alike. (With smaller runs for the last quarter, taken from a
-// queue as CTAs come free, all CTAs end within 4 % of each other, not 20 %, and the
-// pieces this adds cost as much: 219 against 222 us at 256 x 4096 tokens of 32/8
-// heads, 120 against 119 at 256 x 1 to 4000 of 40/8, 83 against 67 at 2 x 131072 of
-// 64/8.) The pieces (O, m,
-// l) of a unit cut by a run's end go to the workspace, and a second kernel joins
-// them in their order, so the result does not depend on which CTA made which.
+// wherever the cuts fall, one per resident CTA, so that every batch (a few long
+// sequences, many ragged ones) loads all SMs alike. The pieces (O, m, l) of a unit
+// that a cut divides go to the workspace, and a second kernel joins them.
+// (Smaller runs for the last quarter, taken from a queue as CTAs come free: all CTAs
+// end within 4 % of each other, not 20 %, and the pieces this adds cost as much, 219
+// against 222 us at 256 x 4096 tokens of 32/8 heads, 120 against 119 at 256 x 1 to
+// 4000 of 40/8, 83 against 67 at 2 x 131072 of 64/8, at two tiles a warp.)
 // (Joined in this kernel, by the warp that brings a unit's last piece: 256 x 4096
 // tokens of 32/8 heads took 242 us against 212, as a warp that waits for counts and
 // other warps' rows holds up its CTA's ring.)
@@ -32,6 +31,10 @@
 //   S^T = K (16 tokens x 128) Q^T (128 x 8 heads), O^T += V^T (128 x 16) P^T
 // on warp MMAs whose A fragments are made in registers: e2m1 -> f16 by the
 // conversion instruction, times the block's scale, exact (6 significant bits).
+// These MMAs are the bound: 8 of them take 18 cycles of an SM, and little else issues
+// meanwhile, so that a tile (16 MMAs, 64 conversions, 64 products, 60 others) takes 84
+// with 12 or with 16 warps, where HBM would bring one every 91; 256 x 4096 tokens take
+// 192 us without any copies and 201 with them.
 // Q enters as in pda_decode (shifted by a power of two into f16), P as one f16,
 // off by at most 2^-11 of itself; the normaliser sums P unrounded in fp32.
 //
@@ -51,16 +54,10 @@
 
 namespace pda {
 
-#ifndef PDA_F4_STAGES
-#define PDA_F4_STAGES 2
-#endif
-#ifndef PDA_F4_CTAS
-#define PDA_F4_CTAS 3
-#endif
 constexpr int kF4Warps = 4;                                    // consumer warps
 constexpr int kF4Threads = kF4Warps * 32 + 32;
-constexpr int kF4CtasPerSm = PDA_F4_CTAS;
-constexpr int kF4Stages = PDA_F4_STAGES;
+constexpr int kF4CtasPerSm = 3;
+constexpr int kF4Stages = 2;
 constexpr int kF4Tiles = 4;                                    // 16-token tiles of a chunk per consumer warp at most
 constexpr int kF4ChunkTokens = 16 * kF4Tiles * kF4Warps;
 constexpr uint32_t kF4StageBytes = kF4ChunkTokens * kFp4TokenBytes;
@@ -116,7 +113,7 @@ struct Fp4DecodeParams {
   int pages_per_chunk;
   int group;                // kv heads of a unit: 4, 2 or 1
   int tiles;                // of a chunk per consumer warp: 4 or 2
-  unsigned long long bs_inverse, chunk_inverse;   // ceil(2^40 / d) of block_size and pages_per_chunk
+  unsigned long long bs_inverse, chunk_inverse;   // ceil(2^37 / d) of block_size and pages_per_chunk
   float logit_scale_log2;   // |scale * k_scale| * log2(e)
   int negate;
   float v_scale;
@@ -150,10 +147,12 @@ __device__ __forceinline__ int fp4_row_token(int r) {
   return ((r & 1) ? (t ^ 1) + 4 : t) + (r & 8);
 }
 
-// x / d for 0 <= x < 2^31 and d <= 128, with ceil(2^40 / d): off by less than 2^-9
-// before it is cut, and x / d lies at least 2^-7 below the next integer.
+// x / d with ceil(2^37 / d), for tokens (x < 2^30 + 128, d = 16 .. 128) and pages
+// (x <= 2^26, d = 1 .. 16): before it is cut the result is off by less than x / 2^37
+// (nothing where d is a power of two), less than 1 / d, and x / d lies at least 1 / d
+// below the next integer; the product stays below 2^64.
 __device__ __forceinline__ int fp4_divide(int x, unsigned long long inverse) {
-  return (int)(((unsigned long long)(unsigned)x * inverse) >> 40);
+  return (int)(((unsigned long long)(unsigned)x * inverse) >> 37);
 }
 __device__ __forceinline__ Fp4Span fp4_span(const Fp4DecodeParams& p, int s) {
   Fp4Span a;

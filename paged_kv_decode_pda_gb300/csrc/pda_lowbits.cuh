@@ -15,8 +15,8 @@
 //
 // Every rounding to 8 or 4 bits is that of the real quotient (nearest, ties to
 // even), whatever the scales' low bits: the quotient is made with a reciprocal,
-// off by less than 2^-21, both ends of that range are rounded, and where they
-// differ the sign of one fused multiply-add, which is exact, decides.
+// off by less than 2^-21, and next to a midpoint the sign of one fused
+// multiply-add, which is exact, decides.
 #pragma once
 
 #include "pda_device.cuh"
@@ -58,7 +58,8 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float e4m3_value(uint32_t code) { return f16lo_f32(e4m3x2_lo_to_f16x2(code)); }
 
-// The margin of a quotient made with a reciprocal: three roundings of 2^-24.
+// The margin of a quotient made with a reciprocal: up to four roundings of 2^-24
+// (unit, reciprocal, its shifted ends, product).
 constexpr float kQuotLo = 1.f - 4.76837158203125e-07f;   // 1 -+ 2^-21
 constexpr float kQuotHi = 1.f + 4.76837158203125e-07f;
 
@@ -70,32 +71,38 @@ __device__ __forceinline__ uint32_t settle(uint32_t lo, float mid, float unit, f
   return r > 0.f ? lo + 1u : r < 0.f ? lo : lo + (lo & 1u);
 }
 
+// Two products at once (fp32, each rounded on its own).
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  unsigned long long x, y, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(r));
+  return d;
+}
+
+// The quotient x / scale for a rounding to e4m3: an approximate one, at most 2^-19
+// of itself too large, cut to 16 significant bits (midpoints have 5, so that a
+// quotient at or just past one is cut to it), and moved one ulp to the side on which
+// the exact one lies, which the sign of one fused multiply-add tells. above: 1 /
+// scale, a little too large. (A row's largest value is 448 scales, so exact and near
+// ties are common here: a branch for them was taken by two of three warps.)
+__device__ __forceinline__ float e4m3_quotient(float x, float scale, float above) {
+  const uint32_t c = __float_as_uint(x * above) & 0xFFFFFF00u;   // (NaN and infinities stay)
+  const float r = copysignf(1.f, x) * fmaf(-__uint_as_float(c), scale, x);   // of the magnitudes
+  return __uint_as_float(c + (r > 0.f ? 1u : 0u) - (r < 0.f ? 1u : 0u));     // (c == 0: r >= 0)
+}
+
 // Eight bf16 values (w) as e4m3 codes of x / scale, the first in the lowest
 // byte of .x. inv is 1 / scale rounded.
 __device__ __forceinline__ uint2 e4m3_codes8(const uint32_t (&w)[4], float scale, float inv) {
-  uint32_t c[2];
+  const float above = inv * (1.f + 9.5367431640625e-07f);   // 1 + 2^-20
+  uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float x[4] = {bf16lo_f32(w[2 * i]), bf16hi_f32(w[2 * i]), bf16lo_f32(w[2 * i + 1]), bf16hi_f32(w[2 * i + 1])};
-    float y[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = x[j] * inv;
-    uint32_t lo = f32x2_to_e4m3x2(y[0] * kQuotLo, y[1] * kQuotLo) | (f32x2_to_e4m3x2(y[2] * kQuotLo, y[3] * kQuotLo) << 16);
-    const uint32_t hi =
-        f32x2_to_e4m3x2(y[0] * kQuotHi, y[1] * kQuotHi) | (f32x2_to_e4m3x2(y[2] * kQuotHi, y[3] * kQuotHi) << 16);
-    if (lo != hi) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t a = (lo >> (8 * j)) & 0x7Fu, b = (hi >> (8 * j)) & 0x7Fu;
-        if (a != b) {
-          const float mid = 0.5f * (e4m3_value(a) + e4m3_value(b));
-          lo = (lo & ~(0x7Fu << (8 * j))) | (settle(a, mid, scale, fabsf(x[j])) << (8 * j));
-        }
-      }
-    }
-    c[i] = lo;
-  }
-  return make_uint2(c[0], c[1]);
+  for (int i = 0; i < 4; ++i)
+    c[i] = f32x2_to_e4m3x2(e4m3_quotient(bf16lo_f32(w[i]), scale, above), e4m3_quotient(bf16hi_f32(w[i]), scale, above));
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
 // Largest magnitude of eight bf16 values as bits (order like the values; NaN
@@ -201,7 +208,191 @@ __global__ void __launch_bounds__(kLowbitsThreads) pda_write_slot_scales_kernel(
   }
 }
 
+// V pages hold a dim's tokens side by side, rows a token's dims: 16 slots x 4 dims
+// of bytes turned in registers. in[i] = the 16 slots of dim i (four words), out[s] =
+// the 4 dims of slot s; and back.
+__device__ __forceinline__ void turn4(const uint32_t (&a)[4], uint32_t (&b)[4]) {
+  const uint32_t t0 = __byte_perm(a[0], a[1], 0x5140), t1 = __byte_perm(a[2], a[3], 0x5140);
+  const uint32_t t2 = __byte_perm(a[0], a[1], 0x7362), t3 = __byte_perm(a[2], a[3], 0x7362);
+  b[0] = __byte_perm(t0, t1, 0x5410);
+  b[1] = __byte_perm(t0, t1, 0x7632);
+  b[2] = __byte_perm(t2, t3, 0x5410);
+  b[3] = __byte_perm(t2, t3, 0x7632);
+}
+
+// A tile of 16 rows by the groups of 16 slots that hold them: group k is slots
+// 16 * part .. + 15 of block `block`; `mask` says which of them are rows of the tile,
+// `map` (4 bits a slot) which rows. Where two rows name one slot, rows make groups
+// alone. One warp; returns the number of groups.
+struct SlotGroup {
+  int block, part;
+  unsigned mask;
+  unsigned long long map;
+};
+__device__ __forceinline__ int slot_groups(int block, int slot, bool live, int lane, SlotGroup* groups) {
+  unsigned left = __ballot_sync(0xffffffffu, live && lane < 16);
+  int n = 0;
+  while (left != 0u) {
+    const int lead = __ffs((int)left) - 1;
+    const int b = __shfl_sync(0xffffffffu, block, lead), part = __shfl_sync(0xffffffffu, slot, lead) >> 4;
+    const bool mine = (left >> lane & 1u) && block == b && (slot >> 4) == part;
+    unsigned mask = __reduce_or_sync(0xffffffffu, mine ? 1u << (slot & 15) : 0u);
+    bool take = mine;
+    if (__popc((int)mask) != __popc((int)__ballot_sync(0xffffffffu, mine))) {   // a slot named twice: one row alone
+      take = lane == lead;
+      mask = 1u << (__shfl_sync(0xffffffffu, slot, lead) & 15);
+    }
+    const unsigned long long place = take ? (unsigned long long)lane << (4 * (slot & 15)) : 0ull;
+    const unsigned lo = __reduce_or_sync(0xffffffffu, (unsigned)place);
+    const unsigned hi = __reduce_or_sync(0xffffffffu, (unsigned)(place >> 32));
+    if (lane == 0) {
+      groups[n].block = b;
+      groups[n].part = part;
+      groups[n].mask = mask;
+      groups[n].map = (unsigned long long)hi << 32 | lo;
+    }
+    ++n;
+    left &= ~__ballot_sync(0xffffffffu, take);
+  }
+  return n;
+}
+
+// Tiles of 16 tokens, a warp per kv head: the rows' codes pass through shared memory,
+// K to go out 16 bytes (a chunk of a row) at a time, V by groups of 16 slots, turned
+// in registers: 16-byte rows of whole groups, and what a group holds of the tile
+// where it is cut or scattered.
+constexpr int kWriteTileThreads = 128;
+template <bool kVec>
+__global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_kernel(const LowbitsWriteParams p) {
+  __shared__ int2 rows[16];
+  __shared__ SlotGroup groups[16];
+  __shared__ int num_groups;
+  __shared__ __align__(16) uint8_t tile[kWriteTileThreads / 32][2][16][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int half = lane >> 4, l = lane & 15;
+  const int t0 = blockIdx.x * 16, bs = p.block_size, Hk = p.num_kv_heads;
+  // 8 rows of a head, two at once: row 8 * (part & 1) + 2 i + half of the keys (parts 0
+  // and 1) or values, 16 bytes a lane
+  auto load = [&](uint32_t (&w)[4][4], int h, int part) {
+    const __nv_bfloat16* src = part >= 2 ? p.v + h * p.v_head : p.k + h * p.k_head;
+    const long long step = part >= 2 ? p.v_tok : p.k_tok;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 8 * (part & 1) + 2 * i + half;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[i][j] = 0u;
+      if (t < p.num_tokens) load8<kVec>(src + t * step + 8 * l, w[i]);
+    }
+  };
+  uint32_t w[4][4], next[4][4];
+  int h = blockIdx.y * (kWriteTileThreads / 32) + warp;
+  if (h < Hk) load(w, h, 0);   // on their way while the slots are sorted out
+  if (warp == 0) {
+    const long long slot = lane < 16 && t0 + lane < p.num_tokens ? write_slot(p, t0 + lane, blockIdx.y == 0) : -1;
+    const int2 at = slot < 0 ? make_int2(-1, 0) : make_int2((int)(slot / bs), (int)(slot % bs));
+    if (lane < 16) rows[lane] = at;
+    const int n = slot_groups(at.x, at.y, at.x >= 0, lane, groups);
+    if (lane == 0) num_groups = n;
+  }
+  __syncthreads();
+  if (num_groups == 0) return;
+  const size_t page = (size_t)(128 * bs);
+  uint8_t(*kt)[128] = tile[warp][0];
+  uint8_t(*vt)[128] = tile[warp][1];
+  for (; h < Hk; h += gridDim.y * (kWriteTileThreads / 32)) {
+#pragma unroll 1
+    for (int part = 0; part < 4; ++part) {
+      const bool is_v = part >= 2;
+      if (part < 3) load(next, h, part + 1);
+      else if (h + gridDim.y * (kWriteTileThreads / 32) < Hk) load(next, h + gridDim.y * (kWriteTileThreads / 32), 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * (part & 1) + 2 * i + half;
+        const int2 at = rows[r];
+        const float scale = slot_scale(w[i], p.min_scale);
+        *reinterpret_cast<uint2*>(&(is_v ? vt : kt)[r][8 * l]) = e4m3_codes8(w[i], scale, __frcp_rn(scale));
+        if (l == 0 && at.x >= 0) (is_v ? p.v_scales : p.k_scales)[((size_t)at.x * Hk + h) * bs + at.y] = scale;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[i][j] = next[i][j];
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // consecutive lanes: consecutive rows of one chunk
+      const int r = lane & 15, c = half + 2 * i;
+      const int2 at = rows[r];
+      if (at.x >= 0)
+        *reinterpret_cast<uint4*>(p.k_cache + ((size_t)at.x * Hk + h) * page + (c * bs + at.y) * 16) =
+            *reinterpret_cast<const uint4*>(&kt[r][16 * c]);
+    }
+    for (int k = 0; k < num_groups; ++k) {
+      const SlotGroup gr = groups[k];
+      uint8_t* dst = p.v_cache + ((size_t)gr.block * Hk + h) * page + 4 * lane * bs + gr.part * 16;
+      if ((gr.mask & (gr.mask - 1u)) == 0u) {   // a token alone
+        const int s = __ffs((int)gr.mask) - 1;
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i * bs + s] = (uint8_t)(c >> (8 * i));
+        continue;
+      }
+      uint32_t v[4][4];   // [dim][four slots]
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t in[4], out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int s = 4 * q + i;
+          in[i] = gr.mask >> s & 1u ? *reinterpret_cast<const uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]) : 0u;
+        }
+        turn4(in, out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i][q] = out[i];
+      }
+      if (gr.mask == 0xFFFFu) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(dst + i * bs) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const unsigned m = gr.mask >> (4 * q) & 15u;
+          if (m == 0u) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint8_t* d = dst + i * bs + 4 * q;
+            if (m == 15u) {
+              *reinterpret_cast<uint32_t*>(d) = v[i][q];
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (m >> j & 1u) d[j] = (uint8_t)(v[i][q] >> (8 * j));
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();   // the tile is read
+  }
+}
+
 // ------------------------------------------------------------------ e2m1
+
+// Eight e2m1 codes c, of which those in d are uncertain between c and c + 1: the
+// exact sign decides. (Rare unless the tensor's scale is a power of two, and so a
+// call.)
+__device__ __noinline__ uint32_t settle_e2m1x8(uint32_t c, uint32_t d, uint4 w, float sf, float g) {
+#pragma unroll 1
+  while (d != 0u) {
+    const int i = (__ffs((int)d) - 1) >> 2;
+    d &= ~(15u << (4 * i));
+    const uint32_t q = (c >> (4 * i)) & 7u;
+    const uint32_t x = (i < 4 ? (i < 2 ? w.x : w.y) : (i < 6 ? w.z : w.w)) >> (16 * (i & 1)) & 0x7FFFu;
+    const float mid4 = (float)((0x00140E0A07050301ull >> (8 * q)) & 0xFFull);   // 4 * midpoint of q and q + 1
+    c = (c & ~(7u << (4 * i))) | (settle(q, 0.25f * mid4 * sf, g, __uint_as_float(x << 16)) << (4 * i));
+  }
+  return c;
+}
 
 // This lane's eight values (two lanes a block of 16) as e2m1 nibbles of
 // x / (s * g), and the block's e4m3 scale code s = E4M3(amax / (6 g)).
@@ -230,68 +421,48 @@ __device__ __forceinline__ uint32_t e2m1_codes8(uint32_t (&w)[4], float g, float
   *scale_code = nan ? 0x7Fu : s;
   const float sf = e4m3_value(s);
   const float inv = s == 0u ? 0.f : __frcp_rn(sf * g);
-  float x[8], lo[8], hi[8];
+  const float2 inv_lo = make_float2(inv * kQuotLo, inv * kQuotLo), inv_hi = make_float2(inv * kQuotHi, inv * kQuotHi);
+  float lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16lo_f32(w[i]);
-    x[2 * i + 1] = bf16hi_f32(w[i]);
+    const float2 x = make_float2(bf16lo_f32(w[i]), bf16hi_f32(w[i]));
+    const float2 a2 = mul_f32x2(x, inv_lo), b2 = mul_f32x2(x, inv_hi);
+    lo[2 * i] = a2.x, lo[2 * i + 1] = a2.y;
+    hi[2 * i] = b2.x, hi[2 * i + 1] = b2.y;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = x[i] * inv;
-    lo[i] = y * kQuotLo;
-    hi[i] = y * kQuotHi;
-  }
-  uint32_t c = f32x8_to_e2m1(lo);
-  const uint32_t d = c ^ f32x8_to_e2m1(hi);
-  if (d != 0u && !nan) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((d >> (4 * i)) & 7u) {
-        const uint32_t q = (c >> (4 * i)) & 7u;
-        // 4 * midpoint of codes q and q + 1
-        const float mid4 = (float)((0x00140E0A07050301ull >> (8 * q)) & 0xFFull);
-        c = (c & ~(7u << (4 * i))) | (settle(q, 0.25f * mid4 * sf, g, fabsf(x[i])) << (4 * i));
-      }
-    }
-  }
-  return c;
+  const uint32_t c = f32x8_to_e2m1(lo), d = f32x8_to_e2m1(hi);
+  return c == d || nan ? c : settle_e2m1x8(c, c ^ d, make_uint4(w[0], w[1], w[2], w[3]), sf, g);
 }
 
-// Items (a token's kv head) of kItems per warp, lanes 0-15 the key row, 16-31
-// the value row: 16 bytes a lane in, 4 bytes of codes out.
+// One warp per token and kItems of its kv heads (blockIdx.y counts them), lanes 0-15
+// the key rows, 16-31 the value rows: 16 bytes a lane in, 4 bytes of codes out.
 template <bool kVec, int kItems>
 __global__ void __launch_bounds__(kLowbitsThreads) pda_write_fp4_kernel(const LowbitsWriteParams p) {
   const int lane = threadIdx.x & 31, l = lane & 15;
   const bool is_v = lane >= 16;
-  const long long items = (long long)p.num_tokens * p.num_kv_heads;
-  const long long first = ((long long)blockIdx.x * (kLowbitsThreads / 32) + (threadIdx.x >> 5)) * kItems;
+  const long long t = (long long)blockIdx.x * (kLowbitsThreads / 32) + (threadIdx.x >> 5);
+  if (t >= p.num_tokens) return;   // whole warps
+  const int h0 = blockIdx.y * kItems, n = min(kItems, p.num_kv_heads - h0);
+  const long long slot = write_slot(p, (int)t, lane == 0 && h0 == 0);
+  const __nv_bfloat16* src = is_v ? p.v + t * p.v_tok : p.k + t * p.k_tok;
+  const long long head = is_v ? p.v_head : p.k_head;
   uint32_t w[kItems][4];
-  long long slot[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i)
+    if (i < n) load8<kVec>(src + (h0 + i) * head + 8 * l, w[i]);
+  if (slot < 0) return;
+  const int bs = p.block_size, o = (int)(slot % bs);
+  const size_t rec = (size_t)(kFp4TokenBytes * bs);
+  uint8_t* base = p.k_cache + ((size_t)(slot / bs) * p.num_kv_heads + h0) * rec;
+  const int code = is_v ? 64 * bs + 64 * o + ((4 * l) ^ (16 * (o & 2))) : 64 * o + 4 * l;
+  const int scale = is_v ? 136 * bs + (o >> 4) * 128 + (l >> 1) * 16 + fp4_scale_place(o & 15) : 128 * bs + 8 * o + (l >> 1);
 #pragma unroll
   for (int i = 0; i < kItems; ++i) {
-    slot[i] = -1;
-    if (first + i < items) {
-      const int t = (int)((first + i) / p.num_kv_heads), h = (int)((first + i) % p.num_kv_heads);
-      slot[i] = write_slot(p, t, lane == 0);
-      load8<kVec>((is_v ? p.v + t * p.v_tok + h * p.v_head : p.k + t * p.k_tok + h * p.k_head) + 8 * l, w[i]);
-    }
-  }
-  const int bs = p.block_size;
-#pragma unroll
-  for (int i = 0; i < kItems; ++i) {
-    if (slot[i] < 0) continue;   // whole warps
-    const int h = (int)((first + i) % p.num_kv_heads);
+    if (i >= n) break;
     uint32_t s;
     const uint32_t c = e2m1_codes8(w[i], is_v ? p.v_scale : p.k_scale, is_v ? p.v_inv6 : p.k_inv6, &s);
-    const int o = (int)(slot[i] % bs);
-    uint8_t* rec = p.k_cache + ((slot[i] / bs) * p.num_kv_heads + h) * (long long)(kFp4TokenBytes * bs);
-    const int at = is_v ? 64 * bs + 64 * o + ((4 * l) ^ (16 * (o & 2))) : 64 * o + 4 * l;
-    *reinterpret_cast<uint32_t*>(rec + at) = c;
-    if ((l & 1) == 0) {
-      const int b = l >> 1;
-      rec[is_v ? 136 * bs + (o >> 4) * 128 + b * 16 + fp4_scale_place(o & 15) : 128 * bs + 8 * o + b] = (uint8_t)s;
-    }
+    *reinterpret_cast<uint32_t*>(base + i * rec + code) = c;
+    if ((l & 1) == 0) base[i * rec + scale] = (uint8_t)s;
   }
 }
 
@@ -351,122 +522,145 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
 constexpr int kGatherRows = 16;        // e4m3 reader: rows of a CTA
 constexpr int kGatherMaxRows4 = 32;    // 4-bit reader: rows of a CTA at most
 
-// 4 bits: one warp per (row, kv head), lanes 0-15 the key, 16-31 the value;
-// 4 bytes of codes and one scale byte a lane in, 16 bytes out.
+// 4 bits: a warp per (row, kv head), lanes 0-15 the key, 16-31 the value; 4 bytes
+// of codes and one scale byte a lane in, 16 bytes out. The warps of a CTA take rows
+// each, or share a row's heads where a CTA has fewer rows than warps.
 __global__ void __launch_bounds__(kLowbitsThreads) pda_gather_fp4_kernel(const GatherParams p) {
   __shared__ int2 rows[kGatherMaxRows4];
   const int r0 = blockIdx.x * p.rows_per_cta;
   const int n = min(p.rows_per_cta, p.num_tokens - r0);
   if (threadIdx.x < n) rows[threadIdx.x] = gather_row(p, r0 + threadIdx.x);
   __syncthreads();
+  constexpr int kWarps = kLowbitsThreads / 32, kAhead = 4;
   const int lane = threadIdx.x & 31, l = lane & 15, warp = threadIdx.x >> 5;
   const bool is_v = lane >= 16;
   const int bs = p.block_size, Hk = p.num_kv_heads;
   const float g = is_v ? p.v_scale : p.k_scale;
-  __nv_bfloat16* out = is_v ? p.v_out : p.k_out;
-  const int items = n * Hk;
-  constexpr int kAhead = 4, kWarps = kLowbitsThreads / 32;
-  for (int i0 = warp; i0 < items; i0 += kWarps * kAhead) {
-    uint32_t c[kAhead], s[kAhead];
-    int blk[kAhead];
+  // rows_per_cta is a power of two
+  const int share = p.rows_per_cta < kWarps ? kWarps / p.rows_per_cta : 1;   // warps of a row
+  const size_t rec = (size_t)(kFp4TokenBytes * bs);
+  for (int r = warp / share; r < n; r += kWarps / share) {
+    const int2 at = rows[r];
+    if (at.x == kRowNone) continue;
+    const int o = at.y, h_first = warp % share;
+    const bool ok = at.x >= 0;   // else zeros
+    const uint8_t* base = p.k_cache + (ok ? (size_t)at.x : 0) * Hk * rec;
+    const uint8_t* code = base + (is_v ? 64 * bs + 64 * o + ((4 * l) ^ (16 * (o & 2))) : 64 * o + 4 * l);
+    const uint8_t* scale = base + (is_v ? 136 * bs + (o >> 4) * 128 + (l >> 1) * 16 + fp4_scale_place(o & 15)
+                                        : 128 * bs + 8 * o + (l >> 1));
+    __nv_bfloat16* out = (is_v ? p.v_out : p.k_out) + ((size_t)(r0 + r) * Hk) * 128 + 8 * l;
+    for (int h0 = h_first; h0 < Hk; h0 += kAhead * share) {
+      uint32_t c[kAhead], s[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int i = i0 + j * kWarps;
-      blk[j] = kRowNone;
-      c[j] = s[j] = 0u;
-      if (i < items) {
-        const int2 at = rows[i / Hk];
-        blk[j] = at.x;
-        if (at.x >= 0) {
-          const int o = at.y;
-          const uint8_t* rec = p.k_cache + ((long long)at.x * Hk + i % Hk) * (long long)(kFp4TokenBytes * bs);
-          c[j] = __ldg(reinterpret_cast<const uint32_t*>(
-              rec + (is_v ? 64 * bs + 64 * o + ((4 * l) ^ (16 * (o & 2))) : 64 * o + 4 * l)));
-          s[j] = __ldg(rec + (is_v ? 136 * bs + (o >> 4) * 128 + (l >> 1) * 16 + fp4_scale_place(o & 15)
-                                   : 128 * bs + 8 * o + (l >> 1)));
+      for (int j = 0; j < kAhead; ++j) {
+        const int h = h0 + j * share;
+        c[j] = s[j] = 0u;
+        if (ok && h < Hk) {
+          c[j] = __ldg(reinterpret_cast<const uint32_t*>(code + h * rec));
+          s[j] = __ldg(scale + h * rec);
         }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (blk[j] == kRowNone) continue;
-      const int i = i0 + j * kWarps;
-      const float f = e4m3_value(s[j]);
-      uint32_t x[4], y[4];
-      e2m1x8_to_f16x2(c[j], x);
+      for (int j = 0; j < kAhead; ++j) {
+        const int h = h0 + j * share;
+        if (h >= Hk) break;
+        const uint32_t s2 = e4m3x2_lo_to_f16x2(s[j] | (s[j] << 8));
+        uint32_t x[4], y[4];
+        e2m1x8_to_f16x2(c[j], x);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) y[u] = bf16x2_of((f16lo_f32(x[u]) * f) * g, (f16hi_f32(x[u]) * f) * g);
-      const long long row = (long long)(r0 + i / Hk) * Hk + i % Hk;
-      *reinterpret_cast<uint4*>(out + row * 128 + 8 * l) = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int u = 0; u < 4; ++u) {
+          const uint32_t v = mul_f16x2(x[u], s2);   // exact
+          y[u] = bf16x2_of(f16lo_f32(v) * g, f16hi_f32(v) * g);
+        }
+        *reinterpret_cast<uint4*>(out + (size_t)h * 128) = make_uint4(y[0], y[1], y[2], y[3]);
+      }
     }
   }
 }
 
-// 16 e4m3 codes * scale -> 16 bf16 at dst.
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const uint4& c, float scale) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-  uint32_t y[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = e4m3x2_lo_to_f16x2(w[i]), b = e4m3x2_hi_to_f16x2(w[i]);
-    y[2 * i] = bf16x2_of(f16lo_f32(a) * scale, f16hi_f32(a) * scale);
-    y[2 * i + 1] = bf16x2_of(f16lo_f32(b) * scale, f16hi_f32(b) * scale);
-  }
-  reinterpret_cast<uint4*>(dst)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  reinterpret_cast<uint4*>(dst)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-}
-
-// e4m3: 16 rows a CTA, thread 8j + c row j, dims 16c..16c+15; V, whose pages
-// hold a dim's tokens side by side, passes through shared memory: thread d
-// reads dim d's 16-byte group of tokens and hands out the rows' bytes.
-__global__ void __launch_bounds__(128) pda_gather_kernel(const GatherParams p) {
+// e4m3: 16 rows a CTA, a warp per kv head. Both tensors pass through shared memory
+// as [row][128] bytes: K 16 bytes (a chunk of a row) at a time, V by groups of 16
+// slots turned in registers; from there a half warp writes a row.
+constexpr int kGatherThreads = 128;
+__global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const GatherParams p) {
   __shared__ int2 rows[kGatherRows];
-  __shared__ __align__(16) uint8_t vt[kGatherRows][128];
-  const int tid = threadIdx.x, j = tid >> 3, c = tid & 7;
+  __shared__ SlotGroup groups[kGatherRows];
+  __shared__ int num_groups;
+  __shared__ __align__(16) uint8_t tile[kGatherThreads / 32][2][kGatherRows][128];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r0 = blockIdx.x * kGatherRows;
-  if (tid < kGatherRows) rows[tid] = r0 + tid < p.num_tokens ? gather_row(p, r0 + tid) : make_int2(kRowNone, 0);
+  if (warp == 0) {
+    const int2 at = lane < kGatherRows && r0 + lane < p.num_tokens ? gather_row(p, r0 + lane) : make_int2(kRowNone, 0);
+    if (lane < kGatherRows) rows[lane] = at;
+    const int n = slot_groups(at.x, at.y, at.x >= 0, lane, groups);
+    if (lane == 0) num_groups = n;
+  }
   __syncthreads();
   const int bs = p.block_size, Hk = p.num_kv_heads;
+  const int half = lane >> 4, l = lane & 15;
   const int h_end = min(Hk, (int)(blockIdx.y + 1) * p.heads_per_cta);
-  const int2 at = rows[j];
-  for (int h = blockIdx.y * p.heads_per_cta; h < h_end; ++h) {
-    uint4 kq = make_uint4(0u, 0u, 0u, 0u);
-    float ks = p.k_scale, vs = p.v_scale;
-    if (at.x >= 0) {
-      const long long row = (long long)at.x * Hk + h;
-      kq = __ldg(reinterpret_cast<const uint4*>(p.k_cache + row * (128 * bs) + (c * bs + at.y) * 16));
-      if (p.k_scales) {
-        ks = __ldg(p.k_scales + row * bs + at.y);
-        vs = __ldg(p.v_scales + row * bs + at.y);
-      }
-    } else {
-      ks = vs = 0.f;
-    }
-    {
-      uint4 grp = make_uint4(0u, 0u, 0u, 0u);
-      int have_b = kRowNone, have_g = -1;
+  const size_t page = (size_t)(128 * bs);
+  const int2 own = rows[l];   // this lane's row, for its scale
+  for (int h = blockIdx.y * p.heads_per_cta + warp; h < h_end; h += kGatherThreads / 32) {
+    uint8_t(*kt)[128] = tile[warp][0];
+    uint8_t(*vt)[128] = tile[warp][1];
+    float scale = half ? p.v_scale : p.k_scale;   // of row l, key (lanes 0-15) or value
+    if (p.k_scales && own.x >= 0) scale = __ldg((half ? p.v_scales : p.k_scales) + ((size_t)own.x * Hk + h) * bs + own.y);
+    uint4 kq[4];
 #pragma unroll
-      for (int i = 0; i < kGatherRows; ++i) {
-        const int2 a = rows[i];
-        if (a.x >= 0 && (a.x != have_b || (a.y >> 4) != have_g)) {   // the same for all threads
-          have_b = a.x;
-          have_g = a.y >> 4;
-          const uint8_t* page = p.v_cache + ((long long)a.x * Hk + h) * (128 * bs);
-          grp = __ldg(reinterpret_cast<const uint4*>(page + (p.v_shuffled ? (have_g * 128 + tid) * 16
-                                                                          : tid * bs + have_g * 16)));
+    for (int i = 0; i < 4; ++i) {
+      const int2 at = rows[(lane >> 3) + 4 * i];
+      kq[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (at.x >= 0)
+        kq[i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + ((size_t)at.x * Hk + h) * page + ((lane & 7) * bs + at.y) * 16));
+    }
+    for (int k = 0; k < num_groups; ++k) {
+      const SlotGroup gr = groups[k];
+      const uint8_t* src = p.v_cache + ((size_t)gr.block * Hk + h) * page;
+      src += p.v_shuffled ? (gr.part * 128 + 4 * lane) * 16 : 4 * lane * bs + gr.part * 16;
+      const int step = p.v_shuffled ? 16 : bs;
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t in[4] = {q == 0 ? v[0].x : q == 1 ? v[0].y : q == 2 ? v[0].z : v[0].w,
+                                q == 0 ? v[1].x : q == 1 ? v[1].y : q == 2 ? v[1].z : v[1].w,
+                                q == 0 ? v[2].x : q == 1 ? v[2].y : q == 2 ? v[2].z : v[2].w,
+                                q == 0 ? v[3].x : q == 1 ? v[3].y : q == 2 ? v[3].z : v[3].w};
+        uint32_t out[4];
+        turn4(in, out);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int s = 4 * q + i;
+          if (gr.mask >> s & 1u) *reinterpret_cast<uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]) = out[i];
         }
-        const int o = a.y & 15;
-        const uint32_t w = o < 8 ? (o < 4 ? grp.x : grp.y) : (o < 12 ? grp.z : grp.w);
-        vt[i][tid] = a.x >= 0 ? (uint8_t)(w >> (8 * (o & 3))) : (uint8_t)0;
       }
     }
-    __syncthreads();
-    if (at.x != kRowNone) {
-      const long long row = (long long)(r0 + j) * Hk + h;
-      store16(p.k_out + row * 128 + 16 * c, kq, ks);
-      store16(p.v_out + row * 128 + 16 * c, *reinterpret_cast<const uint4*>(&vt[j][16 * c]), vs);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(&kt[(lane >> 3) + 4 * i][16 * (lane & 7)]) = kq[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      // two rows at once: keys of rows 0 .. 15, then values
+      const int r = (2 * i + half) & 15;
+      const bool is_v = i >= kGatherRows / 2;
+      const int st = rows[r].x;
+      const float f = __shfl_sync(0xffffffffu, scale, r + (is_v ? 16 : 0));
+      const uint2 c = *reinterpret_cast<const uint2*>(&(is_v ? vt : kt)[r][8 * l]);
+      if (st == kRowNone) continue;
+      uint32_t y[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint32_t w = u < 2 ? c.x : c.y;
+        const uint32_t x = u & 1 ? e4m3x2_hi_to_f16x2(w) : e4m3x2_lo_to_f16x2(w);
+        y[u] = bf16x2_of(f16lo_f32(x) * f, f16hi_f32(x) * f);
+      }
+      uint4 o = make_uint4(y[0], y[1], y[2], y[3]);
+      if (st < 0) o = make_uint4(0u, 0u, 0u, 0u);
+      *reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + ((size_t)(r0 + r) * Hk + h) * 128 + 8 * l) = o;
     }
-    __syncthreads();
+    __syncwarp();   // the tile is read
   }
 }
 

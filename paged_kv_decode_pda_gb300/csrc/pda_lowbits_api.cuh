@@ -5,6 +5,9 @@
 
 namespace {
 
+// Rows (a token's kv head) up to which the slot-scale writer gives each a warp.
+constexpr long long kSlotScalesMaxRows = 4096;
+
 // Scales that the quantising writers take: with them every midpoint's product
 // is a normal number whose last bit binary32 holds, so that its sign is exact.
 bool scale_in_range(float x) { return x >= 0x1p-100f && x <= 0x1p100f; }   // false for NaN
@@ -75,12 +78,12 @@ pda_status gather_e4m3(pda::GatherParams& p, const void* k_cache, const void* v_
   p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
   const int tiles = (p.num_tokens + pda::kGatherRows - 1) / pda::kGatherRows;
-  // Heads of a CTA: all, unless that leaves fewer than 8 CTAs an SM.
+  // Heads of a CTA of four warps: all, unless that leaves fewer than 4 CTAs an SM.
   int per = p.num_kv_heads;
-  while (per > 1 && (long long)tiles * ((p.num_kv_heads + per - 1) / per) < 8 * 152) per = (per + 1) / 2;
+  while (per > 4 && (long long)tiles * ((p.num_kv_heads + per - 1) / per) < 4 * 152) per = (per + 1) / 2;
   p.heads_per_cta = per;
   const dim3 grid((unsigned)tiles, (unsigned)((p.num_kv_heads + per - 1) / per));
-  pda::pda_gather_kernel<<<grid, 128, 0, stream>>>(p);
+  pda::pda_gather_kernel<<<grid, pda::kGatherThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
@@ -149,11 +152,21 @@ pda_status pda_reshape_and_cache_slot_scales(const pda_token_rows* key, const pd
   p.k_scales = k_scales;
   p.v_scales = v_scales;
   p.min_scale = min_scale;
+  // Few rows: a warp each, whatever the slots. More: tiles of 16 tokens, whose V codes
+  // go out by groups of slots (us with a warp a row / tiles, 8 kv heads: 256 tokens in
+  // whole blocks 6.5 / 8.6, scattered 5.9 / 17.6; 512 10.3 / 8.7, 8.5 / 17.8; 1024 16.0 /
+  // 8.6, 12.8 / 19.8; 8192 84.1 / 21.0, 75.6 / 76.5).
   const long long items = (long long)num_tokens * num_kv_heads;
-  const long long blocks = (items + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32);
-  if (blocks > INT32_MAX) return PDA_ERR_UNSUPPORTED;
-  if (vec) pda::pda_write_slot_scales_kernel<true><<<(unsigned)blocks, pda::kLowbitsThreads, 0, stream>>>(p);
-  else pda::pda_write_slot_scales_kernel<false><<<(unsigned)blocks, pda::kLowbitsThreads, 0, stream>>>(p);
+  if (items <= kSlotScalesMaxRows) {
+    const unsigned blocks = (unsigned)((items + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32));
+    if (vec) pda::pda_write_slot_scales_kernel<true><<<blocks, pda::kLowbitsThreads, 0, stream>>>(p);
+    else pda::pda_write_slot_scales_kernel<false><<<blocks, pda::kLowbitsThreads, 0, stream>>>(p);
+  } else {
+    const int warps = pda::kWriteTileThreads / 32;
+    const dim3 grid((unsigned)((num_tokens + 15) / 16), (unsigned)((num_kv_heads + warps - 1) / warps));
+    if (vec) pda::pda_write_slot_scales_tile_kernel<true><<<grid, pda::kWriteTileThreads, 0, stream>>>(p);
+    else pda::pda_write_slot_scales_tile_kernel<false><<<grid, pda::kWriteTileThreads, 0, stream>>>(p);
+  }
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
@@ -177,11 +190,16 @@ pda_status pda_reshape_and_cache_fp4(const pda_token_rows* key, const pda_token_
   p.v_scale = v_scale;
   p.k_inv6 = (float)(1.0 / (6.0 * (double)k_scale));
   p.v_inv6 = (float)(1.0 / (6.0 * (double)v_scale));
-  const long long items = (long long)num_tokens * num_kv_heads;
-  const long long blocks = (items + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32);
-  if (blocks > INT32_MAX) return PDA_ERR_UNSUPPORTED;
-  if (vec) pda::pda_write_fp4_kernel<true, 1><<<(unsigned)blocks, pda::kLowbitsThreads, 0, stream>>>(p);
-  else pda::pda_write_fp4_kernel<false, 1><<<(unsigned)blocks, pda::kLowbitsThreads, 0, stream>>>(p);
+  // Heads of a warp: four, whose loads overlap; one where four leave fewer than 16
+  // warps an SM.
+  const bool four = (long long)num_tokens * num_kv_heads >= 4ll * 16 * 152;
+  const int per = four ? 4 : 1;
+  const dim3 grid((unsigned)((num_tokens + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32)),
+                  (unsigned)((num_kv_heads + per - 1) / per));
+  if (four && vec) pda::pda_write_fp4_kernel<true, 4><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
+  else if (four) pda::pda_write_fp4_kernel<false, 4><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
+  else if (vec) pda::pda_write_fp4_kernel<true, 1><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
+  else pda::pda_write_fp4_kernel<false, 1><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
@@ -317,8 +335,8 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     p.pages_per_chunk = per;
     p.group = group;
     p.tiles = tiles;
-    p.bs_inverse = ((1ull << 40) + block_size - 1) / block_size;
-    p.chunk_inverse = ((1ull << 40) + per - 1) / per;
+    p.bs_inverse = ((1ull << 37) + block_size - 1) / block_size;
+    p.chunk_inverse = ((1ull << 37) + per - 1) / per;
     p.logit_scale_log2 = (float)std::fabs(logit);
     p.negate = logit < 0.0 ? 1 : 0;
     p.v_scale = v_scale;
