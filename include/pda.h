@@ -27,8 +27,10 @@
  *
  * Around that call: the cache write (pda_reshape_and_cache), rotary positions
  * alone or with it (pda_rope, pda_rope_and_cache), attention of chunks of new
- * tokens over the same cache (pda_extend), and the bookkeeping of its pages
- * (pda_grow_pages and the calls beside it).
+ * tokens over the same cache (pda_extend), the bookkeeping of its pages
+ * (pda_grow_pages and the calls beside it), and caches in fewer bits: scales per
+ * slot and 4-bit records, their writers and readers, and decode attention over 4
+ * bits (pda_decode_fp4).
  *
  * Threading and ordering. Every entry point is thread-safe. pda_decode is
  * stream-ordered: it validates on the host, enqueues its kernels on `stream`
@@ -636,9 +638,10 @@ typedef struct pda_token_rows {
  * included), NaN kept. min_scale keeps rows of zeros from a scale of zero, and
  * the scales of one context within pda_decode_slot_scales' ratio of 2^15; it
  * must lie in [2^-100, 2^100].
- * Layouts (the native one), slot_mapping, padding, slots past the pool and
- * repeated slots as for pda_reshape_and_cache. Stream-ordered, no workspace,
- * capturable.
+ * Layouts (the native one), slot_mapping, padding and slots past the pool as for
+ * pda_reshape_and_cache; a slot that the call names twice ends with codes and
+ * scales of either token, not necessarily all of one. Stream-ordered, no
+ * workspace, capturable.
  */
 pda_status pda_reshape_and_cache_slot_scales(const pda_token_rows* key, const pda_token_rows* value, void* k_cache,
                                              void* v_cache, float* k_scales, float* v_scales,
@@ -693,9 +696,9 @@ pda_status pda_reshape_and_cache_fp4(const pda_token_rows* key, const pda_token_
  * outside [0, num_blocks), gets zeros and sets bit 64 of the device status word.
  * The value is code * scale in binary32, rounded to bf16. The slot-scale form
  * reads scales [num_blocks][num_kv_heads][block_size] and the native layout; the
- * 4-bit form reads records. Pointers 16-byte aligned (tables, starts, first,
- * scales 4-byte), on the current device. Stream-ordered, no workspace,
- * capturable.
+ * 4-bit form reads records. k_out and v_out must not overlap. Pointers 16-byte
+ * aligned (tables, starts, first, scales 4-byte), on the current device.
+ * Stream-ordered, no workspace, capturable.
  */
 pda_status pda_gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
                             const int32_t* block_tables, const int32_t* token_starts, const int32_t* first,
@@ -735,10 +738,7 @@ pda_status pda_gather_cache_fp4(void* k_out, void* v_out, const void* kv_cache, 
  * Needs a workspace per (device, stream), of one size (some 18 MB): made by the
  * first call, or by pda_reserve_fp4, which a stream needs before its first
  * capture (else PDA_ERR_WORKSPACE), and freed by pda_release. Graphs that
- * captured calls of one stream share it and must not run at the same time. A call
- * that gave up on a wait (bit 1 or 32 of the device status word) leaves its
- * counters unfinished; pda_query_device_status, which reports the bit, puts them
- * right.
+ * captured calls of one stream share it and must not run at the same time.
  */
 pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
                           const int32_t* seq_lens, int num_seqs, int num_heads, int num_kv_heads, int head_size,
@@ -931,7 +931,7 @@ pda_status pda_release(void);
 
 /*
  * pda_workspace_info -- the decode workspace of (current device, stream; the
- * one that pda_extend and the page calls share is apart): *bytes
+ * one that pda_extend and the page calls share, and pda_decode_fp4's, are apart): *bytes
  * receives its current size (0 when it has none) and *retired the number of
  * smaller buffers it replaced that are still allocated for graphs that
  * captured them. Diagnostic; host only, no synchronisation.
@@ -944,8 +944,8 @@ pda_status pda_workspace_info(cudaStream_t stream, long long* bytes, int* retire
  * kernel since the last query finished normally, or a nonzero code when a
  * kernel gave up on a bounded wait, or skipped or redirected an access
  * outside the pool (a cache-write slot past the pool: bit 16; with
- * pda_set_block_check, or in the page calls, a block id outside the pool: bit
- * 64), or refused a page request (bit 128, which changes nothing); the output
+ * pda_set_block_check, or in the page calls, pda_gather_cache* and
+ * pda_decode_fp4, a block id outside the pool: bit 64), or refused a page request (bit 128, which changes nothing); the output
  * of that call is then undefined but for what the call says of it. Returns PDA_ERR_DEVICE_TIMEOUT when
  * *code != 0. Test / debug call: it blocks.
  */

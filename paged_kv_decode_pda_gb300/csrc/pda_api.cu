@@ -58,9 +58,6 @@ KernelKind per_unit_of(KernelKind k) {
 
 // Forgets pda_decode_noalloc's per-device set-up (defined with it below).
 void noalloc_forget_devices();
-// Zeroes the piece counters of pda_decode_fp4's workspaces on the current device,
-// which a call that gave up on a wait leaves unfinished (defined with it).
-pda_status fp4_zero_counters();
 
 struct DeviceInfo {
   int sm_count = 0;
@@ -1207,8 +1204,6 @@ pda_status pda_query_device_status(cudaStream_t stream, int* code) {
   if (cudaMemcpyFromSymbol(&v, pda::g_status, sizeof v) != cudaSuccess) return PDA_ERR_CUDA;
   if (cudaMemcpyToSymbol(pda::g_status, &zero, sizeof zero) != cudaSuccess) return PDA_ERR_CUDA;
   *code = (int)v;
-  constexpr unsigned int kGaveUp = pda::kStatusFullWaitTimeout | pda::kStatusEmptyWaitTimeout | pda::kStatusMergeWaitTimeout;
-  if ((v & kGaveUp) && fp4_zero_counters() != PDA_OK) return PDA_ERR_CUDA;
   return v ? PDA_ERR_DEVICE_TIMEOUT : PDA_OK;
 }
 

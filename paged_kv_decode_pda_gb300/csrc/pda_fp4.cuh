@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4CtasPerSm) pda_fp4_decode_kerne
       if (done && lane == 0 && pieces > 1 && (int)run == run0) {
         const int many = pieces > kF4FewPieces ? 1 : 0;
         const unsigned at = atomicAdd(&p.head->cuts[many], 1u);
-        p.head->cut[many ? kF4MaxCtas - 1u - at : at] = make_int4(s, hg * hw, run0, pieces);
+        if (at < (unsigned)kF4MaxCtas) p.head->cut[many ? kF4MaxCtas - 1u - at : at] = make_int4(s, hg * hw, run0, pieces);
       }
       const int np = min(PPC, a.n - ci * PPC), t0 = (a.first + ci * PPC) * bs;
       const bool got = mbar_wait_bounded(empty0 + 8u * stage, parity, abort_flag, kWaitLimitNs);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4CtasPerSm) pda_fp4_decode_kerne
       if (__all_sync(0xffffffffu, got)) {
         if (lane == 0) {
           notes[stage].flags = kHdrEnd;
-            mbar_arrive(full0 + 8u * stage);
+          mbar_arrive(full0 + 8u * stage);
         }
         ++fill;
       } else if (lane == 0) {
@@ -711,9 +711,9 @@ __global__ void __launch_bounds__(kF4Threads, kF4CtasPerSm) pda_fp4_decode_kerne
 }
 
 // The join, a programmatic dependent of the decode kernel. Rows of few pieces: a
-// warp each. Rows of many (long sequences): a CTA
-// each, its warps taking every eighth piece. The order of the additions is the
-// pieces' alone.
+// warp each. Rows of many (long sequences): a CTA each, its warps taking every
+// eighth piece. The order of the additions is the pieces' alone. It runs and
+// empties the lists also when CTAs of the decode kernel gave up on a wait.
 constexpr int kF4JoinThreads = 256;
 constexpr int kF4JoinWarps = kF4JoinThreads / 32;
 constexpr int kF4JoinCtas = 760;
@@ -774,10 +774,11 @@ __global__ void __launch_bounds__(kF4JoinThreads, 5) pda_fp4_join_kernel(const F
   grid_dependency_wait();
   if (threadIdx.x < 2) cuts[threadIdx.x] = min((int)__ldcg(&p.head->cuts[threadIdx.x]), kF4MaxCtas);
   __syncthreads();
-  // Entry i of the list (a call that gave up on a wait may have left any).
+  // Entry i of the lists; whatever it holds, what it names lies in bounds.
   auto cut_of = [&](int i) {
     int4 c = __ldcg(p.head->cut + i);
-    if (c.x < 0 || c.x >= p.num_seqs || c.y < 0 || c.y + p.group > p.num_kv_heads || c.z < 0 || c.z + c.w > kF4MaxCtas) c.w = 0;
+    if (c.x < 0 || c.x >= p.num_seqs || c.y < 0 || c.y + p.group > p.num_kv_heads || c.z < 0 || c.w > kF4MaxCtas - c.z)
+      c.w = 0;
     return c;
   };
   for (int r = blockIdx.x * kF4JoinWarps + warp; r < cuts[0] * per; r += gridDim.x * kF4JoinWarps) {

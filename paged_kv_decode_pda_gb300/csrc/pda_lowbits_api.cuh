@@ -17,7 +17,7 @@ pda_status write_checks(const pda_token_rows* key, const pda_token_rows* value, 
   if (!key || !value || num_tokens < 0 || num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks < 0)
     return PDA_ERR_INVALID_ARG;
   if (head_size != kHeadDim || block_size % 16 != 0 || block_size > 128 || num_kv_heads > 65535 ||
-      num_blocks > INT32_MAX)
+      num_blocks > INT32_MAX || num_tokens > INT32_MAX - 64)
     return PDA_ERR_UNSUPPORTED;
   return PDA_OK;
 }
@@ -56,7 +56,7 @@ pda_status gather_checks(int num_tokens, int num_seqs, int num_kv_heads, int hea
 pda_status gather_fill(pda::GatherParams& p, void* k_out, void* v_out, const int32_t* block_tables,
                        const int32_t* token_starts, const int32_t* first, int num_tokens, int num_seqs,
                        int num_kv_heads, int block_size, int max_blocks, long long num_blocks) {
-  if (!k_out || !v_out || !token_starts || (max_blocks > 0 && !block_tables) || !aligned16(k_out) || !aligned16(v_out) ||
+  if (!k_out || !v_out || k_out == v_out || !token_starts || (max_blocks > 0 && !block_tables) || !aligned16(k_out) || !aligned16(v_out) ||
       misaligned(block_tables, 4) || misaligned(token_starts, 4) || misaligned(first, 4))
     return PDA_ERR_INVALID_ARG;
   p.k_out = static_cast<__nv_bfloat16*>(k_out);
@@ -114,16 +114,6 @@ constexpr size_t kFp4HeadBytes = (sizeof(pda::Fp4Head) + 255) / 256 * 256;
 pda_status fp4_workspace(int dev, cudaStream_t stream, void** ws) {
   const size_t bytes = kFp4HeadBytes + (size_t)pda::kF4Slots * pda::kF4PieceFloats * sizeof(float);
   return grow_workspace(g_fp4_ws, dev, stream, bytes, kFp4HeadBytes, ws);
-}
-
-pda_status fp4_zero_counters() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return PDA_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(g_ws_mu);
-  for (auto& kv : g_fp4_ws)
-    if (kv.first.first == dev && kv.second.ptr && cudaMemset(kv.second.ptr, 0, kFp4HeadBytes) != cudaSuccess)
-      return PDA_ERR_CUDA;
-  return cudaDeviceSynchronize() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
 }  // namespace
@@ -355,7 +345,9 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = attr;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, pda::pda_fp4_join_kernel, p) == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&lc, pda::pda_fp4_join_kernel, p) == cudaSuccess) return PDA_OK;
+    cudaMemsetAsync(ws, 0, kFp4HeadBytes, stream);   // the lists that the join would have emptied
+    return PDA_ERR_CUDA;
   });
 }
 

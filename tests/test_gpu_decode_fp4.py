@@ -1,5 +1,10 @@
 """Decode attention over the 4-bit cache against the plain form in 64 bits (tolerances: lowbits_util.decode64)."""
 
+import pathlib
+import subprocess
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -132,6 +137,78 @@ def test_many_sequences():
     lens = torch.randint(0, 40, (1500,), generator=g).tolist()
     lens[700] = 3000
     Batch(lens, 4, 1, 16, seed=22).check()
+
+
+@pytest.mark.parametrize("H,Hk,bs", [(32, 8, 16), (40, 8, 64), (4, 4, 48), (8, 2, 16), (6, 2, 32), (8, 1, 128), (21, 3, 16), (16, 4, 128)])
+@pytest.mark.parametrize("window,with_sinks", [(0, False), (100, True), (333, False)])
+def test_wide_tables(H, Hk, bs, window, with_sinks):
+    """Tables with room for long contexts: the larger chunks, by every number of heads to a unit."""
+    b = Batch([1, 63, 64, 65, 255, 256, 257, 0, 1100, 16, 513, 500], H, Hk, bs, seed=H + bs + window, extra=8000)
+    b.check(window=window, sinks=torch.randn(H, generator=gen(6)) if with_sinks else None)
+
+
+def test_lengths_below_zero_are_empty():
+    b = Batch([40, 0, 64], 4, 2, 16, seed=2)
+    want = b.run()
+    b.lens = [40, -5, 64]
+    assert torch.equal(want, b.run())
+    b.lens = [40, -(1 << 31), 64]
+    assert torch.equal(want, b.run())
+
+
+def test_threads_on_one_stream():
+    """Calls of several threads on one stream take the workspace one after the other."""
+    batches = [Batch([500, 30, 2000], 8, 2, 16, seed=61), Batch([100, 900], 40, 8, 32, seed=62), Batch([1, 7000], 8, 1, 64, seed=63)]
+    want = [b.run() for b in batches]
+    dev = [[x.to(DEV) for x in (b.q, b.cache, b.tables, torch.tensor(b.lens, dtype=torch.int32))] for b in batches]
+    torch.cuda.synchronize()
+    outs = [[] for _ in batches]
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            for _ in range(30):
+                outs[i].append(pda.decode_fp4(*dev[i], 128 ** -0.5, KS, VS))
+
+    stream = torch.cuda.Stream()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(batches))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(len(batches)):
+        assert len(outs[i]) == 30 and all(torch.equal(x, want[i]) for x in outs[i])
+    assert pda.query_device_status() == 0
+
+
+def test_first_call_of_a_process_is_captured():
+    """reserve_fp4, then a capture: nothing of the kernels was loaded before."""
+    code = """
+import torch, paged_kv_decode_pda_gb300 as pda
+from tests.test_gpu_decode_fp4 import Batch, DEV, KS, VS
+b = Batch([500, 30, 2000], 8, 2, 16, seed=31)
+d = [x.to(DEV) for x in (b.q, b.cache, b.tables, torch.tensor(b.lens, dtype=torch.int32))]
+out = torch.zeros_like(d[0])
+side = torch.cuda.Stream()
+pda.reserve_fp4(side)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):
+    pda.decode_fp4(*d, 128 ** -0.5, KS, VS, out=out)
+graph.replay()
+torch.cuda.synchronize()
+b.check(got=out)
+"""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_released_and_made_again():
+    b = Batch([500, 30, 2000], 8, 2, 16, seed=31)
+    want = b.run()
+    torch.cuda.synchronize()
+    pda.release()
+    assert torch.equal(want, b.run())
 
 
 def test_lengths_past_the_table_row_are_cut():

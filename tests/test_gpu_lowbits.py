@@ -134,6 +134,62 @@ def test_write_fp4(T, Hk, bs, kind, layout, ks, vs):
     assert pda.query_device_status() == 0
 
 
+# past 4096 rows (tiles of 16 tokens), and past 9728 (four heads of a token to a warp)
+MANY = [(600, 8, 16, "blocks", "plain"), (1100, 9, 32, "run", "packed"), (530, 9, 64, "scattered", "odd"),
+        (2100, 2, 128, "blocks", "heads_first"), (4105, 1, 48, "run", "plain"), (1300, 10, 16, "scattered", "odd"),
+        (2600, 5, 16, "run", "heads_first"), (9800, 1, 64, "scattered", "packed")]
+
+
+@pytest.mark.parametrize("T,Hk,bs,kind,layout", MANY)
+def test_write_many_slot_scales(T, Hk, bs, kind, layout):
+    test_write_slot_scales(T, Hk, bs, kind, layout, MIN)
+
+
+@pytest.mark.parametrize("T,Hk,bs,kind,layout", MANY)
+def test_write_many_fp4(T, Hk, bs, kind, layout):
+    test_write_fp4(T, Hk, bs, kind, layout, 0.0043, 0.0039)
+
+
+def test_write_many_in_any_order():
+    """Slots in descending order, and runs that change blocks inside a tile: every way a tile's tokens fall into groups of 16 slots."""
+    T, Hk, bs = 600, 8, 32
+    NB = T // bs + 3
+    k, v = tokens(T, Hk, 50, "plain")
+    g = gen(51)
+    runs = torch.randperm(T // 5, generator=g)
+    for slots in (T + 20 - torch.arange(T), (runs[:, None] * 5 + torch.arange(5)).flatten() + 3):
+        kc, vc = (torch.zeros(NB, Hk, *s, dtype=torch.uint8, device=DEV) for s in ((8, bs, 16), (128, bs)))
+        ks, vs = (torch.zeros(NB, Hk, bs, device=DEV) for _ in range(2))
+        pda.reshape_and_cache_slot_scales(k, v, kc, vc, ks, vs, slots.to(DEV))
+        b, o = slots // bs, slots % bs
+        for x, cache, scales in ((k, kc.cpu().permute(0, 3, 1, 2, 4).reshape(NB, bs, Hk, 128), ks),
+                                 (v, vc.cpu().permute(0, 3, 1, 2), vs)):
+            codes, s = U.quantize_rows8(x.cpu(), MIN)
+            got = cache[b, o]
+            assert ((got == codes) | (((got & 0x7F) == 0x7F) & ((codes & 0x7F) == 0x7F))).all()
+            assert torch.equal(scales.cpu().permute(0, 2, 1)[b, o], s)
+            assert int((scales != 0).sum()) == T * Hk
+
+
+def test_write_many_with_repeated_slots():
+    """Rows of one content at one slot leave that content, also several in a tile; the neighbours stay whole."""
+    T, Hk, bs = 600, 8, 16
+    k, v = tokens(T, Hk, 52, "plain")
+    slots = torch.arange(T)
+    for a, b in ((17, 18), (20, 31), (21, 31), (100, 500), (599, 0), (64, 79), (65, 79), (66, 79)):
+        k[a], v[a], slots[a] = k[b], v[b], slots[b]
+    NB = -(-T // bs)
+    kc, vc = (torch.zeros(NB, Hk, *s, dtype=torch.uint8, device=DEV) for s in ((8, bs, 16), (128, bs)))
+    ks, vs = (torch.zeros(NB, Hk, bs, device=DEV) for _ in range(2))
+    pda.reshape_and_cache_slot_scales(k, v, kc, vc, ks, vs, slots.to(DEV))
+    for x, cache, scales in ((k, kc.cpu().permute(0, 3, 1, 2, 4).reshape(NB, bs, Hk, 128), ks), (v, vc.cpu().permute(0, 3, 1, 2), vs)):
+        codes, s = U.quantize_rows8(x.cpu(), MIN)
+        got = cache[slots // bs, slots % bs]
+        assert ((got == codes) | (((got & 0x7F) == 0x7F) & ((codes & 0x7F) == 0x7F))).all()
+        assert torch.equal(scales.cpu().permute(0, 2, 1)[slots // bs, slots % bs], s)
+    assert int((ks.permute(0, 2, 1).reshape(-1, Hk)[[17, 20, 21, 100, 599, 64, 65, 66]] != 0).sum()) == 0
+
+
 def test_writes_skip_slots_past_the_pool():
     k, v = tokens(3, 2, 1, "plain")
     slots = torch.tensor([5, 16 * 2, -1], device=DEV)

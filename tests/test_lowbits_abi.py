@@ -60,7 +60,7 @@ def test_write_fp4_refuses(lib, kw, status):
     assert write4(lib, **kw) == status
 
 
-def gather(lib, kind, ko=A, vo=A, kc=A, vc=A, ksc=A, vsc=A, tab=A, st=A, fi=A, T=4, S=2, K=8, D=128, bs=16, MB=4, NB=4, ks=0.1,
+def gather(lib, kind, ko=A, vo=A + 4096, kc=A, vc=A, ksc=A, vsc=A, tab=A, st=A, fi=A, T=4, S=2, K=8, D=128, bs=16, MB=4, NB=4, ks=0.1,
            vs=0.1, layout=0):
     tail = (tab, st, fi, T, S, K, D, bs, MB, NB)
     if kind == "e4m3":
@@ -72,7 +72,7 @@ def gather(lib, kind, ko=A, vo=A, kc=A, vc=A, ksc=A, vsc=A, tab=A, st=A, fi=A, T
 
 @pytest.mark.parametrize("kind", ["e4m3", "slots", "fp4"])
 @pytest.mark.parametrize("kw,status", [
-    (dict(ko=None), INVALID), (dict(vo=A + 8), INVALID), (dict(kc=None), INVALID), (dict(kc=A + 4), INVALID),
+    (dict(ko=None), INVALID), (dict(vo=A + 8), INVALID), (dict(vo=A), INVALID), (dict(kc=None), INVALID), (dict(kc=A + 4), INVALID),
     (dict(tab=None), INVALID), (dict(tab=A + 2), INVALID), (dict(st=None), INVALID), (dict(st=A + 1), INVALID),
     (dict(fi=A + 2), INVALID), (dict(T=-1), INVALID), (dict(S=-1), INVALID), (dict(K=0), INVALID), (dict(K=65536), UNSUPPORTED),
     (dict(D=64), UNSUPPORTED), (dict(bs=20), UNSUPPORTED), (dict(MB=-1), INVALID), (dict(MB=1 << 27), UNSUPPORTED),
