@@ -144,8 +144,8 @@ pda_status pda_reshape_and_cache_slot_scales(const pda_token_rows* key, const pd
   p.min_scale = min_scale;
   // Few rows: a warp each, whatever the slots. More: tiles of 16 tokens, whose V codes
   // go out by groups of slots (us with a warp a row / tiles, 8 kv heads: 256 tokens in
-  // whole blocks 6.5 / 8.6, scattered 5.9 / 17.6; 512 10.3 / 8.7, 8.5 / 17.8; 1024 16.0 /
-  // 8.6, 12.8 / 19.8; 8192 84.1 / 21.0, 75.6 / 76.5).
+  // whole blocks 6.3 / 7.2, scattered 5.5 / 15.7; 512 9.8 / 7.3, 8.2 / 16.2; 1024 16.3 /
+  // 7.2, 12.5 / 18.6; 8192 82.7 / 16.2, 75.5 / 74.2).
   const long long items = (long long)num_tokens * num_kv_heads;
   if (items <= kSlotScalesMaxRows) {
     const unsigned blocks = (unsigned)((items + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32));
