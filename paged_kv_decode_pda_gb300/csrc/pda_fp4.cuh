@@ -46,7 +46,10 @@
 //
 // The running maximum is let fall up to 8 (log2) behind: P stays below 2^8, well
 // inside f16, and nearly every tile passes with one vote in place of a maximum
-// over the lanes and a rescale.
+// over the lanes and a rescale. The reference is an unscaled logit, taken off the
+// others before the scale, so that the weight of the reference itself is exactly 1
+// at any size (a scaled one leaves the rounding of a product as a power of two:
+// infinite in f16 from 2^27 on).
 #pragma once
 
 #include "pda_kernels.cuh"
@@ -172,8 +175,9 @@ struct Fp4Worker {
   int gid, tig;
   uint32_t k_off, v_off, ks_off, vs_off;
   uint32_t qf[kChunks][2];
-  float lsc0, lsc1;
-  float m0, m1, l0, l1;     // running reference (log2, at most the lag below the maximum), sums
+  float2 lsc;               // log2 units of an unscaled logit, >= 0
+  float2 nr;                // minus the running reference: an unscaled logit, at most the lag below the maximum
+  float l0, l1;             // sums
   float t0, t1;             // unscaled logits past which the reference moves
   float o[kChunks][4];      // dims 16 gid + 2 mt (0, 1) and 16 gid + 2 mt + 1 (2, 3); heads 2 tig, 2 tig + 1
 
@@ -189,18 +193,23 @@ struct Fp4Worker {
   // The state of a unit, when one has ended: nothing of it is held in registers
   // through what ends it.
   __device__ __forceinline__ void reset() {
-    m0 = m1 = t0 = t1 = -INFINITY;
-    l0 = l1 = lsc0 = lsc1 = 0.f;
+    nr.x = nr.y = INFINITY;
+    t0 = t1 = -INFINITY;
+    l0 = l1 = lsc.x = lsc.y = 0.f;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) qf[i][0] = qf[i][1] = 0u;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
 
+  // The reference in log2 units.
+  __device__ __forceinline__ float m0() const { return nr.x == INFINITY ? -INFINITY : -nr.x * lsc.x; }
+  __device__ __forceinline__ float m1() const { return nr.y == INFINITY ? -INFINITY : -nr.y * lsc.y; }
+
   // Q^T fragments of the row at qrow: k step c's slots (2 tig, 2 tig + 1),
   // (2 tig + 8, 2 tig + 9) are dims 32 tig + 4c .. + 3. Each row is shifted by a
   // power of two that puts its largest |q| into [2^14, 2^15).
-  __device__ __forceinline__ void load_q(const __nv_bfloat16* qrow, bool live, float lsc, bool negate) {
+  __device__ __forceinline__ void load_q(const __nv_bfloat16* qrow, bool live, float unit, bool negate) {
     uint2 v[kChunks];
     uint32_t mx = 0u;
 #pragma unroll
@@ -221,8 +230,8 @@ struct Fp4Worker {
       qf[c][0] = pack_f16x2(bf16lo_f32(v[c].x) * down, bf16hi_f32(v[c].x) * down);
       qf[c][1] = pack_f16x2(bf16lo_f32(v[c].y) * down, bf16hi_f32(v[c].y) * down);
     }
-    lsc0 = lsc * exp2_int(__shfl_sync(0xffffffffu, e, 8 * tig));
-    lsc1 = lsc * exp2_int(__shfl_sync(0xffffffffu, e, 8 * tig + 4));
+    lsc.x = unit * exp2_int(__shfl_sync(0xffffffffu, e, 8 * tig));
+    lsc.y = unit * exp2_int(__shfl_sync(0xffffffffu, e, 8 * tig + 4));
   }
 
   // Unscaled logits of a tile: z[0], z[1] token row gid, z[2], z[3] row gid + 8.
@@ -315,12 +324,13 @@ struct Fp4Worker {
       }
       x0 = warp_max_over_gid(x0);
       x1 = warp_max_over_gid(x1);
-      const float n0 = fmaxf(m0, x0 * lsc0), n1 = fmaxf(m1, x1 * lsc1);
-      const float c0 = fast_exp2(m0 - n0), c1 = fast_exp2(m1 - n1);   // 0 while m is -inf
-      m0 = n0;
-      m1 = n1;
-      t0 = (m0 + kF4Lag) / lsc0;   // lsc 0 (all logits 0): infinite
-      t1 = (m1 + kF4Lag) / lsc1;
+      const float n0 = fmaxf(-nr.x, x0), n1 = fmaxf(-nr.y, x1);
+      const float c0 = nr.x == INFINITY ? 0.f : fast_exp2((-nr.x - n0) * lsc.x);
+      const float c1 = nr.y == INFINITY ? 0.f : fast_exp2((-nr.y - n1) * lsc.y);
+      nr = make_float2(-n0, -n1);
+      // (never more than the lag, which would let P past 2^8; infinite where all logits are 0)
+      t0 = __fadd_rd(n0, kF4Lag * (1.f - 0x1p-20f) * rcp_approx(lsc.x));
+      t1 = __fadd_rd(n1, kF4Lag * (1.f - 0x1p-20f) * rcp_approx(lsc.y));
       l0 *= c0;
       l1 *= c1;
 #pragma unroll
@@ -333,9 +343,10 @@ struct Fp4Worker {
     }
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
-      // (one rounding; a masked -inf stays -inf unless lsc is 0, so it is asked for again)
-      float p[4] = {fast_exp2(fmaf(z[i][0], lsc0, -m0)), fast_exp2(fmaf(z[i][1], lsc1, -m1)),
-                    fast_exp2(fmaf(z[i][2], lsc0, -m0)), fast_exp2(fmaf(z[i][3], lsc1, -m1))};
+      // (a masked -inf stays -inf unless lsc is 0, so it is asked for again)
+      const float2 a = mul_f32x2(add_f32x2(make_float2(z[i][0], z[i][1]), nr), lsc);
+      const float2 b = mul_f32x2(add_f32x2(make_float2(z[i][2], z[i][3]), nr), lsc);
+      float p[4] = {fast_exp2(a.x), fast_exp2(a.y), fast_exp2(b.x), fast_exp2(b.y)};
       if (kMasked) {
         if (z[i][0] == -INFINITY) p[0] = p[1] = 0.f;
         if (z[i][2] == -INFINITY) p[2] = p[3] = 0.f;
@@ -358,9 +369,9 @@ struct Fp4Worker {
     }
     if (gid == 0) {
       float* ml = mml + (warp * kMaxGqa + 2 * tig) * 2;
-      ml[0] = m0;
+      ml[0] = m0();
       ml[1] = l0;
-      ml[2] = m1;
+      ml[2] = m1();
       ml[3] = l1;
     }
   }
@@ -377,7 +388,7 @@ struct Fp4Worker {
       if (h + 1 < g)
         __stcg(reinterpret_cast<float4*>(r0 + kHeadDim + 2 * mt), make_float4(o[mt][1], o[mt][3], o[mt + 1][1], o[mt + 1][3]));
     }
-    if (gid == 0) __stcg(reinterpret_cast<float4*>(rows + kMaxGqa * kHeadDim + 4 * tig), make_float4(m0, l0, m1, l1));
+    if (gid == 0) __stcg(reinterpret_cast<float4*>(rows + kMaxGqa * kHeadDim + 4 * tig), make_float4(m0(), l0, m1(), l1));
   }
 
   // The unit's output rows; h0: its first query head.
@@ -389,7 +400,7 @@ struct Fp4Worker {
       const int hh = 2 * tig + e;
       if (hh >= p.gqa) continue;
       const float zs = p.sinks ? __ldg(p.sinks + h0 + hh) * 1.4426950408889634f : -INFINITY;
-      const float M = e ? m1 : m0, den = e ? l1 : l0;
+      const float M = e ? m1() : m0(), den = e ? l1 : l0;
       const size_t at = ((size_t)s * p.num_heads + h0 + hh) * kHeadDim + 16 * gid;
       float r[16];
 #pragma unroll

@@ -109,6 +109,37 @@ def test_large_queries():
     b.check()
 
 
+@pytest.mark.parametrize("size", [0, 20, 24, 27, 28, 30, 40, 80, 110])
+@pytest.mark.parametrize("lens,bs", [([20, 5], 16), ([300], 128), ([5000], 16)])
+def test_far_logits(size, lens, bs):
+    """Logits of 2^size: where the largest is far in front its value comes out; a page named twice is weighted as once."""
+    b = Batch(lens, 8, 2, bs, seed=60)
+    b.tables[0, 1] = b.tables[0, 0] if lens[0] >= 2 * bs else b.tables[0, 1]
+    far = 0
+    for spread in (1.0, 2.0 ** size):
+        b.q = (torch.randn(len(lens), 8, 128, generator=gen(61)) * spread).to(torch.bfloat16)
+        b.scale = 2.0 ** size / spread if size < 40 else 128 ** -0.5
+        got = b.run().double().cpu()
+        assert torch.isfinite(got).all()
+        for i, n in enumerate(lens):
+            pos = torch.arange(n)
+            ids = b.tables[i, pos // bs].long()
+            k, v = (U.read4(b.cache, bs, kind, ids, pos % bs, s)[1] for kind, s in ((0, KS), (1, VS)))
+            for h in range(8):
+                z = k[:, h // 4] @ b.q[i, h].double() * b.scale
+                a = (k[:, h // 4].abs() @ b.q[i, h].double().abs()).max() * b.scale
+                top = z == z.max()
+                rest = z[~top].max()
+                if float(z.max() - rest) < 40 + float(a) * 2.0 ** -15:     # the rest: 2^-57 at most, wherever 128 sums in binary32 put it
+                    continue
+                far += 1
+                want = v[top, h // 4].mean(0)
+                # equal logits have equal weights; P, the output and the sums of few terms round
+                assert ((got[i, h] - want).abs() <= v[top, h // 4].abs().mean(0) * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -16)).all(), (i, h)
+    assert far >= (0 if size <= 20 else 8)
+    assert pda.query_device_status() == 0
+
+
 def test_wild_codes():
     """Codes and group scales over their whole range: exact products, logits far apart."""
     b = Batch([64, 130], 4, 2, 16, seed=12, wild=True, q_scale=0.02)
