@@ -299,10 +299,17 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     if (st != PDA_OK) return st;
     // Half as large chunks where large ones are too few for even runs: below four a CTA
     // (us with 4 / 2 tiles a warp, 32/8 heads: 16 x 1024 tokens 16.3 / 15.0, 32 x 1024
-    // 20.9 / 19.1, 64 x 1024 25.2 / 25.3, 128 x 1 to 2048 43.7 / 48.8).
+    // 20.9 / 19.1, 64 x 1024 25.2 / 25.3, 128 x 1 to 2048 43.7 / 48.8). But not where a
+    // large chunk holds a whole sequence, so that nothing is to be joined (64 x 50 tokens
+    // 9.2 / 11.0).
     if (most < 4ll * ctas) {
+      const int whole = per;
       tiles = 2;
       cut();
+      if (max_num_blocks_per_seq > per && max_num_blocks_per_seq <= whole) {
+        tiles = pda::kF4Tiles;
+        cut();
+      }
     }
     const double logit = (double)scale * (double)k_scale * 1.4426950408889634;
     pda::Fp4DecodeParams p = {};
@@ -336,8 +343,10 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     std::lock_guard<std::mutex> lk(g_ops_mu);   // the two kernels follow each other
     pda::pda_fp4_decode_kernel<<<grid, pda::kF4Threads, pda::kF4Smem, stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+    if (max_num_blocks_per_seq <= per) return PDA_OK;   // units of one chunk: no cut divides them
+    const long long rows = (long long)num_seqs * num_heads;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(pda::kF4JoinCtas);
+    lc.gridDim = dim3((unsigned)(rows < pda::kF4JoinCtas ? rows : pda::kF4JoinCtas));
     lc.blockDim = dim3(pda::kF4JoinThreads);
     lc.stream = stream;
     cudaLaunchAttribute attr[1];
