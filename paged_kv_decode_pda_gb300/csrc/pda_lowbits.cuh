@@ -302,6 +302,10 @@ __device__ __forceinline__ int slot_groups(int block, int slot, bool live, int l
   return n;
 }
 
+// Where a tile's key row r has its 16-byte chunk c: read or written by rows and by
+// columns without bank conflicts.
+__device__ __forceinline__ int key_at(int r, int c) { return 16 * (c ^ (r & 7)); }
+
 // Tiles of 16 tokens, a warp per kv head: the rows' codes pass through shared memory,
 // K to go out 16 bytes (a chunk of a row) at a time, V by groups of 16 slots, turned
 // in registers: 16-byte rows of whole groups, and what a group holds of the tile
@@ -355,7 +359,7 @@ __global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_
         const int r = 8 * (part & 1) + 2 * i + half;
         const int2 at = rows[r];
         const RowScale scale = slot_scale(w[i], p.min_scale);
-        *reinterpret_cast<uint2*>(&(is_v ? vt : kt)[r][8 * l]) = e4m3_codes8(w[i], scale);
+        *reinterpret_cast<uint2*>(is_v ? &vt[r][8 * l] : &kt[r][key_at(r, l >> 1) + 8 * (l & 1)]) = e4m3_codes8(w[i], scale);
         if (l == 0 && at.x >= 0) (is_v ? p.v_scales : p.k_scales)[((size_t)at.x * Hk + h) * bs + at.y] = scale.scale;
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[i][j] = next[i][j];
@@ -369,7 +373,7 @@ __global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_
       const int2 at = rows[r];
       if (at.x >= 0)
         *reinterpret_cast<uint4*>(p.k_cache + ((size_t)at.x * Hk + h) * page + (c * bs + at.y) * 16) =
-            *reinterpret_cast<const uint4*>(&kt[r][16 * c]);
+            *reinterpret_cast<const uint4*>(&kt[r][key_at(r, c)]);
     }
     for (int k = 0; k < num_groups; ++k) {
       const SlotGroup gr = groups[k];
@@ -531,6 +535,7 @@ struct GatherParams {
   long long num_blocks;
   float k_scale, v_scale;
   int v_shuffled;
+  int v_wide;                    // a group's V rows lie side by side, on the 32-byte grid
   int rows_per_cta;              // 4-bit reader
   int heads_per_cta;             // e4m3 reader
 };
@@ -625,8 +630,18 @@ __global__ void __launch_bounds__(kLowbitsThreads) pda_gather_fp4_kernel(const G
 
 // e4m3: 16 rows a CTA, a warp per kv head. Both tensors pass through shared memory
 // as [row][128] bytes: K 16 bytes (a chunk of a row) at a time, V by groups of 16
-// slots turned in registers; from there a half warp writes a row.
+// slots turned in registers; from there a half warp writes a row. What bounds it
+// beside the bytes are L1's passes over scattered 16-byte loads: 32 contexts of 1 to
+// 4000 tokens, 16-token blocks, 71.6 us with V's 16 bytes and K's rows a lane eighth
+// at a time, 66.0 (5.9 TB/s) with V's 32 bytes at a time and K's rows side by side
+// (64 registers and 24 bytes spilled: 69).
 constexpr int kGatherThreads = 128;
+// 32 bytes on their grid in one load.
+__device__ __forceinline__ void ldg_32(const uint8_t* src, uint4& a, uint4& b) {
+  asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+      : "l"(src));
+}
 __global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const GatherParams p) {
   __shared__ int2 rows[kGatherRows];
   __shared__ SlotGroup groups[kGatherRows];
@@ -654,10 +669,10 @@ __global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const Gather
     uint4 kq[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int2 at = rows[(lane >> 3) + 4 * i];
+      // consecutive lanes: consecutive rows of one chunk
       kq[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (at.x >= 0)
-        kq[i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + ((size_t)at.x * Hk + h) * page + ((lane & 7) * bs + at.y) * 16));
+      if (own.x >= 0)
+        kq[i] = __ldg(reinterpret_cast<const uint4*>(p.k_cache + ((size_t)own.x * Hk + h) * page + ((half + 2 * i) * bs + own.y) * 16));
     }
     for (int k = 0; k < num_groups; ++k) {   // (the next group's loads ahead: 104 registers, and 84 us for 72)
       const SlotGroup gr = groups[k];
@@ -665,8 +680,13 @@ __global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const Gather
       src += p.v_shuffled ? (gr.part * 128 + 4 * lane) * 16 : 4 * lane * bs + gr.part * 16;
       const int step = p.v_shuffled ? 16 : bs;
       uint4 v[4];
+      if (p.v_wide) {   // the four rows side by side
+        ldg_32(src, v[0], v[1]);
+        ldg_32(src + 32, v[2], v[3]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step));
+        for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(src + i * step));
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t in[4] = {q == 0 ? v[0].x : q == 1 ? v[0].y : q == 2 ? v[0].z : v[0].w,
@@ -683,7 +703,7 @@ __global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const Gather
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(&kt[(lane >> 3) + 4 * i][16 * (lane & 7)]) = kq[i];
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(&kt[l][key_at(l, half + 2 * i)]) = kq[i];
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kGatherRows; ++i) {
@@ -692,7 +712,7 @@ __global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const Gather
       const bool is_v = i >= kGatherRows / 2;
       const int st = rows[r].x;
       const float f = __shfl_sync(0xffffffffu, scale, r + (is_v ? 16 : 0));
-      const uint2 c = *reinterpret_cast<const uint2*>(&(is_v ? vt : kt)[r][8 * l]);
+      const uint2 c = *reinterpret_cast<const uint2*>(is_v ? &vt[r][8 * l] : &kt[r][key_at(r, l >> 1) + 8 * (l & 1)]);
       if (st == kRowNone) continue;
       uint32_t y[4];
 #pragma unroll

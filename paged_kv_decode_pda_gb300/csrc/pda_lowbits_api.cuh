@@ -77,6 +77,7 @@ pda_status gather_e4m3(pda::GatherParams& p, const void* k_cache, const void* v_
   if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return PDA_ERR_INVALID_ARG;
   p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.v_wide = (p.v_shuffled || p.block_size == 16) && !misaligned(v_cache, 32);
   const int tiles = (p.num_tokens + pda::kGatherRows - 1) / pda::kGatherRows;
   // Heads of a CTA of four warps: all, unless that leaves fewer than 4 CTAs an SM.
   int per = p.num_kv_heads;
