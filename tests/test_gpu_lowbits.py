@@ -134,6 +134,57 @@ def test_write_fp4(T, Hk, bs, kind, layout, ks, vs):
     assert pda.query_device_status() == 0
 
 
+def every_quotient(width, binades):
+    """Rows [., 128] bf16: each group of `width` dims holds a largest value (all 128 significands in turn) and others of every
+    significand in the `binades` binades below it, of both signs."""
+    sig = torch.arange(128, dtype=torch.float64) / 128 + 1
+    x = (sig[None] * 2.0 ** -torch.arange(1, binades + 1, dtype=torch.float64)[:, None]).flatten()
+    x = torch.cat([sig, x])                                     # of the largest's own binade too, those that are not larger
+    x = x * (1 - 2 * (torch.arange(len(x)) % 3 == 0).double())
+    rows = []
+    for a in sig:
+        y = x[x.abs() <= a]
+        y = torch.cat([y, y.new_zeros(-len(y) % (width - 1))]).view(-1, width - 1)
+        rows.append(torch.cat([a.expand(len(y), 1), y], 1))
+    rows = torch.cat(rows).flatten()
+    return torch.cat([rows, rows.new_zeros(-len(rows) % 128)]).view(-1, 128).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("heads", [1, 2])
+def test_every_quotient_slot_scales(heads):
+    """Every pair of significands (a row's largest, another value) down to codes of zero, both kernels: each code the nearest."""
+    x = every_quotient(128, 20)[:, None].expand(-1, heads, -1).contiguous()
+    T, bs = x.shape[0], 16
+    assert (T * heads > 4096) == (heads == 2)
+    NB = -(-T // bs)
+    dev = [torch.zeros(NB, heads, 8, bs, 16, dtype=torch.uint8, device=DEV), torch.zeros(NB, heads, 128, bs, dtype=torch.uint8, device=DEV),
+           torch.zeros(NB, heads, bs, device=DEV), torch.zeros(NB, heads, bs, device=DEV)]
+    key, value = x.to(DEV), (x * -2.0 ** 30).to(DEV)
+    pda.reshape_and_cache_slot_scales(key, value, *dev, torch.arange(T, device=DEV))
+    kc, vc, ks, vs = (t.cpu() for t in dev)
+    t = torch.arange(T)
+    for cache, table, rows in ((kc[t // bs, :, :, t % bs].reshape(T, heads, 128), ks, key), (vc[t // bs, :, :, t % bs], vs, value)):
+        codes, scales = U.quantize_rows8(rows.cpu(), MIN)
+        assert torch.equal(cache, codes) and torch.equal(table[t // bs, :, t % bs], scales)
+
+
+@pytest.mark.parametrize("g", [2.0 ** -8, 0.0043, 7.0 / 1024, 1.0 / 3])
+def test_every_quotient_fp4(g):
+    """Every pair of significands (a group's largest, another value) down to codes of zero; groups of several magnitudes."""
+    x = every_quotient(16, 5)
+    x = torch.cat([x * f for f in (2.0 ** -9, 1.0, 2.0 ** 3)])[:, None].contiguous()
+    T, bs = x.shape[0], 16
+    NB = -(-T // bs)
+    want = torch.zeros(pda.fp4_cache_shape(NB, 1, bs), dtype=torch.uint8)
+    got = want.to(DEV)
+    value = -x.flip(0)
+    slots = torch.arange(T)
+    pda.reshape_and_cache_fp4(x.to(DEV), value.to(DEV), got, slots.to(DEV), g, g)
+    for kind, rows in ((0, x), (1, value)):
+        U.write4(want, bs, kind, slots, *U.quantize_rows4(rows, g))
+    assert torch.equal(got.cpu(), want)
+
+
 # past 4096 rows (tiles of 16 tokens), and past 9728 (four heads of a token to a warp)
 MANY = [(600, 8, 16, "blocks", "plain"), (1100, 9, 32, "run", "packed"), (530, 9, 64, "scattered", "odd"),
         (2100, 2, 128, "blocks", "heads_first"), (4105, 1, 48, "run", "plain"), (1300, 10, 16, "scattered", "odd"),
