@@ -453,6 +453,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4CtasPerSm) pda_fp4_decode_kerne
     *abort_flag = 0;
     fence_barrier_init();
   }
+  grid_dependency_wait();   // nothing above reads what a kernel in front may write
 
   // ---- the chunks of all sequences: thread i counts sequences [i * each, ...)
   const int each = (p.num_seqs + kF4Threads - 1) / kF4Threads;

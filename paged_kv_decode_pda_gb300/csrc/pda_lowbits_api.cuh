@@ -342,19 +342,24 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     p.out_scale = output_scale;
     const unsigned grid = (unsigned)(most < ctas ? most : ctas);
     std::lock_guard<std::mutex> lk(g_ops_mu);   // the two kernels follow each other
-    pda::pda_fp4_decode_kernel<<<grid, pda::kF4Threads, pda::kF4Smem, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-    if (max_num_blocks_per_seq <= per) return PDA_OK;   // units of one chunk: no cut divides them
-    const long long rows = (long long)num_seqs * num_heads;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3((unsigned)(rows < pda::kF4JoinCtas ? rows : pda::kF4JoinCtas));
-    lc.blockDim = dim3(pda::kF4JoinThreads);
-    lc.stream = stream;
+    // Both are programmatic launches: the first sets up its CTAs while the kernel in
+    // front of it ends.
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(pda::kF4Threads);
+    lc.dynamicSmemBytes = pda::kF4Smem;
+    lc.stream = stream;
     lc.attrs = attr;
     lc.numAttrs = 1;
+    if (cudaLaunchKernelEx(&lc, pda::pda_fp4_decode_kernel, p) != cudaSuccess) return PDA_ERR_CUDA;
+    if (max_num_blocks_per_seq <= per) return PDA_OK;   // units of one chunk: no cut divides them
+    const long long rows = (long long)num_seqs * num_heads;
+    lc.gridDim = dim3((unsigned)(rows < pda::kF4JoinCtas ? rows : pda::kF4JoinCtas));
+    lc.blockDim = dim3(pda::kF4JoinThreads);
+    lc.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&lc, pda::pda_fp4_join_kernel, p) == cudaSuccess) return PDA_OK;
     cudaMemsetAsync(ws, 0, kFp4HeadBytes, stream);   // the lists that the join would have emptied
     return PDA_ERR_CUDA;
