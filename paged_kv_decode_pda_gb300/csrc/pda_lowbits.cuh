@@ -229,6 +229,7 @@ __device__ __forceinline__ RowScale slot_scale(const uint32_t (&w)[4], float min
 // One warp per (token, kv head): lanes 0-15 the key row, 16-31 the value row.
 template <bool kVec>
 __global__ void __launch_bounds__(kLowbitsThreads) pda_write_slot_scales_kernel(const LowbitsWriteParams p) {
+  grid_dependency_wait();
   const long long item = (long long)blockIdx.x * (kLowbitsThreads / 32) + (threadIdx.x >> 5);
   if (item >= (long long)p.num_tokens * p.num_kv_heads) return;   // whole warps
   const int lane = threadIdx.x & 31, l = lane & 15;
@@ -313,6 +314,7 @@ __device__ __forceinline__ int key_at(int r, int c) { return 16 * (c ^ (r & 7));
 constexpr int kWriteTileThreads = 128;
 template <bool kVec>
 __global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_kernel(const LowbitsWriteParams p) {
+  grid_dependency_wait();
   __shared__ int2 rows[16];
   __shared__ SlotGroup groups[16];
   __shared__ int num_groups;
@@ -487,6 +489,7 @@ __device__ __forceinline__ uint32_t e2m1_codes8(uint32_t (&w)[4], float g, float
 // the key rows, 16-31 the value rows: 16 bytes a lane in, 4 bytes of codes out.
 template <bool kVec, int kItems>
 __global__ void __launch_bounds__(kLowbitsThreads) pda_write_fp4_kernel(const LowbitsWriteParams p) {
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, l = lane & 15;
   const bool is_v = lane >= 16;
   const long long t = (long long)blockIdx.x * (kLowbitsThreads / 32) + (threadIdx.x >> 5);
@@ -576,6 +579,7 @@ constexpr int kGatherMaxRows4 = 32;    // 4-bit reader: rows of a CTA at most
 // of codes and one scale byte a lane in, 16 bytes out. The warps of a CTA take rows
 // each, or share a row's heads where a CTA has fewer rows than warps.
 __global__ void __launch_bounds__(kLowbitsThreads) pda_gather_fp4_kernel(const GatherParams p) {
+  grid_dependency_wait();
   __shared__ int2 rows[kGatherMaxRows4];
   const int r0 = blockIdx.x * p.rows_per_cta;
   const int n = min(p.rows_per_cta, p.num_tokens - r0);
@@ -643,6 +647,7 @@ __device__ __forceinline__ void ldg_32(const uint8_t* src, uint4& a, uint4& b) {
       : "l"(src));
 }
 __global__ void __launch_bounds__(kGatherThreads) pda_gather_kernel(const GatherParams p) {
+  grid_dependency_wait();
   __shared__ int2 rows[kGatherRows];
   __shared__ SlotGroup groups[kGatherRows];
   __shared__ int num_groups;

@@ -12,6 +12,28 @@ constexpr long long kSlotScalesMaxRows = 4096;
 // is a normal number whose last bit binary32 holds, so that its sign is exact.
 bool scale_in_range(float x) { return x >= 0x1p-100f && x <= 0x1p100f; }   // false for NaN
 
+// A programmatic launch: the kernel sets up its CTAs while the one in front of it ends,
+// and waits for that one's results (grid_dependency_wait) before it touches memory. us
+// without / with it, calls in turn on one stream: slot-scale write of 8192 tokens 18.5 /
+// 15.9, 4-bit write and read of 16384 41.0 / 36.3, 4-bit read of 64 contexts 105.6 / 103.0,
+// decode of 16 x 1024 18.2 / 15.7. (Writers and readers that also let the next kernel's
+// CTAs in early, with grid_dependents_launch: 17.6, 36.6, 103.3, and a write of 256
+// tokens in a graph 6.7 where this takes 4.7.)
+template <typename P>
+bool launch_behind(void (*kernel)(P), dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = stream;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess;
+}
+
 pda_status write_checks(const pda_token_rows* key, const pda_token_rows* value, int num_tokens, int num_kv_heads,
                         int head_size, int block_size, long long num_blocks) {
   if (!key || !value || num_tokens < 0 || num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks < 0)
@@ -84,8 +106,7 @@ pda_status gather_e4m3(pda::GatherParams& p, const void* k_cache, const void* v_
   while (per > 4 && (long long)tiles * ((p.num_kv_heads + per - 1) / per) < 4 * 152) per = (per + 1) / 2;
   p.heads_per_cta = per;
   const dim3 grid((unsigned)tiles, (unsigned)((p.num_kv_heads + per - 1) / per));
-  pda::pda_gather_kernel<<<grid, pda::kGatherThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  return launch_behind(pda::pda_gather_kernel, grid, pda::kGatherThreads, 0, stream, p) ? PDA_OK : PDA_ERR_CUDA;
 }
 
 // Resident CTAs of the 4-bit decode kernel on device `dev`; opts it in to its
@@ -148,17 +169,18 @@ pda_status pda_reshape_and_cache_slot_scales(const pda_token_rows* key, const pd
   // whole blocks 6.3 / 7.2, scattered 5.5 / 15.7; 512 9.8 / 7.3, 8.2 / 16.2; 1024 16.3 /
   // 7.2, 12.5 / 18.6; 8192 82.7 / 16.2, 75.5 / 74.2).
   const long long items = (long long)num_tokens * num_kv_heads;
+  bool done;
   if (items <= kSlotScalesMaxRows) {
-    const unsigned blocks = (unsigned)((items + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32));
-    if (vec) pda::pda_write_slot_scales_kernel<true><<<blocks, pda::kLowbitsThreads, 0, stream>>>(p);
-    else pda::pda_write_slot_scales_kernel<false><<<blocks, pda::kLowbitsThreads, 0, stream>>>(p);
+    const dim3 grid((unsigned)((items + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32)));
+    done = launch_behind(vec ? pda::pda_write_slot_scales_kernel<true> : pda::pda_write_slot_scales_kernel<false>, grid,
+                         pda::kLowbitsThreads, 0, stream, p);
   } else {
     const int warps = pda::kWriteTileThreads / 32;
     const dim3 grid((unsigned)((num_tokens + 15) / 16), (unsigned)((num_kv_heads + warps - 1) / warps));
-    if (vec) pda::pda_write_slot_scales_tile_kernel<true><<<grid, pda::kWriteTileThreads, 0, stream>>>(p);
-    else pda::pda_write_slot_scales_tile_kernel<false><<<grid, pda::kWriteTileThreads, 0, stream>>>(p);
+    done = launch_behind(vec ? pda::pda_write_slot_scales_tile_kernel<true> : pda::pda_write_slot_scales_tile_kernel<false>,
+                         grid, pda::kWriteTileThreads, 0, stream, p);
   }
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  return done ? PDA_OK : PDA_ERR_CUDA;
 }
 
 pda_status pda_reshape_and_cache_fp4(const pda_token_rows* key, const pda_token_rows* value, void* kv_cache,
@@ -187,11 +209,9 @@ pda_status pda_reshape_and_cache_fp4(const pda_token_rows* key, const pda_token_
   const int per = four ? 4 : 1;
   const dim3 grid((unsigned)((num_tokens + pda::kLowbitsThreads / 32 - 1) / (pda::kLowbitsThreads / 32)),
                   (unsigned)((num_kv_heads + per - 1) / per));
-  if (four && vec) pda::pda_write_fp4_kernel<true, 4><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
-  else if (four) pda::pda_write_fp4_kernel<false, 4><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
-  else if (vec) pda::pda_write_fp4_kernel<true, 1><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
-  else pda::pda_write_fp4_kernel<false, 1><<<grid, pda::kLowbitsThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  const auto kernel = four ? (vec ? pda::pda_write_fp4_kernel<true, 4> : pda::pda_write_fp4_kernel<false, 4>)
+                           : (vec ? pda::pda_write_fp4_kernel<true, 1> : pda::pda_write_fp4_kernel<false, 1>);
+  return launch_behind(kernel, grid, pda::kLowbitsThreads, 0, stream, p) ? PDA_OK : PDA_ERR_CUDA;
 }
 
 pda_status pda_gather_cache(void* k_out, void* v_out, const void* k_cache, const void* v_cache,
@@ -254,8 +274,8 @@ pda_status pda_gather_cache_fp4(void* k_out, void* v_out, const void* kv_cache, 
   int rows = pda::kGatherMaxRows4;
   while (rows > 1 && (num_tokens + rows - 1) / rows < 8 * 152) rows /= 2;
   p.rows_per_cta = rows;
-  pda::pda_gather_fp4_kernel<<<(unsigned)((num_tokens + rows - 1) / rows), pda::kLowbitsThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  const dim3 grid((unsigned)((num_tokens + rows - 1) / rows));
+  return launch_behind(pda::pda_gather_fp4_kernel, grid, pda::kLowbitsThreads, 0, stream, p) ? PDA_OK : PDA_ERR_CUDA;
 }
 
 pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const int32_t* block_tables,
@@ -342,25 +362,11 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     p.out_scale = output_scale;
     const unsigned grid = (unsigned)(most < ctas ? most : ctas);
     std::lock_guard<std::mutex> lk(g_ops_mu);   // the two kernels follow each other
-    // Both are programmatic launches: the first sets up its CTAs while the kernel in
-    // front of it ends.
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(grid);
-    lc.blockDim = dim3(pda::kF4Threads);
-    lc.dynamicSmemBytes = pda::kF4Smem;
-    lc.stream = stream;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    if (cudaLaunchKernelEx(&lc, pda::pda_fp4_decode_kernel, p) != cudaSuccess) return PDA_ERR_CUDA;
+    if (!launch_behind(pda::pda_fp4_decode_kernel, dim3(grid), pda::kF4Threads, pda::kF4Smem, stream, p)) return PDA_ERR_CUDA;
     if (max_num_blocks_per_seq <= per) return PDA_OK;   // units of one chunk: no cut divides them
     const long long rows = (long long)num_seqs * num_heads;
-    lc.gridDim = dim3((unsigned)(rows < pda::kF4JoinCtas ? rows : pda::kF4JoinCtas));
-    lc.blockDim = dim3(pda::kF4JoinThreads);
-    lc.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&lc, pda::pda_fp4_join_kernel, p) == cudaSuccess) return PDA_OK;
+    const dim3 join((unsigned)(rows < pda::kF4JoinCtas ? rows : pda::kF4JoinCtas));
+    if (launch_behind(pda::pda_fp4_join_kernel, join, pda::kF4JoinThreads, 0, stream, p)) return PDA_OK;
     cudaMemsetAsync(ws, 0, kFp4HeadBytes, stream);   // the lists that the join would have emptied
     return PDA_ERR_CUDA;
   });
