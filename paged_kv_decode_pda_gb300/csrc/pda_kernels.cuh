@@ -2058,14 +2058,15 @@ __global__ void __launch_bounds__(kHeadDim) pda_tail_merge_kernel(const TailMerg
   const int row = blockIdx.x * kMergeRowsPerBlock + (threadIdx.x >> 5);
   const int nsplit = p.m.nsplit;
   if (row >= p.tail_units * p.gqa) {
-    if (nsplit > 1) grid_dependency_wait();
+    grid_dependency_wait();
     return;
   }
   const int j = row / p.gqa;
   const int hh = row % p.gqa;
   const int4 e = __ldcg(p.tail_info + j);
-  if (e.z <= 1 && nsplit == 1) return;
-  grid_dependency_wait();  // the decode kernel's pieces are stored and visible
+  // The decode kernel's pieces are stored and visible. Every warp waits, also one without
+  // pieces: a programmatic launch behind this kernel waits for this kernel alone.
+  grid_dependency_wait();
   if (e.z <= 1) return;
   const int s = e.x / (p.num_kv_heads * nsplit);
   const int kvh = (e.x / nsplit) % p.num_kv_heads;

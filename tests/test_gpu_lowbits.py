@@ -470,3 +470,36 @@ def test_refusals_on_the_gpu():
         pda.reshape_and_cache_slot_scales(k, v, kc, vc, ks, ks, slots, min_scale=0.0)
     assert e.value.status == pda.PDA_ERR_INVALID_ARG
     assert not cache.any() and not kc.any()
+
+
+def test_writes_behind_a_decode():
+    """A write right behind a decode that still reads the same slots: the decode sees what was there before. Batches whose tail
+    kernel has nothing to join, beside one long sequence that keeps the decode busy."""
+    S, H, Hk, bs, MB = 256, 8, 8, 16, 256
+    g = gen(70)
+    NB = MB + S
+    tables = torch.arange(MB, dtype=torch.int32).repeat(S, 1)
+    tables[1:, 0] = torch.arange(MB, NB - 1, dtype=torch.int32)
+    lens = torch.full((S,), 5, dtype=torch.int32)
+    lens[0] = MB * bs
+    assert pda.plan_launches(S, H, Hk, MB, bs) >= 2
+    kc = torch.randint(0, 0x70, (NB, Hk, 8, bs, 16), generator=g, dtype=torch.uint8)
+    vc = torch.randint(0, 0x70, (NB, Hk, 128, bs), generator=g, dtype=torch.uint8)
+    q = torch.randn(S, H, 128, generator=g).to(torch.bfloat16).to(DEV)
+    tables, lens = tables.to(DEV), lens.to(DEV)
+    T = MB * bs
+    k, v = (torch.randn(T, Hk, 128, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    slots = torch.arange(T, device=DEV)
+    first = [t.to(DEV) for t in (kc, vc)]
+    want = pda.decode(q, *first, tables, lens, 0.01, 0.01, 0.01)
+    torch.cuda.synchronize()
+    for i in range(20):
+        caches = [t.clone() for t in first]
+        scales = [torch.ones(NB, Hk, bs, device=DEV) for _ in range(2)]
+        out = torch.empty_like(want)
+        torch.cuda.synchronize()
+        pda.decode(q, *caches, tables, lens, 0.01, 0.01, 0.01, out=out)
+        pda.reshape_and_cache_slot_scales(k, v, *caches, *scales, slots)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i
+    assert pda.query_device_status() == 0
