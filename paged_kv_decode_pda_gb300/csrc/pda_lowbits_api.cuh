@@ -13,7 +13,8 @@ constexpr long long kSlotScalesMaxRows = 4096;
 bool scale_in_range(float x) { return x >= 0x1p-100f && x <= 0x1p100f; }   // false for NaN
 
 // A programmatic launch: the kernel sets up its CTAs while the one in front of it ends,
-// and waits for that one's results (grid_dependency_wait) before it touches memory. us
+// and waits for that one's results (grid_dependency_wait) before it touches memory. That
+// one has waited for what is in front of it, as every programmatic kernel here does. us
 // without / with it, calls in turn on one stream: slot-scale write of 8192 tokens 18.5 /
 // 15.9, 4-bit write and read of 16384 41.0 / 36.3, 4-bit read of 64 contexts 105.6 / 103.0,
 // decode of 16 x 1024 18.2 / 15.7. (Writers and readers that also let the next kernel's
