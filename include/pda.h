@@ -613,6 +613,12 @@ pda_status pda_reserve_pages(long long num_blocks, int num_rows, int max_request
  * Caches in fewer bits: writers that find the scales of what they write,
  * readers that give a cache's values back, and attention over 4 bits.
  *
+ * The kernels of these calls are programmatic launches: each waits, before it
+ * touches memory, for the kernel in front of it on the stream. A caller's own
+ * programmatic kernel in front must itself have waited for its predecessor
+ * (cudaGridDependencySynchronize) if these calls are to be ordered behind that
+ * one too; ordinary launches, copies and events need no care.
+ *
  * pda_token_rows -- keys or values of new tokens: bf16, the row of (token t, kv
  * head h) at base + t * token_stride + h * head_stride (strides in elements, the
  * row's 128 dims contiguous). Rows on the 16-byte grid are read in wide accesses,

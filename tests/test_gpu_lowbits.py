@@ -503,3 +503,60 @@ def test_writes_behind_a_decode():
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_of_another_stream(captured):
+    """Tokens that another stream makes, late, and an event tells of: written, read back and attended to in this one."""
+    T, Hk, H, bs = 64, 2, 8, 16
+    g = gen(80)
+    src = [torch.randn(T, Hk, 128, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2)]
+    k, v = (torch.zeros_like(t) for t in src)
+    busy = torch.randn(2048, 2048, device=DEV)
+    work = torch.empty_like(busy)
+    cache = torch.zeros(pda.fp4_cache_shape(4, Hk, bs), dtype=torch.uint8, device=DEV)
+    tables = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+    starts, lens = torch.tensor([0, T], dtype=torch.int32, device=DEV), torch.tensor([T], dtype=torch.int32, device=DEV)
+    slots = torch.arange(T, device=DEV)
+    q = torch.randn(1, H, 128, generator=g).to(torch.bfloat16).to(DEV)
+    kb, vb = (torch.zeros(T, Hk, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = torch.zeros_like(q)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        kb.zero_()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                torch.mm(busy, busy, out=work)
+            k.copy_(src[0])
+            v.copy_(src[1])
+        out.zero_()
+        main.wait_stream(side)
+        pda.reshape_and_cache_fp4(k, v, cache, slots, 0.0043, 0.0043)
+        pda.gather_cache_fp4(cache, tables, starts, T, 0.0043, 0.0043, k_out=kb, v_out=vb)
+        pda.decode_fp4(q, cache, tables, lens, 128 ** -0.5, 0.0043, 0.0043, out=out)
+
+    with torch.cuda.stream(main):
+        pda.reserve_fp4(main)
+        step()
+        main.synchronize()
+        want = [t.clone() for t in (cache, kb, vb, out)]
+        assert out.abs().sum() > 0
+        graph = None
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=main):
+                step()
+        for _ in range(10):
+            for t in (k, v, cache, kb, vb, out):
+                t.zero_()
+            graph.replay() if captured else step()
+            main.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((cache, kb, vb, out), want))
+    codes, _ = U.quantize_rows4(src[0].cpu(), 0.0043)
+    table, _, _ = U.Record(bs).tables()
+    t = torch.arange(T)
+    held = cache.cpu()[t // bs][:, :, :].gather(2, table[0][t % bs][:, None].expand(-1, Hk, -1)) >> (torch.arange(128) % 2 * 4) & 15
+    assert torch.equal(held.to(torch.uint8), codes)
+    assert pda.query_device_status() == 0
