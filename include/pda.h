@@ -731,9 +731,9 @@ pda_status pda_gather_cache_fp4(void* k_out, void* v_out, const void* kv_cache, 
  *   num_blocks  > 0: ids outside [0, num_blocks) set bit 64 of the device status
  *               word and read block 0 (that sequence's output is undefined)
  *   window      > 0: the last `window` tokens only; 0: all
- * The probabilities enter the second product as one f16 each (at most 2^-11 of
- * themselves off; those below 2^-24 of the running maximum may vanish); the
- * normaliser sums them unrounded. A NaN among the tokens that count gives
+ * The probabilities enter the second product as one f16 each, at most 2^-11 of
+ * themselves off, or 2^-32 of the row's largest where that is more (those below it
+ * may vanish); the normaliser sums them unrounded. A NaN among the tokens that count gives
  * undefined output in the sequence's heads.
  *
  * Any mix of lengths loads the GPU evenly: the tokens of all sequences and kv

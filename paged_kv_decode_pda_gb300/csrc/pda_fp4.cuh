@@ -35,8 +35,12 @@
 // meanwhile, so that a tile (16 MMAs, 64 conversions, 64 products, 60 others) takes 84
 // with 12 or with 16 warps, where HBM would bring one every 91; 256 x 4096 tokens take
 // 192 us without any copies and 201 with them.
-// Q enters as in pda_decode (shifted by a power of two into f16), P as one f16,
-// off by at most 2^-11 of itself; the normaliser sums P unrounded in fp32.
+// Q enters as in pda_decode (shifted by a power of two into f16), P as one f16, held
+// 2^7 times as large (up to 2^15, with the lag below): off by at most 2^-11 of itself
+// down to 2^-21 of the running maximum, by 2^-32 of that below (held as it is, by 2^-25:
+// the weights behind one far token, 2^-24 of it each, were off by up to half of
+// themselves). The normaliser sums P unrounded in fp32, in the same units, so that they
+// cancel but for the sinks.
 //
 // The contraction's order is free, so each lane takes what lies side by side:
 // of a K row 16 bytes (32 dims), of four V rows one 8-byte block of 16 dims each,
@@ -44,8 +48,8 @@
 // fp4_row_token(r) and V's k slots the same tokens, chosen so that both kinds of
 // loads spread over all banks.
 //
-// The running maximum is let fall up to 8 (log2) behind: P stays below 2^8, well
-// inside f16, and nearly every tile passes with one vote in place of a maximum
+// The running maximum is let fall up to 8 (log2) behind: P stays below 2^8, 2^15 as it
+// is held, inside f16, and nearly every tile passes with one vote in place of a maximum
 // over the lanes and a rescale. The reference is an unscaled logit, taken off the
 // others before the scale, so that the weight of the reference itself is exactly 1
 // at any size (a scaled one leaves the rounding of a product as a power of two:
@@ -67,6 +71,8 @@ constexpr uint32_t kF4StageBytes = kF4ChunkTokens * kFp4TokenBytes;
 constexpr int kF4MergeStride = kHeadDim + 4;
 static_assert(kF4Warps * kMaxGqa * (kF4MergeStride + 2) * 4 <= kF4StageBytes, "merge rows fit a stage");
 constexpr float kF4Lag = 8.f;                                  // the running reference's lag behind the maximum, log2
+constexpr float kF4Shift = 7.f;                                // P and its sums are held in units of 2^-7
+static_assert(kF4Lag + kF4Shift < 16.f, "f16 holds P");
 constexpr int kF4MaxCtas = 512;
 constexpr int kF4RowFloats = kMaxGqa * (kHeadDim + 2);         // a piece: O rows, then (m, l) pairs
 
@@ -177,7 +183,7 @@ struct Fp4Worker {
   uint32_t qf[kChunks][2];
   float2 lsc;               // log2 units of an unscaled logit, >= 0
   float2 nr;                // minus the running reference: an unscaled logit, at most the lag below the maximum
-  float l0, l1;             // sums
+  float l0, l1;             // sums, in units of 2^-kF4Shift, as o
   float t0, t1;             // unscaled logits past which the reference moves
   float o[kChunks][4];      // dims 16 gid + 2 mt (0, 1) and 16 gid + 2 mt + 1 (2, 3); heads 2 tig, 2 tig + 1
 
@@ -328,7 +334,7 @@ struct Fp4Worker {
       const float c0 = nr.x == INFINITY ? 0.f : fast_exp2((-nr.x - n0) * lsc.x);
       const float c1 = nr.y == INFINITY ? 0.f : fast_exp2((-nr.y - n1) * lsc.y);
       nr = make_float2(-n0, -n1);
-      // (never more than the lag, which would let P past 2^8; infinite where all logits are 0)
+      // (never more than the lag, which bounds P; infinite where all logits are 0)
       t0 = __fadd_rd(n0, kF4Lag * (1.f - 0x1p-20f) * rcp_approx(lsc.x));
       t1 = __fadd_rd(n1, kF4Lag * (1.f - 0x1p-20f) * rcp_approx(lsc.y));
       l0 *= c0;
@@ -344,8 +350,9 @@ struct Fp4Worker {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       // (a masked -inf stays -inf unless lsc is 0, so it is asked for again)
-      const float2 a = mul_f32x2(add_f32x2(make_float2(z[i][0], z[i][1]), nr), lsc);
-      const float2 b = mul_f32x2(add_f32x2(make_float2(z[i][2], z[i][3]), nr), lsc);
+      const float2 up = make_float2(kF4Shift, kF4Shift);
+      const float2 a = fma_f32x2(add_f32x2(make_float2(z[i][0], z[i][1]), nr), lsc, up);
+      const float2 b = fma_f32x2(add_f32x2(make_float2(z[i][2], z[i][3]), nr), lsc, up);
       float p[4] = {fast_exp2(a.x), fast_exp2(a.y), fast_exp2(b.x), fast_exp2(b.y)};
       if (kMasked) {
         if (z[i][0] == -INFINITY) p[0] = p[1] = 0.f;
@@ -399,7 +406,7 @@ struct Fp4Worker {
     for (int e = 0; e < 2; ++e) {
       const int hh = 2 * tig + e;
       if (hh >= p.gqa) continue;
-      const float zs = p.sinks ? __ldg(p.sinks + h0 + hh) * 1.4426950408889634f : -INFINITY;
+      const float zs = p.sinks ? __ldg(p.sinks + h0 + hh) * 1.4426950408889634f + kF4Shift : -INFINITY;
       const float M = e ? m1() : m0(), den = e ? l1 : l0;
       const size_t at = ((size_t)s * p.num_heads + h0 + hh) * kHeadDim + 16 * gid;
       float r[16];
@@ -708,7 +715,7 @@ __global__ void __launch_bounds__(kF4Threads, kF4CtasPerSm) pda_fp4_decode_kerne
       }
       if (hd.pieces == 1) {
         store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, hd.s, (hd.kvh + kh) * g + hh, lane,
-                     hd.hi > hd.lo, M, den, acc);
+                     hd.hi > hd.lo, M, den, acc, kF4Shift);
       } else {
         float* to = rows + kh * kF4RowFloats;
         __stcg(reinterpret_cast<float4*>(to + hh * kHeadDim) + lane, acc);
@@ -801,7 +808,7 @@ __global__ void __launch_bounds__(kF4JoinThreads, 5) pda_fp4_join_kernel(const F
     float4 acc;
     fp4_add_pieces(p.pieces, c.z, 0, 1, min(c.w, kF4FewPieces), kh, hh, lane, M, den, acc);
     store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, c.x, (c.y + kh) * g + hh, lane, true, M, den,
-                 acc);
+                 acc, kF4Shift);
   }
 #pragma unroll 1
   for (int r = blockIdx.x; r < cuts[1] * per; r += gridDim.x) {
@@ -825,7 +832,7 @@ __global__ void __launch_bounds__(kF4JoinThreads, 5) pda_fp4_join_kernel(const F
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int v = 0; v < kF4JoinWarps; ++v) lse_fold(M, den, acc, part_ml[v][0], part_ml[v][1], part_o[v][lane]);
       store_merged(p.out, p.sinks, p.out_fp8, p.out_scale, p.v_scale, p.num_heads, c.x, (c.y + kh) * g + hh, lane, true, M,
-                   den, acc);
+                   den, acc, kF4Shift);
     }
     __syncthreads();
   }

@@ -260,11 +260,12 @@ __device__ __forceinline__ void store_out(void* out, size_t idx, float x, int ou
 }
 
 // Store lane's 4 dims of the merged row (s, h): zeros when no split held a
-// page (any == false).
+// page (any == false). den and acc may be held in units of 2^-unit, which the sink
+// takes too.
 __device__ __forceinline__ void store_merged(void* out, const float* sinks, int out_fp8, float out_scale,
                                              float v_scale, int num_heads, int s, int h, int lane, bool any, float M,
-                                             float den, const float4& acc) {
-  const float zs = sinks ? __ldg(sinks + h) * 1.4426950408889634f : -INFINITY;
+                                             float den, const float4& acc, float unit = 0.f) {
+  const float zs = sinks ? __ldg(sinks + h) * 1.4426950408889634f + unit : -INFINITY;
   const float r[4] = {acc.x, acc.y, acc.z, acc.w};
   const size_t o0 = ((size_t)s * num_heads + h) * kHeadDim + 4 * lane;
 #pragma unroll
