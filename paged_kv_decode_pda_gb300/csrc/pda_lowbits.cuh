@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_
     }
   };
   uint32_t w[4][4], next[4][4];
-  int h = blockIdx.y * (kWriteTileThreads / 32) + warp;
+  const int h = blockIdx.y * (kWriteTileThreads / 32) + warp;   // the launch has a warp for every head
   if (h < Hk) load(w, h, 0);   // on their way while the slots are sorted out
   if (warp == 0) {
     const long long slot = lane < 16 && t0 + lane < p.num_tokens ? write_slot(p, t0 + lane, blockIdx.y == 0) : -1;
@@ -364,80 +364,77 @@ __global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_
   const size_t page = (size_t)(128 * bs);
   uint8_t(*kt)[128] = tile[warp][0];
   uint8_t(*vt)[128] = tile[warp][1];
-  for (; h < Hk; h += gridDim.y * (kWriteTileThreads / 32)) {
+  if (h >= Hk) return;
 #pragma unroll 1
-    for (int part = 0; part < 4; ++part) {
-      const bool is_v = part >= 2;
-      if (part < 3) load(next, h, part + 1);
-      else if (h + gridDim.y * (kWriteTileThreads / 32) < Hk) load(next, h + gridDim.y * (kWriteTileThreads / 32), 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * (part & 1) + 2 * i + half;
-        const int2 at = rows[r];
-        const RowScale scale = slot_scale(w[i], p.min_scale);
-        *reinterpret_cast<uint2*>(is_v ? &vt[r][8 * l] : &kt[r][key_at(r, l >> 1) + 8 * (l & 1)]) = e4m3_codes8(w[i], scale);
-        if (l == 0 && at.x >= 0) (is_v ? p.v_scales : p.k_scales)[((size_t)at.x * Hk + h) * bs + at.y] = scale.scale;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w[i][j] = next[i][j];
-      }
-    }
-    __syncwarp();
+  for (int part = 0; part < 4; ++part) {
+    const bool is_v = part >= 2;
+    if (part < 3) load(next, h, part + 1);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      // consecutive lanes: consecutive rows of one chunk
-      const int r = lane & 15, c = half + 2 * i;
+      const int r = 8 * (part & 1) + 2 * i + half;
       const int2 at = rows[r];
-      if (at.x >= 0)
-        *reinterpret_cast<uint4*>(p.k_cache + ((size_t)at.x * Hk + h) * page + (c * bs + at.y) * 16) =
-            *reinterpret_cast<const uint4*>(&kt[r][key_at(r, c)]);
-    }
-    for (int k = 0; k < num_groups; ++k) {
-      const SlotGroup gr = groups[k];
-      uint8_t* dst = p.v_cache + ((size_t)gr.block * Hk + h) * page + 4 * lane * bs + gr.part * 16;
-      if ((gr.mask & (gr.mask - 1u)) == 0u) {   // a token alone
-        const int s = __ffs((int)gr.mask) - 1;
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]);
+      const RowScale scale = slot_scale(w[i], p.min_scale);
+      *reinterpret_cast<uint2*>(is_v ? &vt[r][8 * l] : &kt[r][key_at(r, l >> 1) + 8 * (l & 1)]) = e4m3_codes8(w[i], scale);
+      if (l == 0 && at.x >= 0) (is_v ? p.v_scales : p.k_scales)[((size_t)at.x * Hk + h) * bs + at.y] = scale.scale;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i * bs + s] = (uint8_t)(c >> (8 * i));
-        continue;
+      for (int j = 0; j < 4; ++j) w[i][j] = next[i][j];
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    // consecutive lanes: consecutive rows of one chunk
+    const int r = lane & 15, c = half + 2 * i;
+    const int2 at = rows[r];
+    if (at.x >= 0)
+      *reinterpret_cast<uint4*>(p.k_cache + ((size_t)at.x * Hk + h) * page + (c * bs + at.y) * 16) =
+          *reinterpret_cast<const uint4*>(&kt[r][key_at(r, c)]);
+  }
+  for (int k = 0; k < num_groups; ++k) {
+    const SlotGroup gr = groups[k];
+    uint8_t* dst = p.v_cache + ((size_t)gr.block * Hk + h) * page + 4 * lane * bs + gr.part * 16;
+    if ((gr.mask & (gr.mask - 1u)) == 0u) {   // a token alone
+      const int s = __ffs((int)gr.mask) - 1;
+      const uint32_t c = *reinterpret_cast<const uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i * bs + s] = (uint8_t)(c >> (8 * i));
+      continue;
+    }
+    uint32_t v[4][4];   // [dim][four slots]
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t in[4], out[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int s = 4 * q + i;
+        in[i] = gr.mask >> s & 1u ? *reinterpret_cast<const uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]) : 0u;
       }
-      uint32_t v[4][4];   // [dim][four slots]
+      turn4(in, out);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i][q] = out[i];
+    }
+    if (gr.mask == 0xFFFFu) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(dst + i * bs) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
+    } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t in[4], out[4];
+        const unsigned m = gr.mask >> (4 * q) & 15u;
+        if (m == 0u) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int s = 4 * q + i;
-          in[i] = gr.mask >> s & 1u ? *reinterpret_cast<const uint32_t*>(&vt[(int)(gr.map >> (4 * s)) & 15][4 * lane]) : 0u;
-        }
-        turn4(in, out);
+          uint8_t* d = dst + i * bs + 4 * q;
+          if (m == 15u) {
+            *reinterpret_cast<uint32_t*>(d) = v[i][q];
+          } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i][q] = out[i];
-      }
-      if (gr.mask == 0xFFFFu) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(dst + i * bs) = make_uint4(v[i][0], v[i][1], v[i][2], v[i][3]);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const unsigned m = gr.mask >> (4 * q) & 15u;
-          if (m == 0u) continue;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint8_t* d = dst + i * bs + 4 * q;
-            if (m == 15u) {
-              *reinterpret_cast<uint32_t*>(d) = v[i][q];
-            } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (m >> j & 1u) d[j] = (uint8_t)(v[i][q] >> (8 * j));
-            }
+            for (int j = 0; j < 4; ++j)
+              if (m >> j & 1u) d[j] = (uint8_t)(v[i][q] >> (8 * j));
           }
         }
       }
     }
-    __syncwarp();   // the tile is read
   }
 }
 

@@ -560,3 +560,10 @@ def test_inputs_of_another_stream(captured):
     held = cache.cpu()[t // bs][:, :, :].gather(2, table[0][t % bs][:, None].expand(-1, Hk, -1)) >> (torch.arange(128) % 2 * 4) & 15
     assert torch.equal(held.to(torch.uint8), codes)
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("T,Hk,bs,kind,layout", [(130, 37, 16, "run", "plain"), (70, 66, 32, "scattered", "heads_first"),
+                                                 (4200, 1, 16, "blocks", "odd"), (33, 130, 128, "run", "packed")])
+def test_write_heads_that_do_not_fill_a_block(T, Hk, bs, kind, layout):
+    """The tiled writer where its last warps have no head."""
+    test_write_slot_scales(T, Hk, bs, kind, layout, MIN)
