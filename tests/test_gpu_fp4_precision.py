@@ -26,3 +26,16 @@ def test_small_weights(H, Hk, bs, with_sinks):
     err = (got - want).abs()
     assert (err <= tol).all(), (int((err > tol).sum()), float((err / tol).max()))
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("lens,H,Hk,bs,window", F.MARKED)
+def test_every_page_counts(lens, H, Hk, bs, window):
+    """Long units over many CTAs, up to all of them: equal weights over distinct pages, each seen in a dim of its own set."""
+    c = F.MarkedPages(lens, H, Hk, bs, seed=len(lens) + bs)
+    dev = c.q.to(DEV), c.cache.to(DEV), c.tables.to(DEV), i32(lens)
+    for _ in range(3):
+        got = pda.decode_fp4(*dev, 0.1, 1.0, c.vs, window=window).double().cpu()
+        for i in range(len(lens)):
+            want = c.plain(i, window).repeat_interleave(H // Hk, 0)
+            assert c.agrees(got[i], want).all(), (i, torch.nonzero(~c.agrees(got[i], want))[:5].tolist())
+    assert pda.query_device_status() == 0
