@@ -39,3 +39,30 @@ def test_every_page_counts(lens, H, Hk, bs, window):
             want = c.plain(i, window).repeat_interleave(H // Hk, 0)
             assert c.agrees(got[i], want).all(), (i, torch.nonzero(~c.agrees(got[i], want))[:5].tolist())
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("S,most,long", [(6000, 20, 5000), (65535, 3, 3000), (12345, 1, 0)])
+def test_thousands_of_sequences(S, most, long):
+    """More sequences than the CTAs' threads count one by one; some empty, a long one near the end."""
+    H, Hk, bs = 2, 1, 16
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(0, most + 1, (S,), generator=g)
+    lens[-1] = most
+    if long:
+        lens[S - 37] = long
+    tables, NB = F.shuffled_tables(lens.tolist(), bs, g, extra=0)
+    cache = F.U.random_cache4(NB, Hk, bs, 1.0, g, wild=True)
+    # group scales of 2^-3 to 1, so that the logits of a sequence lie within reach of one another
+    cache[..., 128 * bs:] = torch.randint(0x20, 0x38, cache[..., 128 * bs:].shape, generator=g, dtype=torch.uint8)
+    q = torch.randn(S, H, 128, generator=g).to(torch.bfloat16)
+    scale, ks, vs = 0.125, 0.25, 0.5
+    got = pda.decode_fp4(q.to(DEV), cache.to(DEV), tables.to(DEV), i32(lens), scale, ks, vs).double().cpu()
+    want, mean, top = F.decode_by_length(q, cache, tables, lens, bs, scale, ks, vs)
+    # f16 weights 2^-11; logits: 128 products in binary32, 2^-16 of scale ks sum |q k|, twice (numerator and sum), with
+    # |k| < 6 and sum |q| < 160, so 2^-10; sums of 5000 / 16 steps 2^-13; small weights; the output
+    assert float(q.double().abs().sum(-1).max()) < 160
+    tol = mean * (2.0 ** -11 + 2.0 ** -9) + top * 2.0 ** -32 + want.abs() * 2.0 ** -8
+    err = (got - want).abs()
+    assert (err <= tol).all(), (int((err > tol).sum()), float((err / tol.clamp(min=1e-30)).max()))
+    assert (got[lens == 0] == 0).all()
+    assert pda.query_device_status() == 0
