@@ -66,3 +66,49 @@ def test_thousands_of_sequences(S, most, long):
     assert (err <= tol).all(), (int((err > tol).sum()), float((err / tol.clamp(min=1e-30)).max()))
     assert (got[lens == 0] == 0).all()
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("size", [0, 4, 8, 12, 16, 18])
+@pytest.mark.parametrize("lens,H,Hk,bs,alone", [([64, 33, 7, 0], 8, 4, 16, True), ([300, 5], 8, 2, 128, False), ([5000], 16, 2, 16, False),
+                                                ([2500, 40], 12, 4, 32, False)])
+def test_logits_of_any_size(size, lens, H, Hk, bs, alone):
+    """Logits of about 2^size that differ by 12 at most, all exact in binary32, so that nothing but the weights is rounded. Where one
+    warp sees a whole head (`alone`) that holds at every size; where parts are merged, their references round too, and
+    weights are as precise as the calls promise (size * 2^-22)."""
+    g = torch.Generator().manual_seed(size + bs)
+    tables, NB = F.shuffled_tables(lens, bs, g, extra=0)
+    cache = torch.zeros(NB, Hk, 144 * bs, dtype=torch.uint8)
+    grid = torch.from_numpy(F.U.E2M1)
+    scale, ks, vs = 0.5, 0.25, 0.5
+    q = torch.zeros(len(lens), H, 128, dtype=torch.bfloat16)
+    q[..., 0] = 2.0 ** (size - 7)
+    q[..., 16:32] = 1.0
+    key, val = [], []
+    for i, n in enumerate(lens):
+        pos = torch.arange(n)
+        slots = tables[i, pos // bs].long() * bs + pos % bs
+        k = torch.zeros(n, Hk, 128, dtype=torch.float64)
+        k[..., 0] = 4
+        k[..., 16:32] = grid[torch.randint(0, 8, (n, Hk, 16), generator=g)] * (1 - 2 * torch.randint(0, 2, (n, Hk, 16), generator=g))
+        s = torch.ones(n, Hk, 8, dtype=torch.float64)
+        s[..., 0] = 256
+        F.write_rows(cache, bs, 0, slots, k, s)
+        v = grid[torch.randint(0, 8, (n, Hk, 128), generator=g)] * (1 - 2 * torch.randint(0, 2, (n, Hk, 128), generator=g))
+        F.write_rows(cache, bs, 1, slots, v, torch.ones(n, Hk, 8))
+        key.append(k[..., 16:32].sum(-1) * scale * ks)              # the rest is the same for every token
+        val.append(v * vs)
+    got = pda.decode_fp4(q.to(DEV), cache.to(DEV), tables.to(DEV), i32(lens), scale, ks, vs).double().cpu()
+    # the weights' f16 (2^-11), the exponents' products of up to 40 in binary32 and the exponential (2^-17 together), sums of up
+    # to 5000 / 16 steps (2^-13); the promised precision, in numerator and sum
+    part = 2.0 ** -11 + 2.0 ** -12 + (0 if alone else 2 * 2.0 ** (size - 22))
+    for i, n in enumerate(lens):
+        for h in range(H):
+            if n == 0:
+                assert (got[i, h] == 0).all()
+                continue
+            w = torch.softmax(key[i][:, h // (H // Hk)], 0)
+            v = val[i][:, h // (H // Hk)]
+            want = w @ v
+            tol = (w @ v.abs()) * part + 2.0 ** -32 * n * 3 + want.abs() * 2.0 ** -8
+            assert ((got[i, h] - want).abs() <= tol).all(), (i, h, float(((got[i, h] - want).abs() / tol).max()))
+    assert pda.query_device_status() == 0
