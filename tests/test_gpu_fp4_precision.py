@@ -112,3 +112,22 @@ def test_logits_of_any_size(size, lens, H, Hk, bs, alone):
             tol = (w @ v.abs()) * part + 2.0 ** -32 * n * 3 + want.abs() * 2.0 ** -8
             assert ((got[i, h] - want).abs() <= tol).all(), (i, h, float(((got[i, h] - want).abs() / tol).max()))
     assert pda.query_device_status() == 0
+
+
+@pytest.mark.parametrize("H,Hk,bs,lens,window,with_sinks", [(32, 8, 16, [3, 0, 700, 64], 0, False), (6, 2, 32, [1, 129, 2000], 0, True),
+                                                            (8, 1, 128, [5, 3000], 100, False), (21, 3, 48, [47, 600, 0], 333, True),
+                                                            (4, 4, 16, [30, 30], 0, True)])
+def test_e4m3_output_of_every_path(H, Hk, bs, lens, window, with_sinks):
+    """e4m3 rows written by one warp, merged in a CTA, and joined."""
+    from tests.test_gpu_decode_fp4 import KS, VS, Batch
+    b = Batch(lens, H, Hk, bs, seed=H + bs)
+    kw = dict(window=window, sinks=torch.randn(H, generator=torch.Generator().manual_seed(7)) if with_sinks else None)
+    s = 0.003
+    got = b.run(output_scale=s, **kw).cpu()
+    assert got.dtype == torch.float8_e4m3fn
+    want, tol = F.U.decode64(b.q, b.cache, b.tables, b.lens, bs, b.scale, KS, VS, **kw)
+    want, far = want / s, tol / s
+    # the e4m3 rounding is monotonic: half a step (2^-4, 2^-10 below its normals) of what the kernel rounds
+    limit = far + (want.abs() + far) * 2.0 ** -4 + 2.0 ** -10
+    assert ((got.double() - want.clamp(-448, 448)).abs() <= limit).all()
+    assert pda.query_device_status() == 0
