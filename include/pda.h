@@ -741,7 +741,7 @@ pda_status pda_gather_cache_fp4(void* k_out, void* v_out, const void* kv_cache, 
  * result may differ in the last bits from batch to batch; the same call gives the
  * same bits. num_seqs * max_num_blocks_per_seq < 2^31.
  *
- * Needs a workspace per (device, stream), of one size (17 MB): made by the
+ * Needs a workspace per (device, stream), of one size (19 MB): made by the
  * first call, or by pda_reserve_fp4, which a stream needs before its first
  * capture (else PDA_ERR_WORKSPACE), and freed by pda_release. Graphs that
  * captured calls of one stream share it and must not run at the same time.

@@ -2039,9 +2039,9 @@ __global__ void __launch_bounds__(kHeadDim) pda_merge_wide_kernel(const MergePar
 // launched as this grid's dependent. A unit of one piece was stored whole
 // by the decode kernel. The decode kernel lets this grid launch only after
 // its CTAs have waited for the order kernel, so tail_info can be read
-// before waiting for the decode grid; with one split, rows with nothing to
-// fold leave at once (with several, every row waits, so that this grid
-// ends after the decode grid and the merge kernel after both).
+// before waiting for the decode grid. Every warp waits for the decode grid,
+// also one with nothing to fold: this grid ends after it, and what is
+// launched behind this grid runs after both.
 struct TailMergeParams {
   MergeParams m;         // out, sinks, output format, v_scale, num_heads, nsplit
   float* part_o;         // several splits: the split partials the merge kernel folds
@@ -2065,8 +2065,8 @@ __global__ void __launch_bounds__(kHeadDim) pda_tail_merge_kernel(const TailMerg
   const int j = row / p.gqa;
   const int hh = row % p.gqa;
   const int4 e = __ldcg(p.tail_info + j);
-  // The decode kernel's pieces are stored and visible. Every warp waits, also one without
-  // pieces: a programmatic launch behind this kernel waits for this kernel alone.
+  // The decode kernel's pieces are stored and visible. (A programmatic launch behind this
+  // kernel waits for this kernel alone.)
   grid_dependency_wait();
   if (e.z <= 1) return;
   const int s = e.x / (p.num_kv_heads * nsplit);
