@@ -321,9 +321,10 @@ __device__ __forceinline__ int key_at(int r, int c) { return 16 * (c ^ (r & 7));
 // Tiles of 16 tokens, a warp per kv head: the rows' codes pass through shared memory,
 // K to go out 16 bytes (a chunk of a row) at a time, V by groups of 16 slots, turned
 // in registers: 16-byte rows of whole groups, and what a group holds of the tile
-// where it is cut or scattered. Bound by instructions, the exact roundings first (ALU
-// 50 %, issue 58 % of a single wave of CTAs): 8192 tokens of 8 heads in 64-token blocks
-// 15.8 us, 3.2 TB/s. (Keys and values to warps of their own, twice the CTAs: 16.8
+// where it is cut or scattered. 8192 tokens of 8 heads in whole blocks 15.3 us, 3.3 TB/s:
+// one partly filled wave of CTAs (6.7 an SM, a third of the warps) bounds it, neither
+// bytes (24 % of DRAM) nor instructions (issue 58 %, ALU 50 %) alone. Prompts of odd
+// lengths, whose tiles lie across two groups of slots, 31 us, scattered slots 73. (Keys and values to warps of their own, twice the CTAs: 16.8
 // against 16.4.)
 constexpr int kWriteTileThreads = 128;
 template <bool kVec>

@@ -168,7 +168,8 @@ pda_status pda_reshape_and_cache_slot_scales(const pda_token_rows* key, const pd
   // Few rows: a warp each, whatever the slots. More: tiles of 16 tokens, whose V codes
   // go out by groups of slots (us with a warp a row / tiles, 8 kv heads: 256 tokens in
   // whole blocks 6.3 / 7.2, scattered 5.5 / 15.7; 512 9.8 / 7.3, 8.2 / 16.2; 1024 16.3 /
-  // 7.2, 12.5 / 18.6; 8192 82.7 / 16.2, 75.5 / 74.2).
+  // 7.2, 12.5 / 18.6; 8192 82.7 / 16.2, 75.5 / 74.2). The number of rows alone decides, as
+  // the host does not see the slots: scattered calls from 513 tokens on lose by it.
   const long long items = (long long)num_tokens * num_kv_heads;
   bool done;
   if (items <= kSlotScalesMaxRows) {
@@ -323,7 +324,8 @@ pda_status pda_decode_fp4(void* out, const void* q, const void* kv_cache, const 
     // (us with 4 / 2 tiles a warp, 32/8 heads: 16 x 1024 tokens 16.3 / 15.0, 32 x 1024
     // 20.9 / 19.1, 64 x 1024 25.2 / 25.3, 128 x 1 to 2048 43.7 / 48.8). But not where a
     // large chunk holds a whole sequence, so that nothing is to be joined (64 x 50 tokens
-    // 9.2 / 11.0).
+    // 10.0, and 11.8 with the join). All this goes by the table's width, as the host does not
+    // see the lengths: with 8192 entries a row 16 x 1024 take 17.0, 64 x 50 11.8.
     if (most < 4ll * ctas) {
       const int whole = per;
       tiles = 2;
