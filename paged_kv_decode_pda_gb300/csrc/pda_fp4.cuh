@@ -13,10 +13,10 @@
 // or one where pages are larger or the heads do not divide, a head's tokens then
 // shared by two or four warps, whose rows are merged in shared memory (256 x 4096 tokens
 // of 8/2 heads 62 us for a floor of 45, of 8/1 heads 40 for 22). A unit's tokens go in
-// chunks of whole pages, 256 / heads tokens at most. All units' chunks, one after the other, are cut into runs
-// wherever the cuts fall, one per resident CTA, so that every batch (a few long
-// sequences, many ragged ones) loads all SMs alike. The pieces (O, m, l) of a unit
-// that a cut divides go to the workspace, and a second kernel joins them.
+// chunks of whole pages, 256 / heads tokens at most. All units' chunks, one after the
+// other, are cut into runs wherever the cuts fall, one per resident CTA, so that every
+// batch (a few long sequences, many ragged ones) loads all SMs alike. The pieces (O, m,
+// l) of a unit that a cut divides go to the workspace, and a second kernel joins them.
 // (Smaller runs for the last quarter, taken from a queue as CTAs come free: all CTAs
 // end within 4 % of each other, not 20 %, and the pieces this adds cost as much, 219
 // against 222 us at 256 x 4096 tokens of 32/8 heads, 120 against 119 at 256 x 1 to

@@ -324,8 +324,8 @@ __device__ __forceinline__ int key_at(int r, int c) { return 16 * (c ^ (r & 7));
 // where it is cut or scattered. 8192 tokens of 8 heads in whole blocks 15.3 us, 3.3 TB/s:
 // one partly filled wave of CTAs (6.7 an SM, a third of the warps) bounds it, neither
 // bytes (24 % of DRAM) nor instructions (issue 54 %, ALU 52 %) alone. Prompts of odd
-// lengths, whose tiles lie across two groups of slots, 31 us, scattered slots 73. (Keys and values to warps of their own, twice the CTAs: 16.8
-// against 16.4.)
+// lengths, whose tiles lie across two groups of slots, 31 us, scattered slots 73. (Keys
+// and values to warps of their own, twice the CTAs: 16.8 against 16.4.)
 constexpr int kWriteTileThreads = 128;
 template <bool kVec>
 __global__ void __launch_bounds__(kWriteTileThreads) pda_write_slot_scales_tile_kernel(const LowbitsWriteParams p) {
